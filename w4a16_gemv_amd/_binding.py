@@ -1,4 +1,6 @@
-"""ctypes binding of libnf4 (include/nf4.h, include/int4.h).
+"""ctypes binding of libnf4 (include/nf4.h, include/int4.h, include/int8.h,
+include/moe.h; the classes and functions of the last two are in _int8.py and
+_moe.py).
 
 Argument marshalling only: every step of the dequant and GEMV runs in the HIP
 kernels of libnf4.so.  Tensors must live on an AMD GPU; there is no CPU
@@ -26,7 +28,12 @@ EXPORTED = ("nf4_abi_version", "nf4_status_string", "nf4_dequant", "nf4_gemv", "
             "nf4_gemv_sched_size", "nf4_gemv_grouped_noalloc", "nf4_gemv_desc_check",
             "nf4_code2_linear", "nf4_quantize_workspace_size",
             "nf4_quantize", "nf4_quantize_absmax32", "int4_dequant", "int4_gemv",
-            "int4_quantize")
+            "int4_quantize",
+            "int8_pitch", "int8_quantize", "int8_dequant", "int8_gemm",
+            "int8_gemm_workspace_size", "int8_linear", "int8_linear_workspace_size",
+            "int8_gemm_grouped",
+            "moe_sort", "moe_sort_workspace_size", "moe_gather", "moe_combine",
+            "moe_combine_grad")
 
 _lib = None
 
@@ -93,6 +100,33 @@ def load() -> C.CDLL:
     lib.int4_gemv.argtypes = [p, p, p, i64, i64, i32, p, i32, p, p]
     lib.int4_quantize.restype = C.c_int
     lib.int4_quantize.argtypes = [p, i64, i32, p, p, p, p]
+    size = C.c_size_t
+    lib.int8_pitch.restype = i64
+    lib.int8_pitch.argtypes = [i64]
+    lib.int8_quantize.restype = C.c_int
+    lib.int8_quantize.argtypes = [p, i32, i64, i64, p, p, p]
+    lib.int8_dequant.restype = C.c_int
+    lib.int8_dequant.argtypes = [p, p, i64, i64, p, i32, p]
+    lib.int8_gemm.restype = C.c_int
+    lib.int8_gemm.argtypes = [p, p, p, p, i64, i64, i64, p, i32, p, size, p]
+    lib.int8_gemm_workspace_size.restype = size
+    lib.int8_gemm_workspace_size.argtypes = [i64, i64, i64]
+    lib.int8_linear.restype = C.c_int
+    lib.int8_linear.argtypes = [p, i32, p, p, i64, i64, i64, p, i32, p, size, p]
+    lib.int8_linear_workspace_size.restype = size
+    lib.int8_linear_workspace_size.argtypes = [i64, i64, i64]
+    lib.int8_gemm_grouped.restype = C.c_int
+    lib.int8_gemm_grouped.argtypes = [p, p, i64, p, i32, p, p, p, i32, i64, i64, i64, p, i32, p]
+    lib.moe_sort.restype = C.c_int
+    lib.moe_sort.argtypes = [p, i32, i64, i32, i32, p, p, p, p, size, p]
+    lib.moe_sort_workspace_size.restype = size
+    lib.moe_sort_workspace_size.argtypes = [i64, i32, i32]
+    lib.moe_gather.restype = C.c_int
+    lib.moe_gather.argtypes = [p, i32, p, i64, i32, i64, i64, p, p]
+    lib.moe_combine.restype = C.c_int
+    lib.moe_combine.argtypes = [p, i32, p, p, i64, i32, i64, i64, p, p]
+    lib.moe_combine_grad.restype = C.c_int
+    lib.moe_combine_grad.argtypes = [p, p, i32, p, p, i64, i32, i64, i64, p, p, p]
     _lib = lib
     return lib
 

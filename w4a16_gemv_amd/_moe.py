@@ -1,0 +1,167 @@
+"""Routing around expert products (include/moe.h): slots sorted by expert, rows
+moved into that order and back with the router's weights, and the gradients.
+
+Argument marshalling only, as in _binding.py; work goes on torch's current
+stream of the tensors' device, whichever device is current.  Nothing here is
+recorded by autograd: a program that trains calls moe_combine_grad and
+moe_gather_grad in its backward pass, and tensors that require a gradient are
+refused while gradients are being recorded.
+"""
+from __future__ import annotations
+
+import torch
+
+from ._binding import _dev, _F32
+from ._int8 import _row_dtype, _run, _same_device, _scratch, _size
+
+_I32 = (torch.int32,)
+
+
+class MoeRoute:
+    """Where the slots of a batch went (moe_sort): T tokens with top_k slots
+    each, over `experts` experts.
+
+    offsets: int32 [experts + 1], expert e has the sorted rows [offsets[e],
+    offsets[e + 1]); order: int32 [T * top_k], the flat slot t * top_k + j of
+    each sorted row, -1 behind the last expert's; pos: int32 [T][top_k], the
+    sorted row of each slot, -1 for a dropped one."""
+
+    def __init__(self, offsets: torch.Tensor, order: torch.Tensor, pos: torch.Tensor):
+        if pos.dim() != 2 or pos.shape[1] < 1:
+            raise ValueError(f"pos must be [T, top_k], got shape {tuple(pos.shape)}")
+        _dev(pos, "pos", _I32, 0)
+        _dev(order, "order", _I32, 0)
+        _dev(offsets, "offsets", _I32, 1)
+        if order.numel() != pos.numel():
+            raise ValueError(f"order has {order.numel()} elements, pos {pos.numel()}")
+        _same_device(pos.device, offsets=offsets, order=order)
+        self.offsets, self.order, self.pos = offsets, order, pos
+
+    @property
+    def T(self) -> int:
+        return self.pos.shape[0]
+
+    @property
+    def top_k(self) -> int:
+        return self.pos.shape[1]
+
+    @property
+    def rows(self) -> int:
+        """Rows of a buffer in sorted order: one for each slot, dropped or not."""
+        return self.order.numel()
+
+    @property
+    def experts(self) -> int:
+        return self.offsets.numel() - 1
+
+
+def moe_sort(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = None) -> MoeRoute:
+    """Sort the slots of ids (int32 or int64 [T][top_k]) by expert, stable.
+    Ids outside [0, experts) are dropped slots.  workspace: a uint8 tensor of
+    moe_sort_workspace_size bytes, or None for one from torch's allocator."""
+    if ids.dim() != 2 or ids.shape[1] < 1:
+        raise ValueError(f"ids must be [T, top_k], got shape {tuple(ids.shape)}")
+    T, top_k = ids.shape
+    experts = int(experts)
+    if experts < 0:
+        raise ValueError(f"experts must not be negative, got {experts}")
+    pi = _dev(ids, "ids", (torch.int32, torch.int64), 0)
+    dev = ids.device
+    route = MoeRoute.__new__(MoeRoute)
+    route.offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+    route.order = torch.empty(T * top_k, dtype=torch.int32, device=dev)
+    route.pos = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    pw, nbytes, _keep = _scratch(workspace, _size("moe_sort_workspace_size", dev, T, top_k, experts)
+                                 if workspace is None else 0, dev)
+    _run("moe_sort", dev, pi, ids.element_size(), T, top_k, experts, route.offsets.data_ptr(),
+         route.order.data_ptr(), route.pos.data_ptr(), pw, nbytes)
+    return route
+
+
+def _no_grad(fn: str, **tensors) -> None:
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{fn}: {name} requires a gradient, which autograd would not see; "
+                                 "call it under torch.no_grad() or in a Function, and its gradient "
+                                 "function in the backward pass")
+
+
+def _rows(t: torch.Tensor, name: str, shape, dev, dtype=None) -> int:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
+    _same_device(dev, **{name: t})
+    return _dev(t, name, (t.dtype if dtype is None else dtype,), 0)
+
+
+def _weights(weights, route: MoeRoute, dev):
+    if weights is None:
+        return None
+    _rows(weights, "weights", route.pos.shape, dev)
+    return _dev(weights, "weights", _F32, 0)
+
+
+def moe_gather(x: torch.Tensor, route: MoeRoute, out: torch.Tensor | None = None) -> torch.Tensor:
+    """x's rows ([T][H]: bf16, fp16 or fp32) in sorted order, [route.rows][H];
+    rows that no slot has are left as they were (undefined where out is None)."""
+    _no_grad("moe_gather", x=x, out=out)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [T, H], got shape {tuple(x.shape)}")
+    dev, H = x.device, x.shape[1]
+    code = _row_dtype(x.dtype, "x")
+    px = _rows(x, "x", (route.T, H), dev)
+    _same_device(dev, route=route.pos)
+    if out is None:
+        out = torch.empty((route.rows, H), dtype=x.dtype, device=dev)
+    po = _rows(out, "out", (route.rows, H), dev, x.dtype)
+    _run("moe_gather", dev, px, code, route.pos.data_ptr(), route.T, route.top_k, route.rows, H, po)
+    return out
+
+
+def moe_combine(ys: torch.Tensor, route: MoeRoute, weights: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = sum_j weights[t][j] ys[pos[t][j]] ([T][H]) over the slots of each
+    token that have a row; weights: fp32 [T][top_k], or None for ones."""
+    _no_grad("moe_combine", ys=ys, weights=weights, out=out)
+    if ys.dim() != 2:
+        raise ValueError(f"ys must be [rows, H], got shape {tuple(ys.shape)}")
+    dev, H = ys.device, ys.shape[1]
+    code = _row_dtype(ys.dtype, "ys")
+    ps = _rows(ys, "ys", (route.rows, H), dev)
+    _same_device(dev, route=route.pos)
+    pw = _weights(weights, route, dev)
+    if out is None:
+        out = torch.empty((route.T, H), dtype=ys.dtype, device=dev)
+    po = _rows(out, "out", (route.T, H), dev, ys.dtype)
+    _run("moe_combine", dev, ps, code, pw, route.pos.data_ptr(), route.T, route.top_k, route.rows,
+         H, po)
+    return out
+
+
+def moe_gather_grad(dxs: torch.Tensor, route: MoeRoute,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of moe_gather: dx[t] = sum_j dxs[pos[t][j]]."""
+    return moe_combine(dxs, route, None, out)
+
+
+def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, route: MoeRoute,
+                     weights: torch.Tensor | None = None, dys: torch.Tensor | None = None):
+    """The gradients (dys [route.rows][H], dweights fp32 [T][top_k]) of
+    moe_combine, given dy [T][H] and its inputs.  Rows of dys that no slot has
+    are left as they were (undefined where dys is None)."""
+    _no_grad("moe_combine_grad", dy=dy, ys=ys, weights=weights, dys=dys)
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be [T, H], got shape {tuple(dy.shape)}")
+    dev, H = dy.device, dy.shape[1]
+    code = _row_dtype(dy.dtype, "dy")
+    pg = _rows(dy, "dy", (route.T, H), dev)
+    ps = _rows(ys, "ys", (route.rows, H), dev, dy.dtype)
+    _same_device(dev, route=route.pos)
+    pw = _weights(weights, route, dev)
+    if dys is None:
+        dys = torch.empty((route.rows, H), dtype=dy.dtype, device=dev)
+    po = _rows(dys, "dys", (route.rows, H), dev, dy.dtype)
+    dweights = torch.empty((route.T, route.top_k), dtype=torch.float32, device=dev)
+    _run("moe_combine_grad", dev, pg, ps, code, pw, route.pos.data_ptr(), route.T, route.top_k,
+         route.rows, H, po, dweights.data_ptr())
+    return dys, dweights

@@ -1,0 +1,416 @@
+// moe.hip -- routing around expert products: slots sorted by expert, rows moved
+// into that order and back with the router's weights, and the gradients.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "int8_product.h"
+#include "moe.h"
+#include "nf4_device.h"
+#include "row_io.h"
+
+namespace {
+
+using namespace nf4dev;
+using namespace rowio;
+
+// ---------------------------------------------------------------------------
+// Sort.  A stable counting sort: the row of a slot is the number of slots with
+// a smaller expert, plus those of its expert before it.  A workgroup of 16
+// waves takes a tile of 4096 slots, wave w the 256 from 256 w on, 64 at a time:
+// the lanes of a wave find those with their own expert by one ballot per bit
+// of the id, which gives the rank among the 64; counters per wave and expert
+// in LDS carry it on.  After the tile, a sum over the waves and one over the
+// experts turn the counters into rows.
+//
+// Up to one tile one workgroup does it all in one launch.  Beyond, a first
+// kernel writes each workgroup's counts per expert to the workspace and a
+// second one adds those of the workgroups before it to its own.
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kSortSteps = 4;
+constexpr int kSortTile = kSortThreads * kSortSteps;
+constexpr int kMaxSortGroups = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int64_t kMaxSlots = int64_t(1) << 30;
+
+struct SortShared {
+  uint16_t count[kSortWaves][kMaxExperts];  // per wave and expert, later the rows before the wave's
+  uint32_t base[kMaxExperts];               // row of the expert's next slot
+  uint32_t wave_sum[kSortWaves];
+  uint32_t total;
+};
+
+__device__ __forceinline__ int slot_expert(const void* ids, int id_bytes, int64_t i, int64_t n,
+                                           int experts) {
+  if (i >= n) return -1;
+  const int64_t e = id_bytes == 8 ? static_cast<const int64_t*>(ids)[i]
+                                  : static_cast<const int32_t*>(ids)[i];
+  return e >= 0 && e < experts ? static_cast<int>(e) : -1;
+}
+
+// Ranks the tile's slots within (wave, expert) and leaves the counters in
+// s.count.
+__device__ __forceinline__ void rank_tile(SortShared& s, const int (&e)[kSortSteps],
+                                          int (&rank)[kSortSteps], int experts, int bits) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int i = lane; i < experts; i += 64) s.count[wave][i] = 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+  for (int t = 0; t < kSortSteps; ++t) {
+    uint64_t same = __ballot(e[t] >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t set = __ballot((e[t] >> b) & 1);
+      same &= (e[t] >> b) & 1 ? set : ~set;
+    }
+    rank[t] = 0;
+    int before = 0, mine = 0;
+    if (e[t] >= 0) {
+      before = s.count[wave][e[t]];
+      mine = __popcll(same & ((uint64_t(1) << lane) - 1));
+      rank[t] = before + mine;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (e[t] >= 0 && mine == 0) s.count[wave][e[t]] = static_cast<uint16_t>(before + __popcll(same));
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
+__device__ __forceinline__ uint32_t wave_inclusive(uint32_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = static_cast<uint32_t>(__shfl_up(static_cast<int>(v), d));
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Thread i < experts gives expert i's count; returns the sum of those before it
+// and leaves the sum of all in s.total.
+__device__ __forceinline__ uint32_t scan_experts(SortShared& s, uint32_t v) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint32_t in = wave_inclusive(v);
+  if (lane == 63) s.wave_sum[wave] = in;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    before += w < wave ? s.wave_sum[w] : 0u;
+    all += s.wave_sum[w];
+  }
+  if (threadIdx.x == 0) s.total = all;
+  __syncthreads();
+  return before + in - v;
+}
+
+// s.count[w][e] becomes the number of the tile's slots of expert e in the waves
+// before w; returns the tile's count of expert threadIdx.x.
+__device__ __forceinline__ uint32_t scan_waves(SortShared& s, int experts) {
+  uint32_t sum = 0;
+  const int e = threadIdx.x;
+  if (e < experts)
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = s.count[w][e];
+      s.count[w][e] = static_cast<uint16_t>(sum);
+      sum += c;
+    }
+  return sum;
+}
+
+struct SortArgs {
+  const void* ids;
+  int id_bytes;
+  int64_t n;
+  int experts, bits;
+  int32_t *offsets, *order, *pos;
+  uint32_t* counts;    // [groups][experts] of the workspace
+  int64_t per_group;   // slots of a workgroup, a multiple of the tile
+};
+
+__device__ __forceinline__ void load_tile(const SortArgs& a, int64_t tile, int (&e)[kSortSteps]) {
+  const int64_t first = tile + (threadIdx.x >> 6) * (64 * kSortSteps) + (threadIdx.x & 63);
+#pragma unroll
+  for (int t = 0; t < kSortSteps; ++t)
+    e[t] = slot_expert(a.ids, a.id_bytes, first + 64 * t, a.n, a.experts);
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
+  __shared__ uint32_t s_count[kMaxExperts];
+  for (int i = threadIdx.x; i < a.experts; i += kSortThreads) s_count[i] = 0;
+  __syncthreads();
+  const int64_t begin = a.per_group * blockIdx.x;
+  const int64_t end = min(a.n, begin + a.per_group);
+  for (int64_t i = begin + threadIdx.x; i < end; i += kSortThreads) {
+    const int e = slot_expert(a.ids, a.id_bytes, i, a.n, a.experts);
+    if (e >= 0) atomicAdd(&s_count[e], 1u);  // whole numbers: the order does not matter
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.experts; i += kSortThreads)
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.experts + i] = s_count[i];
+}
+
+// ONE: the only workgroup, of a single tile; its own counts are the totals.
+template <bool ONE>
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
+  __shared__ SortShared s;
+  int e[kSortSteps], rank[kSortSteps];
+  const int wave = threadIdx.x >> 6;
+  const int64_t begin = ONE ? 0 : a.per_group * blockIdx.x;
+  const int64_t end = ONE ? a.n : min(a.n, begin + a.per_group);
+  if constexpr (!ONE) {
+    uint32_t before = 0, all = 0;
+    if (static_cast<int>(threadIdx.x) < a.experts)
+      for (uint32_t g = 0; g < gridDim.x; ++g) {
+        const uint32_t c = a.counts[static_cast<int64_t>(g) * a.experts + threadIdx.x];
+        before += g < blockIdx.x ? c : 0u;
+        all += c;
+      }
+    const uint32_t row = scan_experts(s, all);
+    if (static_cast<int>(threadIdx.x) < a.experts) {
+      s.base[threadIdx.x] = row + before;
+      if (blockIdx.x == 0) a.offsets[threadIdx.x] = static_cast<int32_t>(row);
+    }
+  }
+  for (int64_t tile = begin; tile < end || (ONE && tile == 0); tile += kSortTile) {
+    load_tile(a, tile, e);
+    rank_tile(s, e, rank, a.experts, a.bits);
+    __syncthreads();
+    const uint32_t tile_count = scan_waves(s, a.experts);
+    if constexpr (ONE) {
+      const uint32_t row = scan_experts(s, tile_count);
+      if (static_cast<int>(threadIdx.x) < a.experts) {
+        s.base[threadIdx.x] = row;
+        a.offsets[threadIdx.x] = static_cast<int32_t>(row);
+      }
+    }
+    __syncthreads();
+    const int64_t first = tile + wave * (64 * kSortSteps) + (threadIdx.x & 63);
+#pragma unroll
+    for (int t = 0; t < kSortSteps; ++t) {
+      const int64_t i = first + 64 * t;
+      if (i >= a.n) continue;
+      int row = -1;
+      if (e[t] >= 0) {
+        row = static_cast<int>(s.base[e[t]] + s.count[wave][e[t]] + rank[t]);
+        a.order[row] = static_cast<int32_t>(i);
+      }
+      a.pos[i] = row;
+    }
+    __syncthreads();
+    if (!ONE && static_cast<int>(threadIdx.x) < a.experts) s.base[threadIdx.x] += tile_count;
+    __syncthreads();
+  }
+  const uint32_t total = s.total;
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.experts] = static_cast<int32_t>(total);
+  for (int64_t i = total + static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < a.n;
+       i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+    a.order[i] = -1;
+}
+
+// ---------------------------------------------------------------------------
+// Rows.  A workgroup per token (a grid may not have 2^32 threads, so beyond
+// kMaxRowGroups tokens a workgroup takes several).
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+constexpr int64_t kMaxRowGroups = 1 << 20;
+
+uint32_t row_groups(int64_t T) { return static_cast<uint32_t>(T < kMaxRowGroups ? T : kMaxRowGroups); }
+
+__device__ __forceinline__ bool has_row(int32_t p, int64_t rows) {
+  return p >= 0 && static_cast<int64_t>(p) < rows;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void gather_kernel(const void* __restrict__ x,
+                                                             const int32_t* __restrict__ pos,
+                                                             int64_t T, int top_k, int64_t rows,
+                                                             int64_t H, void* __restrict__ xs) {
+  const int64_t row_bytes = H * dtype_bytes(DT);
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  const char* xr = static_cast<const char*>(x) + t * row_bytes;
+  for (int64_t at = 8 * threadIdx.x; at < H; at += 8 * kRowThreads) {
+    const Piece<DT> p = load_piece<DT>(xr, at, H);
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t r = pos[t * top_k + j];
+      if (has_row(r, rows)) store_piece<DT>(static_cast<char*>(xs) + r * row_bytes, at, H, p);
+    }
+  }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(const void* __restrict__ ys,
+                                                              const float* __restrict__ weights,
+                                                              const int32_t* __restrict__ pos,
+                                                              int64_t T, int top_k, int64_t rows,
+                                                              int64_t H, void* __restrict__ y) {
+  const int64_t row_bytes = H * dtype_bytes(DT);
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
+  for (int64_t at = 8 * threadIdx.x; at < H; at += 8 * kRowThreads) {
+    float acc[8] = {};
+    for (int j = 0; j < top_k; ++j) {
+      const int32_t r = pos[t * top_k + j];
+      if (!has_row(r, rows)) continue;
+      const float w = weights ? weights[t * top_k + j] : 1.0f;
+      const Piece<DT> p = load_piece<DT>(static_cast<const char*>(ys) + r * row_bytes, at, H);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, element<DT>(p, i), acc[i]);
+    }
+    store_piece<DT>(static_cast<char*>(y) + t * row_bytes, at, H, make_piece<DT>(acc));
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(
+    const void* __restrict__ dy, const void* __restrict__ ys, const float* __restrict__ weights,
+    const int32_t* __restrict__ pos, int64_t T, int top_k, int64_t rows, int64_t H,
+    void* __restrict__ dys, float* __restrict__ dweights) {
+  __shared__ float s_sum[kRowThreads / 64];
+  const int64_t row_bytes = H * dtype_bytes(DT);
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  const char* dyr = static_cast<const char*>(dy) + t * row_bytes;
+  for (int j = 0; j < top_k; ++j) {
+    const int32_t r = pos[t * top_k + j];
+    const bool live = has_row(r, rows);
+    const float w = weights ? weights[t * top_k + j] : 1.0f;
+    float dot = 0.0f;
+    if (live)
+      for (int64_t at = 8 * threadIdx.x; at < H; at += 8 * kRowThreads) {
+        const Piece<DT> g = load_piece<DT>(dyr, at, H);
+        if (dweights) {
+          const Piece<DT> p = load_piece<DT>(static_cast<const char*>(ys) + r * row_bytes, at, H);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dot = fmaf(element<DT>(p, i), element<DT>(g, i), dot);
+        }
+        if (dys) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = w * element<DT>(g, i);
+          store_piece<DT>(static_cast<char*>(dys) + r * row_bytes, at, H, make_piece<DT>(f));
+        }
+      }
+    if (dweights) {
+      dot = wave_sum(dot);
+      if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        float sum = 0.0f;
+        for (int i = 0; i < kRowThreads / 64; ++i) sum += s_sum[i];
+        dweights[t * top_k + j] = live ? sum : 0.0f;
+      }
+      __syncthreads();
+    }
+  }
+  }
+}
+
+int64_t sort_groups(int64_t n, int64_t* per_group) {
+  const int64_t tiles = (n + kSortTile - 1) / kSortTile;
+  const int64_t per = (tiles + kMaxSortGroups - 1) / kMaxSortGroups;
+  *per_group = per * kSortTile;
+  return (tiles + per - 1) / per;
+}
+
+bool slots_fit(int64_t T, int32_t top_k) { return T <= kMaxSlots / top_k; }
+
+// What gather, combine and combine_grad check alike.
+nf4_status check_rows(int32_t dtype, const int32_t* pos, int64_t T, int32_t top_k, int64_t rows,
+                      int64_t H) {
+  if (T < 0 || top_k < 1 || rows < 0 || H < 0 || !known_dtype(dtype)) return NF4_EINVAL;
+  if (T > 0 && (!pos || !aligned(pos, 4))) return NF4_EINVAL;
+  if (!slots_fit(T, top_k) || rows > int8dev::kMaxDim || H > int8dev::kMaxDim)
+    return NF4_EUNSUPPORTED;
+  return NF4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_sort_workspace_size(int64_t T, int32_t top_k, int32_t experts) {
+  if (T <= 0 || top_k < 1 || experts < 1 || experts > kMaxExperts || !slots_fit(T, top_k)) return 0;
+  if (T * top_k <= kSortTile) return 0;
+  int64_t per = 0;
+  return static_cast<size_t>(sort_groups(T * top_k, &per)) * experts * sizeof(uint32_t);
+}
+
+nf4_status moe_sort(const void* ids, int32_t id_bytes, int64_t T, int32_t top_k, int32_t experts,
+                    int32_t* offsets, int32_t* order, int32_t* pos, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (T < 0 || top_k < 1 || experts < 0 || (id_bytes != 4 && id_bytes != 8)) return NF4_EINVAL;
+  if (!offsets || !aligned(offsets, 4)) return NF4_EINVAL;
+  if (T > 0 && (!ids || !order || !pos)) return NF4_EINVAL;
+  if (!aligned(ids, id_bytes) || !aligned(order, 4) || !aligned(pos, 4) || !aligned(workspace, 256))
+    return NF4_EINVAL;
+  if (experts > kMaxExperts || !slots_fit(T, top_k)) return NF4_EUNSUPPORTED;
+  const size_t need = moe_sort_workspace_size(T, top_k, experts);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return NF4_EINVAL;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  SortArgs a = {ids, id_bytes, T * top_k, experts, 0, offsets, order, pos, nullptr, 0};
+  while ((1 << a.bits) < experts) ++a.bits;
+  if (a.n <= kSortTile) {
+    hipLaunchKernelGGL((sort_place_kernel<true>), dim3(1), dim3(kSortThreads), 0, st, a);
+    return launch_status();
+  }
+  const uint32_t groups = static_cast<uint32_t>(sort_groups(a.n, &a.per_group));
+  a.counts = static_cast<uint32_t*>(workspace);
+  hipLaunchKernelGGL(sort_count_kernel, dim3(groups), dim3(kSortThreads), 0, st, a);
+  hipLaunchKernelGGL((sort_place_kernel<false>), dim3(groups), dim3(kSortThreads), 0, st, a);
+  return launch_status();
+}
+
+nf4_status moe_gather(const void* x, int32_t dtype, const int32_t* pos, int64_t T, int32_t top_k,
+                      int64_t rows, int64_t H, void* xs, void* stream) {
+  if (const nf4_status st = check_rows(dtype, pos, T, top_k, rows, H)) return st;
+  if (T == 0 || rows == 0 || H == 0) return NF4_OK;
+  if (!x || !xs || !aligned(x, dtype_bytes(dtype)) || !aligned(xs, dtype_bytes(dtype)))
+    return NF4_EINVAL;
+  with_dtype(dtype, [&](auto d) {
+    hipLaunchKernelGGL((gather_kernel<decltype(d)::value>), dim3(row_groups(T)),
+                       dim3(kRowThreads), 0, reinterpret_cast<hipStream_t>(stream), x, pos, T,
+                       top_k, rows, H, xs);
+  });
+  return launch_status();
+}
+
+nf4_status moe_combine(const void* ys, int32_t dtype, const float* weights, const int32_t* pos,
+                       int64_t T, int32_t top_k, int64_t rows, int64_t H, void* y, void* stream) {
+  if (const nf4_status st = check_rows(dtype, pos, T, top_k, rows, H)) return st;
+  if (T == 0 || H == 0) return NF4_OK;
+  if ((rows > 0 && !ys) || !y || !aligned(ys, dtype_bytes(dtype)) ||
+      !aligned(y, dtype_bytes(dtype)) || !aligned(weights, 4))
+    return NF4_EINVAL;
+  with_dtype(dtype, [&](auto d) {
+    hipLaunchKernelGGL((combine_kernel<decltype(d)::value>), dim3(row_groups(T)),
+                       dim3(kRowThreads), 0, reinterpret_cast<hipStream_t>(stream), ys, weights, pos,
+                       T, top_k, rows, H, y);
+  });
+  return launch_status();
+}
+
+nf4_status moe_combine_grad(const void* dy, const void* ys, int32_t dtype, const float* weights,
+                            const int32_t* pos, int64_t T, int32_t top_k, int64_t rows, int64_t H,
+                            void* dys, float* dweights, void* stream) {
+  if (const nf4_status st = check_rows(dtype, pos, T, top_k, rows, H)) return st;
+  if (T == 0 || (!dys && !dweights)) return NF4_OK;
+  const int b = dtype_bytes(dtype);
+  if ((H > 0 && !dy) || (H > 0 && rows > 0 && dweights && !ys)) return NF4_EINVAL;
+  if (!aligned(dy, b) || !aligned(ys, b) || !aligned(dys, b) || !aligned(weights, 4) ||
+      !aligned(dweights, 4))
+    return NF4_EINVAL;
+  with_dtype(dtype, [&](auto d) {
+    hipLaunchKernelGGL((combine_grad_kernel<decltype(d)::value>), dim3(row_groups(T)),
+                       dim3(kRowThreads), 0, reinterpret_cast<hipStream_t>(stream), dy, ys, weights,
+                       pos, T, top_k, rows, H, dys, dweights);
+  });
+  return launch_status();
+}
+
+}  // extern "C"
