@@ -127,6 +127,64 @@ __device__ __forceinline__ uint32_t count_tiles(const Product& p) {
   return __builtin_amdgcn_readfirstlane(sum);
 }
 
+// Scales a wave's 32 TM tokens from m0 on x 32 TN channels from n0 on and writes
+// them, 32 tokens x CHANNELS at a time through an LDS region of its own, so that
+// whole lines of y are written.  16-byte pieces of an LDS row lie at piece ^ row,
+// so that neither side meets in a bank.
+template <int DT, bool GROUPED, int TM, int TN, int CHANNELS>
+__device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, int64_t n0, int64_t m0,
+                                           const i32x16 (&acc)[TN][TM], int8_t* lds) {
+  constexpr int kB = dtype_bytes(DT), kRow = CHANNELS * kB, kSwap = kRow / 16 - 1;
+  constexpr int kTiles = CHANNELS / 32, kPieces = CHANNELS / 8;  // of eight channels, to a row
+  const int lane = threadIdx.x & 63;
+  const float* ws = p.ws + t.expert * p.N;
+#pragma unroll
+  for (int i0 = 0; i0 < TN; i0 += kTiles) {
+    const int64_t n1 = n0 + 32 * i0;
+    const int64_t wide = min(p.N - n1, int64_t(CHANNELS));
+    float wscale[kTiles][16];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const int64_t n = n1 + 32 * i + 8 * (c >> 2) + 4 * (lane >> 5) + (c & 3);
+        wscale[i][c] = n < p.N ? ws[n] : 0.0f;
+      }
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int64_t m1 = m0 + 32 * j, m = m1 + (lane & 31);
+      const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
+      const float xs = src >= 0 ? p.xs[src] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i0 + i][j][c + e]) * xs * wscale[i][c + e];
+          const int at = (32 * i + 2 * c + 4 * (lane >> 5)) * kB;
+          int8_t* to = lds + (lane & 31) * kRow + (((at >> 4) ^ (lane & kSwap)) << 4) + (at & 15);
+          if constexpr (DT == INT8_FP32)
+            *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+          else
+            *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair<DT>(f[0], f[1]), pack_pair<DT>(f[2], f[3]));
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = lane; i < 32 * kPieces; i += 64) {
+        const int r = i / kPieces, at = i % kPieces;
+        if (m1 + r >= t.end || 8 * at >= wide) continue;
+        Piece<DT> v;
+#pragma unroll
+        for (int h = 0; h < kB / 2; ++h)
+          v.v[h] = *reinterpret_cast<const u32x4*>(lds + r * kRow + (((at * (kB / 2) + h) ^ (r & kSwap)) << 4));
+        store_piece<DT>(static_cast<char*>(p.y) + ((m1 + r) * p.N + n1) * kB, 8 * at, wide, v);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Tiles through LDS.  Four waves, 2 x 2, share a tile of BN channels x BM
 // tokens; each holds its quarter in int32 accumulators.  128 bytes of K at a
@@ -155,20 +213,21 @@ constexpr uint32_t kNever = 0x80000000u;
 
 // In the order of the program: one vector-memory load or LDS instruction
 // (kind), then `count` matrix instructions.
-constexpr int kSchedMfma = 0x8, kSchedLoad = 0x20, kSchedRead = 0x100, kSchedWrite = 0x200;
+constexpr int kSchedMfma = 0x8, kSchedLoad = 0x20, kSchedRead = 0x100;
 
-template <int DT, int BM, int BN>
-constexpr int tile_lds() {
-  constexpr int in = 2 * (BM + BN) * kDepth;
-  constexpr int out = 4 * 32 * (BN / 2 * dtype_bytes(DT) + 16);
-  return in > out ? in : out;
-}
+typedef __attribute__((address_space(3))) void* LdsPtr;
+typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
 template <int DT, bool GROUPED, int BM, int BN>
-__global__ __launch_bounds__(kTileThreads, BM* BN >= 256 * 256 ? 1 : 2) void tile_kernel(Product p) {
+__global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void tile_kernel(Product p) {
   constexpr int TM = BM / 64, TN = BN / 64;          // 32 x 32 tiles of a wave
   constexpr int LM = BM / 32, LN = BN / 32;          // 16-byte loads of a thread per step
-  __shared__ __attribute__((aligned(16))) int8_t s_mem[tile_lds<DT, BM, BN>()];
+  constexpr int kB = dtype_bytes(DT);
+  // two buffers that the compiler can tell apart: reads of one do not wait for
+  // the loads into the other
+  __shared__ __attribute__((aligned(256))) int8_t s_a[(BM + BN) * kDepth], s_b[(BM + BN) * kDepth];
+  constexpr int kOutChannels = DT == INT8_FP32 && BN == 256 ? BN / 4 : BN / 2;  // of a wave at a time
+  __shared__ __attribute__((aligned(256))) int8_t s_out[4 * 32 * kOutChannels * kB];
 
   // --- which tile
   const uint32_t tiles_n = static_cast<uint32_t>((p.N + BN - 1) / BN);
@@ -180,9 +239,10 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 256 * 256 ? 1 : 2) void til
   if constexpr (GROUPED) t = find_tile<BM>(p, tm);
   const int64_t n0 = static_cast<int64_t>(tn) * BN;
 
-  // --- memory to registers: eight threads a row
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int row = threadIdx.x >> 3, chunk = (threadIdx.x & 7) * 16;
+  // --- memory to LDS: a wave fills eight rows at a time
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int row = 8 * wave + (lane >> 3);
+  const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
   const int pitch = static_cast<int>(p.pitch);
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
   const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
@@ -198,36 +258,29 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 256 * 256 ? 1 : 2) void til
       xrow[i] = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
     }
   }
-  i32x4 g[LN + LM];
-  auto load = [&](int i, int k) {
+  auto load = [&](int8_t* buf, int i, int k) {
     const bool in = k + chunk < pitch;
     const uint32_t v = in ? voff + k : kNever;
+    const LdsPtr to = (LdsPtr)(buf + (32 * i + 8 * wave) * kDepth);
     if (i < LN)
-      g[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, v, 32 * i * pitch, 0));
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, v, 32 * i * pitch, 0, 0);
     else if constexpr (GROUPED)
-      g[i] = *reinterpret_cast<const i32x4*>(xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0));
+      __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
     else
-      g[i] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, v, 32 * (i - LN) * pitch, 0));
-  };
-
-  // --- registers to LDS: the weights' rows first, then the tokens'
-  constexpr int kBuffer = (BM + BN) * kDepth;
-  const int put = row * kDepth + (chunk ^ ((row >> 1 & 7) * 16));
-  auto store = [&](int i, int buf) {
-    *reinterpret_cast<i32x4*>(s_mem + buf * kBuffer + put + 32 * i * kDepth) = g[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v, 32 * (i - LN) * pitch, 0, 0);
   };
 
   // --- LDS to the matrix cores
   const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
   i32x4 fw[2][TN], fx[2][TM];
-  auto fetch = [&](int set, int buf, int part) {
-    const int at = buf * kBuffer + (lane & 31) * kDepth + (((2 * part + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
+  auto fetch = [&](int set, const int8_t* buf, int part) {
+    const int at = (lane & 31) * kDepth + (((2 * part + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
 #pragma unroll
     for (int i = 0; i < TN; ++i)
-      fw[set][i] = *reinterpret_cast<const i32x4*>(s_mem + (wn + 32 * i) * kDepth + at);
+      fw[set][i] = *reinterpret_cast<const i32x4*>(buf + (wn + 32 * i) * kDepth + at);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
-      fx[set][i] = *reinterpret_cast<const i32x4*>(s_mem + (BN + wm + 32 * i) * kDepth + at);
+      fx[set][i] = *reinterpret_cast<const i32x4*>(buf + (BN + wm + 32 * i) * kDepth + at);
   };
   i32x16 acc[TN][TM] = {};
   auto multiply = [&](int set) {
@@ -237,117 +290,337 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 256 * 256 ? 1 : 2) void til
       for (int j = 0; j < TM; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][i], fx[set][j], acc[i][j], 0, 0, 0);
   };
-
-  const int steps = (pitch + kDepth - 1) / kDepth;
-  if (steps > 0) {
+  constexpr int kMoves = LN + LM, kFirst = kMoves / 2;
+  // one step: `now` holds this step's rows, `next` the next one's
+  auto step = [&](int8_t* now, int8_t* next, int k) {
 #pragma unroll
-    for (int i = 0; i < LN + LM; ++i) load(i, 0);
+    for (int part = 0; part < 3; ++part) {
+      fetch((part + 1) & 1, now, part + 1);
+      if (part == 0) {
 #pragma unroll
-    for (int i = 0; i < LN + LM; ++i) {
-      store(i, 0);
-      load(i, kDepth);
-    }
-    __syncthreads();
-    fetch(0, 0, 0);
-    for (int k = 0; k < steps; ++k) {
-      const int buf = k & 1;
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        fetch((part + 1) & 1, buf, part + 1);
-        constexpr int kAll = LN + LM, kThird = (kAll + 2) / 3;
-        const int moves = part < 2 ? kThird : kAll - 2 * kThird;
-#pragma unroll
-        for (int i = part * kThird; i < part * kThird + moves; ++i) {
-          store(i, buf ^ 1);
-          load(i, (k + 2) * kDepth);
-        }
-        multiply(part & 1);
-        // operand reads first, one to a matrix instruction, then the moves
-#pragma unroll
-        for (int i = 0; i < TN + TM; ++i) {
-          __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < moves; ++i) {
-          __builtin_amdgcn_sched_group_barrier(kSchedWrite, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = kFirst; i < kMoves; ++i) load(next, i, (k + 1) * kDepth);
       }
-      __syncthreads();
-      fetch(0, buf ^ 1, 0);
-      multiply(1);
+      multiply(part & 1);
 #pragma unroll
       for (int i = 0; i < TN + TM; ++i) {
         __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
         __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+        if (part == 0 && i < kMoves - kFirst) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
+    fetch(0, next, 0);
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) load(now, i, (k + 2) * kDepth);
+    multiply(1);
+#pragma unroll
+    for (int i = 0; i < TN + TM; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (i < kFirst) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  const int steps = (pitch + kDepth - 1) / kDepth;
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < kMoves; ++i) load(s_a, i, 0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) load(s_b, i, kDepth);
+    fetch(0, s_a, 0);
+    for (int k = 0; k < steps; k += 2) {  // with an odd number the last step is one of zeros
+      step(s_a, s_b, k);
+      step(s_b, s_a, k + 1);
+    }
+    __syncthreads();
   }
 
-  // --- out: each wave has an LDS region of its own, 32 tokens of its channels
-  constexpr int kB = dtype_bytes(DT);
-  constexpr int kRow = BN / 2 * kB + 16;  // 16 bytes of padding
-  int8_t* mine = s_mem + wave * 32 * kRow;
-  const float* ws = p.ws + t.expert * p.N;
-  const int64_t n1 = n0 + wn;  // the wave's first channel
-  const int64_t wide = min(p.N - n1, int64_t(BN / 2));
-  float wscale[TN][16];
+  write_tile<DT, GROUPED, TM, TN, kOutChannels>(p, t, n0 + wn, t.first + wm, acc, s_out + wave * 32 * kOutChannels * kB);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: up to 16 tokens.  The eight waves of a workgroup share K, and each
+// holds the codes of its range, of all the tokens, in registers while the
+// workgroup goes through its share of the channels, 16 at a time: the weights go
+// from memory straight to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g
+// holds A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]),
+// each byte read once, a whole tile of them in flight while the one before is
+// used.  The waves' int32 sums meet in LDS.
+//
+// XT is the tokens' type.  Codes (kCodes) are read as they are; other types are
+// quantized on the way: first the tokens' peaks (a wave's lanes read what they
+// will encode; the waves' peaks meet in LDS), then the codes.
+// ---------------------------------------------------------------------------
+constexpr int kRowWaves = 8;
+constexpr int kRowThreads = 64 * kRowWaves;
+constexpr int kCodes = 3;
+
+template <int DT>
+__device__ __forceinline__ void store_four(void* y, int64_t i, int left, const float (&f)[4]) {
+  if (left >= 4) {
+    if constexpr (DT == INT8_FP32) {
+      const u32x4 v = {__builtin_bit_cast(uint32_t, f[0]), __builtin_bit_cast(uint32_t, f[1]),
+                       __builtin_bit_cast(uint32_t, f[2]), __builtin_bit_cast(uint32_t, f[3])};
+      *reinterpret_cast<u32x4_a4*>(static_cast<float*>(y) + i) = v;
+    } else {
+      const u32x2 v = {pack_pair<DT>(f[0], f[1]), pack_pair<DT>(f[2], f[3])};
+      *reinterpret_cast<u32x2_a2*>(static_cast<uint16_t*>(y) + i) = v;
+    }
+    return;
+  }
 #pragma unroll
-  for (int i = 0; i < TN; ++i)
+  for (int e = 0; e < 3; ++e)
+    if (e < left) {
+      if constexpr (DT == INT8_FP32)
+        static_cast<float*>(y)[i + e] = f[e];
+      else
+        static_cast<uint16_t*>(y)[i + e] = to_half_bits<DT>(f[e]);
+    }
+}
+
+template <int XT, int DT, bool GROUPED, int UNITS>
+__global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Product p, const void* x, int K) {
+  __shared__ i32x4 s_sum[2][kRowWaves][64];
+  __shared__ uint32_t s_peak[kRowWaves][16];
+  const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16);
+  RowTile t = {0, p.M, 0};
+  if constexpr (GROUPED) {
+    t = find_tile<16>(p, blockIdx.y);
+    if (t.end <= t.first) return;
+  }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int pitch = static_cast<int>(p.pitch);
+  const int inside = (lane >> 4) * 16;
+  // the wave's range, in units of 64 bytes
+  const int units = pitch / 64, each = (units + kRowWaves - 1) / kRowWaves;
+  const int first = wave * each, end = min(units, first + each);
+  const uint32_t voff = static_cast<uint32_t>((lane & 15) * pitch + inside);
+  const int8_t* w0 = p.wq + t.expert * p.N * p.pitch;
+  i32x4 w[UNITS];
+  auto load = [&](uint32_t tile) {
+    const int64_t n0 = static_cast<int64_t>(tile) * 16;
+    const auto rw = rsrc(w0 + n0 * p.pitch, static_cast<uint32_t>(min(int64_t(16), p.N - n0) * p.pitch));
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const int64_t n = n1 + 32 * i + 8 * (c >> 2) + 4 * (lane >> 5) + (c & 3);
-      wscale[i][c] = n < p.N ? ws[n] : 0.0f;
+    for (int u = 0; u < UNITS; ++u)
+      w[u] = __builtin_bit_cast(
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, first + u < end ? voff + 64 * (first + u) : kNever, 0, 0));
+  };
+  load(blockIdx.x);
+
+  const int64_t m = t.first + (lane & 15);
+  const int64_t src = source_row<GROUPED>(p, min(m, t.end - 1));
+  float xs = 0.0f;
+  i32x4 codes[UNITS];
+  if constexpr (XT == kCodes) {
+    const int8_t* xr = (src >= 0 ? p.xq + src * p.pitch : w0) + inside;  // any row that may be read
+    if (src >= 0) xs = p.xs[src];
+    // past the wave's range the weights are zeros
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u)
+      codes[u] = *reinterpret_cast<const i32x4*>(xr + (first + u < end ? 64 * (first + u) : 0));
+  } else {
+    // K is a multiple of 16, so a lane's 16 elements of a unit all exist or none
+    // does; in place of the latter the row's first ones, which change no peak
+    const char* xr = static_cast<const char*>(x) + src * K * dtype_bytes(XT);
+    constexpr bool kHold = UNITS * dtype_bytes(XT) <= 8;  // in registers from the first reading to the second
+    Piece<XT> held[kHold ? UNITS : 1][2];
+    auto read = [&](int u, int h) {
+      const int k = 64 * (first + u) + inside;
+      return whole_piece<XT>(xr, (first + u < end && k < K ? k : 0) + 8 * h);
+    };
+    uint32_t peak = 0;
+    if constexpr (kHold) {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) held[u][0] = read(u, 0), held[u][1] = read(u, 1);
     }
 #pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const int64_t m0 = t.first + wm + 32 * j;
-    const int64_t m = m0 + (lane & 31);
-    const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
-    const float xs = src >= 0 ? p.xs[src] : 0.0f;
+    for (int u = 0; u < UNITS; ++u)
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+      for (int h = 0; h < 2; ++h) peak = max(peak, piece_peak<XT>(kHold ? held[kHold ? u : 0][h] : read(u, h)));
+    peak = max(peak, static_cast<uint32_t>(__shfl_xor(static_cast<int>(peak), 16)));
+    peak = max(peak, static_cast<uint32_t>(__shfl_xor(static_cast<int>(peak), 32)));
+    if (lane < 16) s_peak[wave][lane] = peak;
+    __syncthreads();
 #pragma unroll
-      for (int c = 0; c < 16; c += 4) {
-        float f[4];
+    for (int v = 0; v < kRowWaves; ++v) peak = max(peak, s_peak[v][lane & 15]);
+    const RowScale scale = row_scale(peak);
+    xs = scale.scale;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i][j][c + e]) * xs * wscale[i][c + e];
-        int8_t* to = mine + (lane & 31) * kRow + (32 * i + 2 * c + 4 * (lane >> 5)) * kB;
-        if constexpr (DT == INT8_FP32)
-          *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
-        else
-          *reinterpret_cast<uint2*>(to) = make_uint2(pack_pair<DT>(f[0], f[1]), pack_pair<DT>(f[2], f[3]));
-      }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    constexpr int kPieces = BN / 2 / 8;  // of eight channels, to a row
-#pragma unroll
-    for (int i = lane; i < 32 * kPieces; i += 64) {
-      const int r = i / kPieces, at = i % kPieces * 8;
-      if (m0 + r >= t.end || at >= wide) continue;
-      Piece<DT> v;
-      v.v[0] = *reinterpret_cast<const u32x4*>(mine + r * kRow + at * kB);
-      if constexpr (DT == INT8_FP32) v.v[1] = *reinterpret_cast<const u32x4*>(mine + r * kRow + at * kB + 16);
-      store_piece<DT>(static_cast<char*>(p.y) + ((m0 + r) * p.N + n1) * kB, at, wide, v);
+    for (int u = 0; u < UNITS; ++u) {
+      const uint2 lo = encode_piece<XT>(kHold ? held[kHold ? u : 0][0] : read(u, 0), scale);
+      const uint2 hi = encode_piece<XT>(kHold ? held[kHold ? u : 0][1] : read(u, 1), scale);
+      codes[u] = i32x4{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(hi.x), static_cast<int>(hi.y)};
+      if (64 * (first + u) + inside >= K) codes[u] = i32x4{0, 0, 0, 0};  // the row's padding
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+
+  int turn = 0;
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
+    i32x4 acc = {};
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u], codes[u], acc, 0, 0, 0);
+    if (tile + gridDim.x < tiles) load(tile + gridDim.x);
+    s_sum[turn & 1][wave][lane] = acc;
+    __syncthreads();
+    // one wave a turn adds up; its buffer is written again two turns later, after
+    // a barrier that this wave reaches when it is through
+    if (wave != (turn & (kRowWaves - 1))) continue;
+    i32x4 sum = {};
+#pragma unroll
+    for (int v = 0; v < kRowWaves; ++v) sum += s_sum[turn & 1][v][lane];
+    const int64_t n = static_cast<int64_t>(tile) * 16 + 4 * (lane >> 4);
+    const int left = static_cast<int>(min(p.N - n, int64_t(4)));
+    if (m >= t.end || left <= 0) continue;
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      f[e] = static_cast<float>(sum[e]) * xs * p.ws[t.expert * p.N + n + min(e, left - 1)];
+    store_four<DT>(p.y, m * p.N + n, left, f);
   }
 }
 
-template <bool GROUPED, int BM, int BN>
-nf4_status launch_tiles(const Product& p, int32_t y_dtype, int64_t tiles_m, hipStream_t st) {
-  const int64_t all = tiles_m * ((p.N + BN - 1) / BN);
-  const int64_t groups = (all + kDies - 1) / kDies * kDies;
-  if (groups * kTileThreads >= (int64_t(1) << 32)) return NF4_EUNSUPPORTED;
-  with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, BM, BN>),
-                       dim3(static_cast<uint32_t>(groups)), dim3(kTileThreads), 0, st, p);
-  });
-  return launch_status();
+// ---------------------------------------------------------------------------
+// Small tiles: WM x WN x WK waves, each with one or more 32 x 32 tiles (TM x
+// TN); the WK waves of a tile share each step's K, 128 / WK bytes each.  STAGES
+// buffers: the rows of a step are asked for STAGES - 1 steps ahead, and a wave
+// waits only for those of the step that it is about to use.  Several workgroups
+// share a compute unit, so nothing is done by hand within a step.
+// ---------------------------------------------------------------------------
+template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES>
+__global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
+  constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
+  constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
+  constexpr int kRows = kThreads / 8;                         // rows that a load of all threads fills
+  constexpr int LM = BM / kRows, LN = BN / kRows, kLoads = LM + LN;
+  static_assert(LM * kRows == BM && LN * kRows == BN && STAGES >= 2 && STAGES <= 4);
+  constexpr int kB = dtype_bytes(DT);
+  constexpr int kStage = (BM + BN) * kDepth;
+  static_assert(WK == 1 || (TM == 1 && TN == 1));
+  // buffers that the compiler can tell apart: reads of one do not wait for the
+  // loads into another
+  __shared__ __attribute__((aligned(256))) int8_t s_0[kStage], s_1[kStage], s_2[STAGES > 2 ? kStage : 16],
+      s_3[STAGES > 3 ? kStage : 16];
+  __shared__ __attribute__((aligned(256))) int8_t s_out[WM * WN * 32 * 32 * TN * kB];
+  __shared__ __attribute__((aligned(256))) i32x4 s_meet[WK > 1 ? (WK - 1) * WM * WN * 256 : 1];
+
+  const uint32_t tiles_n = static_cast<uint32_t>((p.N + BN - 1) / BN);
+  uint32_t tiles_m = static_cast<uint32_t>((p.M + BM - 1) / BM);
+  if constexpr (GROUPED) tiles_m = count_tiles<BM>(p);
+  uint32_t tm, tn;
+  if (!place_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
+  RowTile t = {static_cast<int64_t>(tm) * BM, min(p.M, static_cast<int64_t>(tm) * BM + BM), 0};
+  if constexpr (GROUPED) t = find_tile<BM>(p, tm);
+  const int64_t n0 = static_cast<int64_t>(tn) * BN;
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int row = 8 * wave + (lane >> 3);
+  const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
+  const int pitch = static_cast<int>(p.pitch);
+  const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
+  const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
+  const auto rx = rsrc(GROUPED ? nullptr : p.xq + t.first * p.pitch,
+                       static_cast<uint32_t>((t.end - t.first) * p.pitch));
+  const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
+  const int8_t* xrow[GROUPED ? LM : 1];
+  if constexpr (GROUPED) {
+#pragma unroll
+    for (int i = 0; i < LM; ++i) {
+      const int64_t m = t.first + row + kRows * i;
+      const int64_t src = m < t.end ? source_row<true>(p, m) : -1;
+      xrow[i] = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
+    }
+  }
+  auto load = [&](int8_t* buf, int k) {
+    const bool in = k + chunk < pitch;
+    const uint32_t v = in ? voff + k : kNever;
+#pragma unroll
+    for (int i = 0; i < LN; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(buf + (kRows * i + 8 * wave) * kDepth), 16, v,
+                                               kRows * i * pitch, 0, 0);
+#pragma unroll
+    for (int i = 0; i < LM; ++i) {
+      const LdsPtr to = (LdsPtr)(buf + (BN + kRows * i + 8 * wave) * kDepth);
+      if constexpr (GROUPED)
+        __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[i] + (in ? k + chunk : 0)), to, 16, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v, kRows * i * pitch, 0, 0);
+    }
+  };
+
+  const int wk = wave % WK, wn = wave / WK % WN * (32 * TN), wm = wave / (WK * WN) * (32 * TM);
+  constexpr int kParts = 4 / WK;
+  i32x16 acc[TN][TM] = {};
+  auto step = [&](const int8_t* now, int8_t* free, int k) {
+    // this step's rows are there when no more than the later steps' loads are
+    // out; past the barrier that holds for all waves, and all are through with
+    // the step before
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
+    load(free, k + (STAGES - 1) * kDepth);
+    i32x4 fw[kParts][TN], fx[kParts][TM];
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      const int at = (lane & 31) * kDepth + (((2 * (wk * kParts + part) + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
+#pragma unroll
+      for (int i = 0; i < TN; ++i) fw[part][i] = *reinterpret_cast<const i32x4*>(now + (wn + 32 * i) * kDepth + at);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        fx[part][i] = *reinterpret_cast<const i32x4*>(now + (BN + wm + 32 * i) * kDepth + at);
+    }
+#pragma unroll
+    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[part][i], fx[part][j], acc[i][j], 0, 0, 0);
+  };
+  if (pitch > 0) {
+    load(s_0, 0);
+    if constexpr (STAGES > 2) load(s_1, kDepth);
+    if constexpr (STAGES > 3) load(s_2, 2 * kDepth);
+    for (int k = 0; k < pitch;) {
+      // past the last step the rows are zeros
+      if constexpr (STAGES == 2) {
+        step(s_0, s_1, k), step(s_1, s_0, k + kDepth);
+      } else if constexpr (STAGES == 3) {
+        step(s_0, s_2, k);
+        if ((k += kDepth) >= pitch) break;
+        step(s_1, s_0, k);
+        if ((k += kDepth) >= pitch) break;
+        step(s_2, s_1, k);
+      } else {
+        step(s_0, s_3, k);
+        if ((k += kDepth) >= pitch) break;
+        step(s_1, s_0, k);
+        if ((k += kDepth) >= pitch) break;
+        step(s_2, s_1, k);
+        if ((k += kDepth) >= pitch) break;
+        step(s_3, s_2, k);
+      }
+      k += kDepth;
+    }
+  }  if constexpr (WK > 1) {
+    // the tile's other waves hand their sums to the first
+    const int slot = (wave / WK) * (WK - 1) - 1;
+    if (wk > 0)
+#pragma unroll
+      for (int c = 0; c < 16; c += 4)
+        s_meet[((slot + wk) * 4 + c / 4) * 64 + lane] = i32x4{acc[0][0][c], acc[0][0][c + 1], acc[0][0][c + 2], acc[0][0][c + 3]};
+    __syncthreads();
+    if (wk > 0) return;
+#pragma unroll
+    for (int v = 1; v < WK; ++v)
+#pragma unroll
+      for (int c = 0; c < 16; c += 4) {
+        const i32x4 o = s_meet[((slot + v) * 4 + c / 4) * 64 + lane];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[0][0][c + e] += o[e];
+      }
+  }
+  write_tile<DT, GROUPED, TM, TN, 32 * TN>(p, t, n0 + wn, t.first + wm, acc, s_out + wave / WK * (32 * 32 * TN * kB));
 }
 
 // Tiles of BM rows that p.M rows need at most: every expert ends in at most one
@@ -358,12 +631,77 @@ int64_t row_tiles(const Product& p, int64_t BM) {
   return (p.M + BM - 1) / BM;
 }
 
+// Workgroups of `threads` for the tiles, a multiple of the dies; 0 if a grid
+// cannot have so many.
+template <bool GROUPED>
+uint32_t tile_groups(const Product& p, int BM, int BN, int threads) {
+  const int64_t all = row_tiles<GROUPED>(p, BM) * ((p.N + BN - 1) / BN);
+  const int64_t groups = (all + kDies - 1) / kDies * kDies;
+  return groups * threads < (int64_t(1) << 32) ? static_cast<uint32_t>(groups) : 0;
+}
+
+template <bool GROUPED, int BM, int BN>
+nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
+  const uint32_t groups = tile_groups<GROUPED>(p, BM, BN, kTileThreads);
+  if (groups == 0) return NF4_EUNSUPPORTED;
+  with_dtype(y_dtype, [&](auto d) {
+    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, BM, BN>), dim3(groups), dim3(kTileThreads), 0,
+                       st, p);
+  });
+  return launch_status();
+}
+
+template <bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES>
+nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
+  constexpr int kThreads = 64 * WM * WN * WK;
+  const uint32_t groups = tile_groups<GROUPED>(p, 32 * WM * TM, 32 * WN * TN, kThreads);
+  if (groups == 0) return NF4_EUNSUPPORTED;
+  with_dtype(y_dtype, [&](auto d) {
+    hipLaunchKernelGGL((stream_kernel<decltype(d)::value, GROUPED, WM, WN, WK, TM, TN, STAGES>), dim3(groups),
+                       dim3(kThreads), 0, st, p);
+  });
+  return launch_status();
+}
+
+constexpr int64_t kRowMaxUnits = 22;
+constexpr int64_t kRowMaxPitch = kRowMaxUnits * kRowWaves * 64;
+
+// Few rows: the tokens' codes or, with XT another type, the tokens at x.
+template <int XT, bool GROUPED>
+nf4_status launch_rows(const Product& p, const void* x, int64_t K, int32_t y_dtype, hipStream_t st) {
+  const int64_t tiles = (p.N + 15) / 16, rows = row_tiles<GROUPED>(p, 16);
+  if (rows > 65535) return NF4_EUNSUPPORTED;
+  // two workgroups fit a compute unit
+  const int64_t most = 2 * device_cus(), share = (most + rows - 1) / rows;
+  const dim3 grid(static_cast<uint32_t>(tiles < share ? tiles : share), static_cast<uint32_t>(rows));
+  const int64_t units = (p.pitch / 64 + kRowWaves - 1) / kRowWaves;
+  with_dtype(y_dtype, [&](auto d) {
+    constexpr int DT = decltype(d)::value;
+    if (units <= 4)
+      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, 4>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+    else if (units <= 8)
+      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, 8>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+    else
+      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, kRowMaxUnits>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+  });
+  return launch_status();
+}
+
+// Whether int8_linear quantizes on the way.
+bool fuses(int64_t M, int64_t K) { return M <= 16 && K > 0 && K % 16 == 0 && K <= kRowMaxPitch; }
+
 template <bool GROUPED>
 nf4_status launch(const Product& p, int32_t y_dtype, hipStream_t st) {
   const int64_t rows = GROUPED ? p.M / p.experts : p.M;
-  if (rows > 128) return launch_tiles<GROUPED, 256, 256>(p, y_dtype, row_tiles<GROUPED>(p, 256), st);
-  if (rows > 64) return launch_tiles<GROUPED, 128, 128>(p, y_dtype, row_tiles<GROUPED>(p, 128), st);
-  return launch_tiles<GROUPED, 64, 64>(p, y_dtype, row_tiles<GROUPED>(p, 64), st);
+  if (rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch) return launch_rows<kCodes, GROUPED>(p, nullptr, 0, y_dtype, st);
+#ifdef FORCE
+  return FORCE;
+#endif
+  if (rows <= 32) return launch_stream<GROUPED, 1, 1, 4, 1, 1, 4>(p, y_dtype, st);
+  if (rows <= 64) return launch_stream<GROUPED, 2, 1, 2, 1, 1, 4>(p, y_dtype, st);
+  if (rows <= 256) return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
+  if (rows <= 1024) return launch_stream<GROUPED, 2, 2, 1, 2, 2, 3>(p, y_dtype, st);
+  return launch_tiles<GROUPED, 256, 256>(p, y_dtype, st);
 }
 
 // What the products check alike (the activations apart).
@@ -402,6 +740,7 @@ nf4_status int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const 
 
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return 0;
+  if (fuses(M, K)) return 0;
   return codes_bytes(M, K) + (static_cast<size_t>(M) * 4 + 255) / 256 * 256 +
          int8_gemm_workspace_size(M, N, K);
 }
@@ -416,8 +755,14 @@ nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const f
   if ((K > 0 && !x) || !aligned(x, dtype_bytes(x_dtype))) return NF4_EINVAL;
   if (const nf4_status st = check_product(wq, ws, N, K, y, y_dtype)) return st;
   if (M > kMaxDim) return NF4_EUNSUPPORTED;
-  if (!workspace || workspace_bytes < int8_linear_workspace_size(M, N, K)) return NF4_EINVAL;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (fuses(M, K)) {
+    const Product p = {nullptr, nullptr, wq, ws, y, M, N, pitch_of(K), nullptr, nullptr, M, 1, 1};
+    nf4_status result = NF4_OK;
+    with_dtype(x_dtype, [&](auto a) { result = launch_rows<decltype(a)::value, false>(p, x, K, y_dtype, st); });
+    return result;
+  }
+  if (!workspace || workspace_bytes < int8_linear_workspace_size(M, N, K)) return NF4_EINVAL;
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(xq + codes_bytes(M, K));
   quantize_launch(x, x_dtype, M, K, xq, xs, st);

@@ -21,6 +21,8 @@ using nf4dev::u32x4;
 // the element's alignment.
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
 
 __device__ __host__ constexpr int dtype_bytes(int dt) { return dt == INT8_FP32 ? 4 : 2; }
 
@@ -30,20 +32,26 @@ struct Piece {
   u32x4 v[DT == INT8_FP32 ? 2 : 1];
 };
 
+// Elements [at, at + 8) of the row at p, all of which exist.
+template <int DT>
+__device__ __forceinline__ Piece<DT> whole_piece(const void* p, int64_t at) {
+  Piece<DT> r;
+  const char* a = static_cast<const char*>(p) + at * dtype_bytes(DT);
+  if constexpr (DT == INT8_FP32) {
+    r.v[0] = *reinterpret_cast<const u32x4_a4*>(a);
+    r.v[1] = *reinterpret_cast<const u32x4_a4*>(a + 16);
+  } else {
+    r.v[0] = *reinterpret_cast<const u32x4_a2*>(a);
+  }
+  return r;
+}
+
 // Elements [at, at + 8) of the n elements at p; those past n are zero.
 template <int DT>
 __device__ __forceinline__ Piece<DT> load_piece(const void* p, int64_t at, int64_t n) {
   Piece<DT> r;
   const char* a = static_cast<const char*>(p) + at * dtype_bytes(DT);
-  if (at + 8 <= n) {
-    if constexpr (DT == INT8_FP32) {
-      r.v[0] = *reinterpret_cast<const u32x4_a4*>(a);
-      r.v[1] = *reinterpret_cast<const u32x4_a4*>(a + 16);
-    } else {
-      r.v[0] = *reinterpret_cast<const u32x4_a2*>(a);
-    }
-    return r;
-  }
+  if (at + 8 <= n) return whole_piece<DT>(p, at);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (DT == INT8_FP32) {
