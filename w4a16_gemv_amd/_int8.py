@@ -22,17 +22,27 @@ def _row_dtype(dtype: torch.dtype, name: str) -> int:
     return code
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _on(dev: torch.device, t: torch.Tensor, name: str) -> None:
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """The pointer of a contiguous GPU tensor (of a type that was checked)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on the GPU, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _run(fn: str, dev: torch.device, *args) -> None:
     """One library call on the current stream of `dev`."""
     f = getattr(load(), fn)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
+    # the raw handle: torch.cuda.current_stream builds an object for it, which
+    # costs as much as the rest of a small call's marshalling
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    if dev.index == torch._C._cuda_getDevice():
         st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -43,18 +53,19 @@ def _run(fn: str, dev: torch.device, *args) -> None:
 
 def _size(fn: str, dev: torch.device, *args) -> int:
     f = getattr(load(), fn)
-    if dev.index == torch.cuda.current_device():
+    if dev.index == torch._C._cuda_getDevice():
         return f(*args)
     with torch.cuda.device(dev):
         return f(*args)
 
 
-def _scratch(workspace, nbytes: int, dev: torch.device):
+def _scratch(workspace, fn: str, dev: torch.device, *sizes):
     """(pointer, bytes, tensor to keep until the call has returned) of the
     caller's workspace, or of one from torch's allocator."""
     if workspace is not None:
-        _same_device(dev, workspace=workspace)
+        _on(dev, workspace, "workspace")
         return _dev(workspace, "workspace", (torch.uint8,), 0), workspace.numel(), workspace
+    nbytes = _size(fn, dev, *sizes)
     if nbytes == 0:
         return None, 0, None
     t = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -86,7 +97,7 @@ class Int8Tensor:
         _dev(scale, "scale", _F32, rows)
         if scale.numel() != rows:
             raise ValueError(f"scale has {scale.numel()} elements for {rows} rows")
-        _same_device(data.device, scale=scale)
+        _on(data.device, scale, "scale")
         self.data, self.scale, self.K = data, scale, K
 
     @property
@@ -119,16 +130,16 @@ def int8_quantize(x: torch.Tensor, out: Int8Tensor | None = None) -> Int8Tensor:
     for n in x.shape[:-1]:
         rows *= n
     code = _row_dtype(x.dtype, "x")
-    px = _dev(x, "x", (x.dtype,), rows * K)
-    dev = x.device
+    px, dev = _gpu(x, "x"), x.device
     if out is None:
         out = Int8Tensor.__new__(Int8Tensor)
         out.data = torch.empty((rows, int8_pitch(K)), dtype=torch.int8, device=dev)
         out.scale = torch.empty(rows, dtype=torch.float32, device=dev)
         out.K = K
-    elif out.rows != rows or out.K != K:
-        raise ValueError(f"out is {out.rows} x {out.K}, expected {rows} x {K}")
-    _same_device(dev, out=out.data)
+    else:
+        if out.rows != rows or out.K != K:
+            raise ValueError(f"out is {out.rows} x {out.K}, expected {rows} x {K}")
+        _on(dev, out.data, "out")
     _run("int8_quantize", dev, px, code, rows, K, out.data.data_ptr(), out.scale.data_ptr())
     return out
 
@@ -136,29 +147,30 @@ def int8_quantize(x: torch.Tensor, out: Int8Tensor | None = None) -> Int8Tensor:
 def int8_dequant(t: Int8Tensor, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of t's codes as [rows][K] in bf16, fp16 or fp32."""
-    dev = t.data.device
+    dev, rows, K = t.data.device, t.data.shape[0], t.K
     if out is None:
-        out = torch.empty((t.rows, t.K), dtype=out_dtype, device=dev)
-    code = _row_dtype(out.dtype, "out")
-    if tuple(out.shape) != (t.rows, t.K):
-        raise ValueError(f"out must be [{t.rows}, {t.K}], got shape {tuple(out.shape)}")
-    _same_device(dev, out=out)
-    _run("int8_dequant", dev, t.data.data_ptr(), t.scale.data_ptr(), t.rows, t.K,
-         _dev(out, "out", (out.dtype,), 0), code)
+        code = _row_dtype(out_dtype, "out_dtype")
+        out = torch.empty((rows, K), dtype=out_dtype, device=dev)
+    else:
+        code = _row_dtype(out.dtype, "out")
+        if out.shape != (rows, K):
+            raise ValueError(f"out must be [{rows}, {K}], got shape {tuple(out.shape)}")
+        _on(dev, out, "out")
+    _run("int8_dequant", dev, t.data.data_ptr(), t.scale.data_ptr(), rows, K, _gpu(out, "out"), code)
     return out
 
 
 def _out(y, rows: int, N: int, dtype: torch.dtype, dev: torch.device):
-    """(y, its type code) with y allocated if it is None."""
+    """(y, its pointer, its type code) with y allocated if it is None."""
     if y is None:
         code = _row_dtype(dtype, "out_dtype")
-        return torch.empty((rows, N), dtype=dtype, device=dev), code
+        y = torch.empty((rows, N), dtype=dtype, device=dev)
+        return y, y.data_ptr(), code
     code = _row_dtype(y.dtype, "y")
-    if tuple(y.shape) != (rows, N):
+    if y.shape != (rows, N):
         raise ValueError(f"y must be [{rows}, {N}], got shape {tuple(y.shape)}")
-    _same_device(dev, y=y)
-    _dev(y, "y", (y.dtype,), 0)
-    return y, code
+    _on(dev, y, "y")
+    return y, _gpu(y, "y"), code
 
 
 def int8_gemm_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | None:
@@ -192,13 +204,13 @@ def int8_gemm(x: Int8Tensor, w: Int8Tensor, y: torch.Tensor | None = None,
     allocator."""
     if x.K != w.K:
         raise ValueError(f"x has K={x.K}, w has K={w.K}")
-    M, N, dev = x.rows, w.rows, x.data.device
-    _same_device(dev, w=w.data)
-    y, code = _out(y, M, N, out_dtype, dev)
-    pw, wbytes, _keep = _scratch(workspace, _size("int8_gemm_workspace_size", dev, M, N, x.K)
-                                 if workspace is None else 0, dev)
-    _run("int8_gemm", dev, x.data.data_ptr(), x.scale.data_ptr(), w.data.data_ptr(),
-         w.scale.data_ptr(), M, N, x.K, y.data_ptr(), code, pw, wbytes)
+    xd, wd = x.data, w.data
+    M, N, dev = xd.shape[0], wd.shape[0], xd.device
+    _on(dev, wd, "w")
+    y, py, code = _out(y, M, N, out_dtype, dev)
+    pw, wbytes, _keep = _scratch(workspace, "int8_gemm_workspace_size", dev, M, N, x.K)
+    _run("int8_gemm", dev, xd.data_ptr(), x.scale.data_ptr(), wd.data_ptr(), w.scale.data_ptr(), M, N,
+         x.K, py, code, pw, wbytes)
     return y
 
 
@@ -210,22 +222,21 @@ def int8_linear(x: torch.Tensor, w: Int8Tensor, y: torch.Tensor | None = None,
 
     workspace: a uint8 tensor from int8_linear_workspace, or None for one from
     torch's allocator."""
-    if x.dim() not in (1, 2) or x.shape[-1] != w.K:
+    one = x.dim() == 1
+    if x.dim() > 2 or x.dim() < 1 or x.shape[-1] != w.K:
         raise ValueError(f"x must be [M, {w.K}] or [{w.K}], got shape {tuple(x.shape)}")
-    M, N, dev = 1 if x.dim() == 1 else x.shape[0], w.rows, x.device
     xcode = _row_dtype(x.dtype, "x")
-    px = _dev(x, "x", (x.dtype,), 0)
-    _same_device(dev, w=w.data)
-    if y is not None and x.dim() == 1 and y.dim() == 1:
-        _out(y.unsqueeze(0), M, N, out_dtype, dev)
-        y2, code = y, _ROWS[y.dtype]
-    else:
-        y2, code = _out(y, M, N, out_dtype, dev)
-    pw, wbytes, _keep = _scratch(workspace, _size("int8_linear_workspace_size", dev, M, N, w.K)
-                                 if workspace is None else 0, dev)
-    _run("int8_linear", dev, px, xcode, w.data.data_ptr(), w.scale.data_ptr(), M, N, w.K,
-         y2.data_ptr(), code, pw, wbytes)
-    return y2.view(N) if x.dim() == 1 and y is None else y2
+    px, dev, wd = _gpu(x, "x"), x.device, w.data
+    M, N = 1 if one else x.shape[0], wd.shape[0]
+    _on(dev, wd, "w")
+    flat = one and (y is None or y.dim() == 1)
+    y2, py, code = _out(y.unsqueeze(0) if flat and y is not None else y, M, N, out_dtype, dev)
+    pw, wbytes, _keep = _scratch(workspace, "int8_linear_workspace_size", dev, M, N, w.K)
+    _run("int8_linear", dev, px, xcode, wd.data_ptr(), w.scale.data_ptr(), M, N, w.K, py, code, pw,
+         wbytes)
+    if y is not None:
+        return y
+    return y2.view(N) if one else y2
 
 
 def int8_gemm_grouped(x: Int8Tensor, w: Int8Tensor, route, y: torch.Tensor | None = None,
@@ -248,10 +259,12 @@ def int8_gemm_grouped(x: Int8Tensor, w: Int8Tensor, route, y: torch.Tensor | Non
     want = route.rows if x_sorted else route.T
     if x.rows != want:
         raise ValueError(f"x has {x.rows} rows, expected {want}")
-    N, dev = w.rows // E, x.data.device
-    _same_device(dev, w=w.data, route=route.offsets)
-    y, code = _out(y, route.rows, N, out_dtype, dev)
-    _run("int8_gemm_grouped", dev, x.data.data_ptr(), x.scale.data_ptr(), x.rows,
-         None if x_sorted else route.order.data_ptr(), route.top_k, w.data.data_ptr(),
-         w.scale.data_ptr(), route.offsets.data_ptr(), E, route.rows, N, x.K, y.data_ptr(), code)
+    xd, wd, rows = x.data, w.data, route.rows
+    N, dev = wd.shape[0] // E, xd.device
+    _on(dev, wd, "w")
+    _on(dev, route.offsets, "route")
+    y, py, code = _out(y, rows, N, out_dtype, dev)
+    _run("int8_gemm_grouped", dev, xd.data_ptr(), x.scale.data_ptr(), xd.shape[0],
+         None if x_sorted else route.order.data_ptr(), route.top_k, wd.data_ptr(),
+         w.scale.data_ptr(), route.offsets.data_ptr(), E, rows, N, x.K, py, code)
     return y

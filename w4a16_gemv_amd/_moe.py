@@ -11,10 +11,11 @@ from __future__ import annotations
 
 import torch
 
-from ._binding import _dev, _F32
-from ._int8 import _row_dtype, _run, _same_device, _scratch, _size
+from ._binding import _dev
+from ._int8 import _gpu, _on, _row_dtype, _run, _scratch
 
 _I32 = (torch.int32,)
+_IDS = {torch.int32: 4, torch.int64: 8}
 
 
 class MoeRoute:
@@ -34,7 +35,8 @@ class MoeRoute:
         _dev(offsets, "offsets", _I32, 1)
         if order.numel() != pos.numel():
             raise ValueError(f"order has {order.numel()} elements, pos {pos.numel()}")
-        _same_device(pos.device, offsets=offsets, order=order)
+        _on(pos.device, offsets, "offsets")
+        _on(pos.device, order, "order")
         self.offsets, self.order, self.pos = offsets, order, pos
 
     @property
@@ -65,56 +67,48 @@ def moe_sort(ids: torch.Tensor, experts: int, workspace: torch.Tensor | None = N
     experts = int(experts)
     if experts < 0:
         raise ValueError(f"experts must not be negative, got {experts}")
-    pi = _dev(ids, "ids", (torch.int32, torch.int64), 0)
-    dev = ids.device
+    if ids.dtype not in _IDS:
+        raise ValueError(f"ids must be int32 or int64, got {ids.dtype}")
+    pi, dev = _gpu(ids, "ids"), ids.device
     route = MoeRoute.__new__(MoeRoute)
     route.offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
     route.order = torch.empty(T * top_k, dtype=torch.int32, device=dev)
     route.pos = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    pw, nbytes, _keep = _scratch(workspace, _size("moe_sort_workspace_size", dev, T, top_k, experts)
-                                 if workspace is None else 0, dev)
-    _run("moe_sort", dev, pi, ids.element_size(), T, top_k, experts, route.offsets.data_ptr(),
+    pw, nbytes, _keep = _scratch(workspace, "moe_sort_workspace_size", dev, T, top_k, experts)
+    _run("moe_sort", dev, pi, _IDS[ids.dtype], T, top_k, experts, route.offsets.data_ptr(),
          route.order.data_ptr(), route.pos.data_ptr(), pw, nbytes)
     return route
 
 
-def _no_grad(fn: str, **tensors) -> None:
-    if torch.is_grad_enabled():
-        for name, t in tensors.items():
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{fn}: {name} requires a gradient, which autograd would not see; "
-                                 "call it under torch.no_grad() or in a Function, and its gradient "
-                                 "function in the backward pass")
+def _no_grad(fn: str, *tensors) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{fn}: a tensor requires a gradient, which autograd would not see; call it under "
+                         "torch.no_grad() or in a Function, and its gradient function in the backward pass")
 
 
-def _rows(t: torch.Tensor, name: str, shape, dev, dtype=None) -> int:
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
-    _same_device(dev, **{name: t})
-    return _dev(t, name, (t.dtype if dtype is None else dtype,), 0)
-
-
-def _weights(weights, route: MoeRoute, dev):
-    if weights is None:
-        return None
-    _rows(weights, "weights", route.pos.shape, dev)
-    return _dev(weights, "weights", _F32, 0)
+def _rows(t: torch.Tensor, name: str, rows: int, H: int, dev, dtype) -> int:
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, H):
+        raise ValueError(f"{name} must be [{rows}, {H}], got shape {tuple(t.shape)}")
+    _on(dev, t, name)
+    return _gpu(t, name)
 
 
 def moe_gather(x: torch.Tensor, route: MoeRoute, out: torch.Tensor | None = None) -> torch.Tensor:
     """x's rows ([T][H]: bf16, fp16 or fp32) in sorted order, [route.rows][H];
     rows that no slot has are left as they were (undefined where out is None)."""
-    _no_grad("moe_gather", x=x, out=out)
+    _no_grad("moe_gather", x, out)
     if x.dim() != 2:
         raise ValueError(f"x must be [T, H], got shape {tuple(x.shape)}")
-    dev, H = x.device, x.shape[1]
-    code = _row_dtype(x.dtype, "x")
-    px = _rows(x, "x", (route.T, H), dev)
-    _same_device(dev, route=route.pos)
+    dev, dtype, H, pos = x.device, x.dtype, x.shape[1], route.pos
+    (T, k), code = pos.shape, _row_dtype(x.dtype, "x")
+    px = _rows(x, "x", T, H, dev, dtype)
+    _on(dev, pos, "route")
     if out is None:
-        out = torch.empty((route.rows, H), dtype=x.dtype, device=dev)
-    po = _rows(out, "out", (route.rows, H), dev, x.dtype)
-    _run("moe_gather", dev, px, code, route.pos.data_ptr(), route.T, route.top_k, route.rows, H, po)
+        out = torch.empty((T * k, H), dtype=dtype, device=dev)
+    po = _rows(out, "out", T * k, H, dev, dtype)
+    _run("moe_gather", dev, px, code, pos.data_ptr(), T, k, T * k, H, po)
     return out
 
 
@@ -122,19 +116,18 @@ def moe_combine(ys: torch.Tensor, route: MoeRoute, weights: torch.Tensor | None 
                 out: torch.Tensor | None = None) -> torch.Tensor:
     """y[t] = sum_j weights[t][j] ys[pos[t][j]] ([T][H]) over the slots of each
     token that have a row; weights: fp32 [T][top_k], or None for ones."""
-    _no_grad("moe_combine", ys=ys, weights=weights, out=out)
+    _no_grad("moe_combine", ys, weights, out)
     if ys.dim() != 2:
         raise ValueError(f"ys must be [rows, H], got shape {tuple(ys.shape)}")
-    dev, H = ys.device, ys.shape[1]
-    code = _row_dtype(ys.dtype, "ys")
-    ps = _rows(ys, "ys", (route.rows, H), dev)
-    _same_device(dev, route=route.pos)
-    pw = _weights(weights, route, dev)
+    dev, dtype, H, pos = ys.device, ys.dtype, ys.shape[1], route.pos
+    (T, k), code = pos.shape, _row_dtype(ys.dtype, "ys")
+    ps = _rows(ys, "ys", T * k, H, dev, dtype)
+    _on(dev, pos, "route")
+    pw = None if weights is None else _rows(weights, "weights", T, k, dev, torch.float32)
     if out is None:
-        out = torch.empty((route.T, H), dtype=ys.dtype, device=dev)
-    po = _rows(out, "out", (route.T, H), dev, ys.dtype)
-    _run("moe_combine", dev, ps, code, pw, route.pos.data_ptr(), route.T, route.top_k, route.rows,
-         H, po)
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+    po = _rows(out, "out", T, H, dev, dtype)
+    _run("moe_combine", dev, ps, code, pw, pos.data_ptr(), T, k, T * k, H, po)
     return out
 
 
@@ -149,19 +142,18 @@ def moe_combine_grad(dy: torch.Tensor, ys: torch.Tensor, route: MoeRoute,
     """The gradients (dys [route.rows][H], dweights fp32 [T][top_k]) of
     moe_combine, given dy [T][H] and its inputs.  Rows of dys that no slot has
     are left as they were (undefined where dys is None)."""
-    _no_grad("moe_combine_grad", dy=dy, ys=ys, weights=weights, dys=dys)
+    _no_grad("moe_combine_grad", dy, ys, weights, dys)
     if dy.dim() != 2:
         raise ValueError(f"dy must be [T, H], got shape {tuple(dy.shape)}")
-    dev, H = dy.device, dy.shape[1]
-    code = _row_dtype(dy.dtype, "dy")
-    pg = _rows(dy, "dy", (route.T, H), dev)
-    ps = _rows(ys, "ys", (route.rows, H), dev, dy.dtype)
-    _same_device(dev, route=route.pos)
-    pw = _weights(weights, route, dev)
+    dev, dtype, H, pos = dy.device, dy.dtype, dy.shape[1], route.pos
+    (T, k), code = pos.shape, _row_dtype(dy.dtype, "dy")
+    pg = _rows(dy, "dy", T, H, dev, dtype)
+    ps = _rows(ys, "ys", T * k, H, dev, dtype)
+    _on(dev, pos, "route")
+    pw = None if weights is None else _rows(weights, "weights", T, k, dev, torch.float32)
     if dys is None:
-        dys = torch.empty((route.rows, H), dtype=dy.dtype, device=dev)
-    po = _rows(dys, "dys", (route.rows, H), dev, dy.dtype)
-    dweights = torch.empty((route.T, route.top_k), dtype=torch.float32, device=dev)
-    _run("moe_combine_grad", dev, pg, ps, code, pw, route.pos.data_ptr(), route.T, route.top_k,
-         route.rows, H, po, dweights.data_ptr())
+        dys = torch.empty((T * k, H), dtype=dtype, device=dev)
+    po = _rows(dys, "dys", T * k, H, dev, dtype)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _run("moe_combine_grad", dev, pg, ps, code, pw, pos.data_ptr(), T, k, T * k, H, po, dweights.data_ptr())
     return dys, dweights

@@ -41,6 +41,14 @@ struct Product {
   int top_k, experts;
 };
 
+template <int DT>
+__device__ __forceinline__ void store_one(void* y, int64_t i, float v) {
+  if constexpr (DT == INT8_FP32)
+    static_cast<float*>(y)[i] = v;
+  else
+    static_cast<uint16_t*>(y)[i] = to_half_bits<DT>(v);
+}
+
 // Where a tile of rows lies: rows [first, end) of y, of expert `expert`
 // (end <= first: no tile).
 struct RowTile {
@@ -209,6 +217,9 @@ __device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, i
 // ---------------------------------------------------------------------------
 constexpr int kTileThreads = 256;
 constexpr int kDepth = 128;  // bytes of K per step
+// Offset of a load that is to give zeros: past every range, whatever row offset
+// is added.  (Row offsets go into the vector offset too: the range is checked
+// against that alone once a scalar offset passes it.)
 constexpr uint32_t kNever = 0x80000000u;
 
 // In the order of the program: one vector-memory load or LDS instruction
@@ -216,6 +227,16 @@ constexpr uint32_t kNever = 0x80000000u;
 constexpr int kSchedMfma = 0x8, kSchedLoad = 0x20, kSchedRead = 0x100;
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
+__device__ __forceinline__ uint32_t lds_address(void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((LdsPtr)p));
+}
+// The four words of rsrc(p, bytes), one value per wave.
+__device__ __forceinline__ i32x4 range_words(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p);
+  return i32x4{__builtin_amdgcn_readfirstlane(static_cast<int>(a)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32 & 0xFFFF)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>(p ? bytes : 0)), 0x00020000};
+}
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
 template <int DT, bool GROUPED, int BM, int BN>
@@ -263,11 +284,11 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
     const uint32_t v = in ? voff + k : kNever;
     const LdsPtr to = (LdsPtr)(buf + (32 * i + 8 * wave) * kDepth);
     if (i < LN)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, v, 32 * i * pitch, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, v + 32 * i * pitch, 0, 0, 0);
     else if constexpr (GROUPED)
       __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v, 32 * (i - LN) * pitch, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v + 32 * (i - LN) * pitch, 0, 0, 0);
   };
 
   // --- LDS to the matrix cores
@@ -290,7 +311,21 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
       for (int j = 0; j < TM; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][i], fx[set][j], acc[i][j], 0, 0, 0);
   };
-  constexpr int kMoves = LN + LM, kFirst = kMoves / 2;
+  // The step after the next one's loads may start when the barrier has freed its
+  // buffer: they are spread over the parts 3, 0 and 1, one to two or more matrix
+  // instructions, since four waves' loads in a row would hold up the issue.
+  constexpr int kMoves = LN + LM, kThree = (kMoves + 2) / 3, kZero = (kMoves - kThree + 1) / 2;
+  constexpr int kOne = kMoves - kThree - kZero;
+  auto order = [&](int loads) {
+#pragma unroll
+    for (int i = 0; i < TN + TM; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (i < loads) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   // one step: `now` holds this step's rows, `next` the next one's
   auto step = [&](int8_t* now, int8_t* next, int k) {
 #pragma unroll
@@ -298,29 +333,21 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
       fetch((part + 1) & 1, now, part + 1);
       if (part == 0) {
 #pragma unroll
-        for (int i = kFirst; i < kMoves; ++i) load(next, i, (k + 1) * kDepth);
+        for (int i = kThree; i < kThree + kZero; ++i) load(next, i, (k + 1) * kDepth);
+      }
+      if (part == 1) {
+#pragma unroll
+        for (int i = kThree + kZero; i < kMoves; ++i) load(next, i, (k + 1) * kDepth);
       }
       multiply(part & 1);
-#pragma unroll
-      for (int i = 0; i < TN + TM; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-        if (part == 0 && i < kMoves - kFirst) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      order(part == 0 ? kZero : part == 1 ? kOne : 0);
     }
     __syncthreads();
     fetch(0, next, 0);
 #pragma unroll
-    for (int i = 0; i < kFirst; ++i) load(now, i, (k + 2) * kDepth);
+    for (int i = 0; i < kThree; ++i) load(now, i, (k + 2) * kDepth);
     multiply(1);
-#pragma unroll
-    for (int i = 0; i < TN + TM; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-      if (i < kFirst) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    order(kThree);
   };
 
   const int steps = (pitch + kDepth - 1) / kDepth;
@@ -329,7 +356,7 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
     for (int i = 0; i < kMoves; ++i) load(s_a, i, 0);
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kFirst; ++i) load(s_b, i, kDepth);
+    for (int i = 0; i < kThree; ++i) load(s_b, i, kDepth);
     fetch(0, s_a, 0);
     for (int k = 0; k < steps; k += 2) {  // with an odd number the last step is one of zeros
       step(s_a, s_b, k);
@@ -340,23 +367,6 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
 
   write_tile<DT, GROUPED, TM, TN, kOutChannels>(p, t, n0 + wn, t.first + wm, acc, s_out + wave * 32 * kOutChannels * kB);
 }
-
-// ---------------------------------------------------------------------------
-// Few rows: up to 16 tokens.  The eight waves of a workgroup share K, and each
-// holds the codes of its range, of all the tokens, in registers while the
-// workgroup goes through its share of the channels, 16 at a time: the weights go
-// from memory straight to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g
-// holds A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]),
-// each byte read once, a whole tile of them in flight while the one before is
-// used.  The waves' int32 sums meet in LDS.
-//
-// XT is the tokens' type.  Codes (kCodes) are read as they are; other types are
-// quantized on the way: first the tokens' peaks (a wave's lanes read what they
-// will encode; the waves' peaks meet in LDS), then the codes.
-// ---------------------------------------------------------------------------
-constexpr int kRowWaves = 8;
-constexpr int kRowThreads = 64 * kRowWaves;
-constexpr int kCodes = 3;
 
 template <int DT>
 __device__ __forceinline__ void store_four(void* y, int64_t i, int left, const float (&f)[4]) {
@@ -373,18 +383,168 @@ __device__ __forceinline__ void store_four(void* y, int64_t i, int left, const f
   }
 #pragma unroll
   for (int e = 0; e < 3; ++e)
-    if (e < left) {
-      if constexpr (DT == INT8_FP32)
-        static_cast<float*>(y)[i + e] = f[e];
-      else
-        static_cast<uint16_t*>(y)[i + e] = to_half_bits<DT>(f[e]);
-    }
+    if (e < left) store_one<DT>(y, i + e, f[e]);
 }
 
-template <int XT, int DT, bool GROUPED, int UNITS>
-__global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Product p, const void* x, int K) {
+// ---------------------------------------------------------------------------
+// Single tokens: one or two.  No matrix instructions: a wave takes whole rows of
+// weights, two at a time, 1024 contiguous bytes to a load, and multiplies them
+// by the tokens' codes, which its workgroup keeps in LDS, with v_dot4_i32_i8;
+// the lanes' sums are added at a row's end.  The weights of the next two rows
+// are asked for as soon as the registers are free.
+//
+// XT is the tokens' type.  Codes (kCodes) are copied to LDS; tokens of other
+// types are quantized on the way there, after the workgroup's first weights have
+// been asked for.
+// ---------------------------------------------------------------------------
+constexpr int kDotWaves = 8;
+constexpr int kDotThreads = 64 * kDotWaves;
+constexpr int kDotRows = 2 * kDotWaves;  // of weights, of a workgroup at a time
+constexpr int kCodes = 3;
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+
+// The sum over the 64 lanes, in all of them.
+__device__ __forceinline__ int wave_total(int v) {
+  v += dpp<0xB1>(v);   // the neighbour (quad permutation 1 0 3 2)
+  v += dpp<0x4E>(v);   // the other pair of the four (2 3 0 1)
+  v += dpp<0x141>(v);  // the other four of the eight (half mirror)
+  v += dpp<0x140>(v);  // the other eight of the sixteen (mirror)
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = a[0] + a[1];
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return b[0] + b[1];
+}
+
+// BLOCKS: 1024-byte blocks of a row, most; MT: tokens, most.
+template <int XT, int DT, int MT, int BLOCKS>
+__global__ __launch_bounds__(kDotThreads, 4) void dot_kernel(Product p, const void* x, int K) {
+  constexpr int kLds = BLOCKS * 1024;  // of a token's codes
+  __shared__ __attribute__((aligned(16))) int8_t s_x[MT * kLds];
+  __shared__ uint32_t s_peak[kDotWaves][MT];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int pitch = static_cast<int>(p.pitch), M = static_cast<int>(p.M);
+  const int blocks = (pitch + 1023) / 1024;
+  const uint32_t tiles = static_cast<uint32_t>((p.N + kDotRows - 1) / kDotRows);
+  i32x4 w[2][BLOCKS];
+  auto range = [&](uint32_t tile) {
+    const int64_t n0 = static_cast<int64_t>(tile) * kDotRows;
+    const int64_t rows = tile < tiles ? min(int64_t(kDotRows), p.N - n0) : 0;  // no rows: zeros
+    return rsrc(p.wq + n0 * p.pitch, static_cast<uint32_t>(rows * p.pitch));
+  };
+  const uint32_t row0 = static_cast<uint32_t>(2 * wave * pitch + 16 * lane);
+  auto load = [&](__amdgpu_buffer_rsrc_t rw, int b) {
+    // a row's last block ends in the next row, against zeros in LDS
+    const uint32_t at = b < blocks ? row0 + 1024 * b : kNever;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      w[r][b] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, at + r * pitch, 0, 0));
+  };
+  const auto first = range(blockIdx.x);
+#pragma unroll
+  for (int b = 0; b < BLOCKS; ++b) load(first, b);
+
+  float xs[MT];
+  if constexpr (XT == kCodes) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m >= M) continue;
+      xs[m] = p.xs[m];
+      for (int at = 16 * threadIdx.x; at < 1024 * blocks; at += 16 * kDotThreads) {
+        i32x4 v = {};
+        if (at < pitch) v = *reinterpret_cast<const i32x4*>(p.xq + m * p.pitch + at);
+        // bytes past K may hold anything where the weights' are zero, but those
+        // past the pitch meet the next row's weights
+        *reinterpret_cast<i32x4*>(s_x + m * kLds + at) = v;
+      }
+    }
+  } else {
+    constexpr int kPieces = (BLOCKS * 128 + kDotThreads - 1) / kDotThreads;  // of a thread, to a row
+    auto row = [&](int m) { return static_cast<const char*>(x) + static_cast<int64_t>(m) * K * dtype_bytes(XT); };
+    uint32_t peak[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      peak[m] = 0;
+      if (m >= M) continue;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = 8 * (threadIdx.x + i * kDotThreads);
+        if (at < K) peak[m] = max(peak[m], piece_peak<XT>(load_piece<XT>(row(m), at, K)));
+      }
+      peak[m] = wave_max(peak[m]);
+      if (lane == 0) s_peak[wave][m] = peak[m];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      if (m >= M) continue;
+#pragma unroll
+      for (int v = 0; v < kDotWaves; ++v) peak[m] = max(peak[m], s_peak[v][m]);
+      const RowScale scale = row_scale(peak[m]);
+      xs[m] = scale.scale;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = 8 * (threadIdx.x + i * kDotThreads);
+        if (at < 1024 * blocks)
+          *reinterpret_cast<uint2*>(s_x + m * kLds + at) =
+              at < K ? encode_piece<XT>(load_piece<XT>(row(m), at, K), scale) : make_uint2(0u, 0u);
+      }
+    }
+  }
+  __syncthreads();
+
+  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int acc[2][MT] = {};
+    // few codes may stay in registers from tile to tile; more would spill
+    if constexpr (MT * BLOCKS > 8) asm volatile("" ::: "memory");
+    const auto next = range(tile + gridDim.x);
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) {
+      // blocks past the row: zeros against whatever LDS holds
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const i32x4 c = *reinterpret_cast<const i32x4*>(s_x + m * kLds + 1024 * b + 16 * lane);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[r][m] = __builtin_amdgcn_sdot4(w[r][b][e], c[e], acc[r][m], false);
+      }
+      // the products first, then the load into the registers that they free: the
+      // other way round the compiler takes twice the registers
+#pragma unroll
+      for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(acc[0][m]), "+v"(acc[1][m]));
+      __builtin_amdgcn_sched_barrier(0);
+      load(next, b);
+    }
+    const int64_t n = static_cast<int64_t>(tile) * kDotRows + 2 * wave;
+    const float ws0 = n < p.N ? p.ws[n] : 0.0f, ws1 = n + 1 < p.N ? p.ws[n + 1] : 0.0f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const float f0 = static_cast<float>(wave_total(acc[0][m])) * xs[m] * ws0;
+      const float f1 = static_cast<float>(wave_total(acc[1][m])) * xs[m] * ws1;
+      if (m < M && lane < 2 && n + lane < p.N) store_one<DT>(p.y, m * p.N + n + lane, lane ? f1 : f0);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: up to 16 tokens.  The eight waves of a workgroup share K, and each
+// holds the codes of its share, of all the tokens, in registers while the
+// workgroup goes through its channels, 16 at a time: the weights go from memory
+// straight to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g holds
+// A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]), each
+// byte read once, a whole tile of them in flight while the one before is used.
+// The waves' int32 sums meet in LDS.
+// ---------------------------------------------------------------------------
+constexpr int kRowWaves = 8;
+constexpr int kRowThreads = 64 * kRowWaves;
+
+template <int DT, bool GROUPED, int UNITS>
+__global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Product p) {
   __shared__ i32x4 s_sum[2][kRowWaves][64];
-  __shared__ uint32_t s_peak[kRowWaves][16];
   const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16);
   RowTile t = {0, p.M, 0};
   if constexpr (GROUPED) {
@@ -394,9 +554,9 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int pitch = static_cast<int>(p.pitch);
   const int inside = (lane >> 4) * 16;
-  // the wave's range, in units of 64 bytes
-  const int units = pitch / 64, each = (units + kRowWaves - 1) / kRowWaves;
-  const int first = wave * each, end = min(units, first + each);
+  // the wave's units of 64 bytes: pairs, so that two loads read whole lines
+  const int units = pitch / 64;
+  auto unit = [&](int u) { return 2 * wave + 2 * kRowWaves * (u >> 1) + (u & 1); };
   const uint32_t voff = static_cast<uint32_t>((lane & 15) * pitch + inside);
   const int8_t* w0 = p.wq + t.expert * p.N * p.pitch;
   i32x4 w[UNITS];
@@ -406,56 +566,18 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
 #pragma unroll
     for (int u = 0; u < UNITS; ++u)
       w[u] = __builtin_bit_cast(
-          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, first + u < end ? voff + 64 * (first + u) : kNever, 0, 0));
+          i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, unit(u) < units ? voff + 64 * unit(u) : kNever, 0, 0));
   };
   load(blockIdx.x);
 
   const int64_t m = t.first + (lane & 15);
   const int64_t src = source_row<GROUPED>(p, min(m, t.end - 1));
-  float xs = 0.0f;
+  const int8_t* xr = (src >= 0 ? p.xq + src * p.pitch : w0) + inside;  // any row that may be read
+  const float xs = src >= 0 ? p.xs[src] : 0.0f;
   i32x4 codes[UNITS];
-  if constexpr (XT == kCodes) {
-    const int8_t* xr = (src >= 0 ? p.xq + src * p.pitch : w0) + inside;  // any row that may be read
-    if (src >= 0) xs = p.xs[src];
-    // past the wave's range the weights are zeros
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-      codes[u] = *reinterpret_cast<const i32x4*>(xr + (first + u < end ? 64 * (first + u) : 0));
-  } else {
-    // K is a multiple of 16, so a lane's 16 elements of a unit all exist or none
-    // does; in place of the latter the row's first ones, which change no peak
-    const char* xr = static_cast<const char*>(x) + src * K * dtype_bytes(XT);
-    constexpr bool kHold = UNITS * dtype_bytes(XT) <= 8;  // in registers from the first reading to the second
-    Piece<XT> held[kHold ? UNITS : 1][2];
-    auto read = [&](int u, int h) {
-      const int k = 64 * (first + u) + inside;
-      return whole_piece<XT>(xr, (first + u < end && k < K ? k : 0) + 8 * h);
-    };
-    uint32_t peak = 0;
-    if constexpr (kHold) {
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) held[u][0] = read(u, 0), held[u][1] = read(u, 1);
-    }
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) peak = max(peak, piece_peak<XT>(kHold ? held[kHold ? u : 0][h] : read(u, h)));
-    peak = max(peak, static_cast<uint32_t>(__shfl_xor(static_cast<int>(peak), 16)));
-    peak = max(peak, static_cast<uint32_t>(__shfl_xor(static_cast<int>(peak), 32)));
-    if (lane < 16) s_peak[wave][lane] = peak;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < kRowWaves; ++v) peak = max(peak, s_peak[v][lane & 15]);
-    const RowScale scale = row_scale(peak);
-    xs = scale.scale;
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-      const uint2 lo = encode_piece<XT>(kHold ? held[kHold ? u : 0][0] : read(u, 0), scale);
-      const uint2 hi = encode_piece<XT>(kHold ? held[kHold ? u : 0][1] : read(u, 1), scale);
-      codes[u] = i32x4{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(hi.x), static_cast<int>(hi.y)};
-      if (64 * (first + u) + inside >= K) codes[u] = i32x4{0, 0, 0, 0};  // the row's padding
-    }
-  }
+  for (int u = 0; u < UNITS; ++u)  // past the row the weights are zeros
+    codes[u] = *reinterpret_cast<const i32x4*>(xr + (unit(u) < units ? 64 * unit(u) : 0));
 
   int turn = 0;
   for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
@@ -483,26 +605,37 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
 }
 
 // ---------------------------------------------------------------------------
-// Small tiles: WM x WN x WK waves, each with one or more 32 x 32 tiles (TM x
-// TN); the WK waves of a tile share each step's K, 128 / WK bytes each.  STAGES
-// buffers: the rows of a step are asked for STAGES - 1 steps ahead, and a wave
-// waits only for those of the step that it is about to use.  Several workgroups
-// share a compute unit, so nothing is done by hand within a step.
+// Small tiles: WM x WN x WK waves, each with TM x TN tiles of 32 x 32; the WK
+// waves of a tile share each step's K, 128 / WK bytes each.  Few steps are long
+// enough to hide anything, so the chain of a step is kept short: kStages buffers
+// in LDS, each asked for kStages steps ahead; operands read from LDS a step ahead
+// of the matrix instructions that use them; one barrier, at which a wave waits
+// for the next step's rows only.
 // ---------------------------------------------------------------------------
+// Loads of 16 bytes a lane from memory to LDS, lane l's to byte 16 l from `to` on
+// (one address per wave).  The builtins for these would do, but for the waits: the
+// compiler puts one for all of them before a loop's first LDS read, every time
+// round.  Nothing lands in a register, and arrive() in stream_kernel does all the
+// waiting.  (m0 holds the LDS address; nothing else in that kernel uses it.)
+__device__ __forceinline__ void lds_load(uint32_t to, i32x4 range, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at), "s"(range)
+               : "memory");
+}
+__device__ __forceinline__ void lds_load(uint32_t to, const int8_t* from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+}
+
 template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES>
 __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   constexpr int kRows = kThreads / 8;                         // rows that a load of all threads fills
   constexpr int LM = BM / kRows, LN = BN / kRows, kLoads = LM + LN;
-  static_assert(LM * kRows == BM && LN * kRows == BN && STAGES >= 2 && STAGES <= 4);
+  static_assert(LM * kRows == BM && LN * kRows == BN);
   constexpr int kB = dtype_bytes(DT);
   constexpr int kStage = (BM + BN) * kDepth;
   static_assert(WK == 1 || (TM == 1 && TN == 1));
-  // buffers that the compiler can tell apart: reads of one do not wait for the
-  // loads into another
-  __shared__ __attribute__((aligned(256))) int8_t s_0[kStage], s_1[kStage], s_2[STAGES > 2 ? kStage : 16],
-      s_3[STAGES > 3 ? kStage : 16];
+  __shared__ __attribute__((aligned(256))) int8_t s_rows[STAGES][kStage];
   __shared__ __attribute__((aligned(256))) int8_t s_out[WM * WN * 32 * 32 * TN * kB];
   __shared__ __attribute__((aligned(256))) i32x4 s_meet[WK > 1 ? (WK - 1) * WM * WN * 256 : 1];
 
@@ -520,9 +653,9 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
   const int pitch = static_cast<int>(p.pitch);
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
-  const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
-  const auto rx = rsrc(GROUPED ? nullptr : p.xq + t.first * p.pitch,
-                       static_cast<uint32_t>((t.end - t.first) * p.pitch));
+  const i32x4 rw = range_words(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
+  const i32x4 rx = range_words(GROUPED ? nullptr : p.xq + t.first * p.pitch,
+                               static_cast<uint32_t>((t.end - t.first) * p.pitch));
   const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
   const int8_t* xrow[GROUPED ? LM : 1];
   if constexpr (GROUPED) {
@@ -533,76 +666,77 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
       xrow[i] = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
     }
   }
-  auto load = [&](int8_t* buf, int k) {
+  const uint32_t lds0 = lds_address(s_rows[0]) + 8 * wave * kDepth;
+  auto load = [&](int stage, int k) {
     const bool in = k + chunk < pitch;
-    const uint32_t v = in ? voff + k : kNever;
+    const uint32_t v = in ? voff + k : kNever, to = lds0 + stage * kStage;
 #pragma unroll
-    for (int i = 0; i < LN; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsPtr)(buf + (kRows * i + 8 * wave) * kDepth), 16, v,
-                                               kRows * i * pitch, 0, 0);
+    for (int i = 0; i < LN; ++i) lds_load(to + kRows * i * kDepth, rw, v + kRows * i * pitch);
 #pragma unroll
     for (int i = 0; i < LM; ++i) {
-      const LdsPtr to = (LdsPtr)(buf + (BN + kRows * i + 8 * wave) * kDepth);
       if constexpr (GROUPED)
-        __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[i] + (in ? k + chunk : 0)), to, 16, 0, 0);
+        lds_load(to + (BN + kRows * i) * kDepth, xrow[i] + (in ? k + chunk : 0));
       else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v, kRows * i * pitch, 0, 0);
+        lds_load(to + (BN + kRows * i) * kDepth, rx, v + kRows * i * pitch);
     }
   };
 
   const int wk = wave % WK, wn = wave / WK % WN * (32 * TN), wm = wave / (WK * WN) * (32 * TM);
   constexpr int kParts = 4 / WK;
   i32x16 acc[TN][TM] = {};
-  auto step = [&](const int8_t* now, int8_t* free, int k) {
-    // this step's rows are there when no more than the later steps' loads are
-    // out; past the barrier that holds for all waves, and all are through with
-    // the step before
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
-    load(free, k + (STAGES - 1) * kDepth);
-    i32x4 fw[kParts][TN], fx[kParts][TM];
+  i32x4 fw[2][kParts][TN], fx[2][kParts][TM];
+  auto fetch = [&](int set, int stage) {
+    const int8_t* buf = s_rows[stage];
 #pragma unroll
     for (int part = 0; part < kParts; ++part) {
       const int at = (lane & 31) * kDepth + (((2 * (wk * kParts + part) + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
 #pragma unroll
-      for (int i = 0; i < TN; ++i) fw[part][i] = *reinterpret_cast<const i32x4*>(now + (wn + 32 * i) * kDepth + at);
+      for (int i = 0; i < TN; ++i) fw[set][part][i] = *reinterpret_cast<const i32x4*>(buf + (wn + 32 * i) * kDepth + at);
 #pragma unroll
       for (int i = 0; i < TM; ++i)
-        fx[part][i] = *reinterpret_cast<const i32x4*>(now + (BN + wm + 32 * i) * kDepth + at);
+        fx[set][part][i] = *reinterpret_cast<const i32x4*>(buf + (BN + wm + 32 * i) * kDepth + at);
     }
+  };
+  // Waits until this wave's operands have been read and its loads of the next
+  // stage have landed; past the barrier both hold for all waves.
+  auto arrive = [] {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0), in a form that the compiler counts with
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((STAGES - 2) * kLoads) : "memory");
+  };
+  auto step = [&](int set, int stage, int k) {
+    arrive();
+    load(stage, k + STAGES * kDepth);
+    fetch(set ^ 1, (stage + 1) % STAGES);
+    __builtin_amdgcn_sched_barrier(0);  // the reads first: the products are of the step before
 #pragma unroll
     for (int part = 0; part < kParts; ++part)
 #pragma unroll
       for (int i = 0; i < TN; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[part][i], fx[part][j], acc[i][j], 0, 0, 0);
+          acc[i][j] =
+              __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][part][i], fx[set][part][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
   };
+  static_assert(STAGES % 2 == 0, "the operand sets alternate with the stages");
   if (pitch > 0) {
-    load(s_0, 0);
-    if constexpr (STAGES > 2) load(s_1, kDepth);
-    if constexpr (STAGES > 3) load(s_2, 2 * kDepth);
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) load(i, i * kDepth);
+    arrive();
+    load(STAGES - 1, (STAGES - 1) * kDepth);
+    fetch(0, 0);
     for (int k = 0; k < pitch;) {
-      // past the last step the rows are zeros
-      if constexpr (STAGES == 2) {
-        step(s_0, s_1, k), step(s_1, s_0, k + kDepth);
-      } else if constexpr (STAGES == 3) {
-        step(s_0, s_2, k);
+      // the rows of a step past the last are zeros
+#pragma unroll
+      for (int i = 0; i < STAGES; ++i) {
+        step(i & 1, i, k);
         if ((k += kDepth) >= pitch) break;
-        step(s_1, s_0, k);
-        if ((k += kDepth) >= pitch) break;
-        step(s_2, s_1, k);
-      } else {
-        step(s_0, s_3, k);
-        if ((k += kDepth) >= pitch) break;
-        step(s_1, s_0, k);
-        if ((k += kDepth) >= pitch) break;
-        step(s_2, s_1, k);
-        if ((k += kDepth) >= pitch) break;
-        step(s_3, s_2, k);
       }
-      k += kDepth;
     }
-  }  if constexpr (WK > 1) {
+    // nothing may be on its way to LDS when the workgroup ends
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
+  if constexpr (WK > 1) {
     // the tile's other waves hand their sums to the first
     const int slot = (wave / WK) * (WK - 1) - 1;
     if (wk > 0)
@@ -666,9 +800,8 @@ nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
 constexpr int64_t kRowMaxUnits = 22;
 constexpr int64_t kRowMaxPitch = kRowMaxUnits * kRowWaves * 64;
 
-// Few rows: the tokens' codes or, with XT another type, the tokens at x.
-template <int XT, bool GROUPED>
-nf4_status launch_rows(const Product& p, const void* x, int64_t K, int32_t y_dtype, hipStream_t st) {
+template <bool GROUPED>
+nf4_status launch_rows(const Product& p, int32_t y_dtype, hipStream_t st) {
   const int64_t tiles = (p.N + 15) / 16, rows = row_tiles<GROUPED>(p, 16);
   if (rows > 65535) return NF4_EUNSUPPORTED;
   // two workgroups fit a compute unit
@@ -678,29 +811,60 @@ nf4_status launch_rows(const Product& p, const void* x, int64_t K, int32_t y_dty
   with_dtype(y_dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     if (units <= 4)
-      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, 4>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+      hipLaunchKernelGGL((row_kernel<DT, GROUPED, 4>), grid, dim3(kRowThreads), 0, st, p);
     else if (units <= 8)
-      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, 8>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+      hipLaunchKernelGGL((row_kernel<DT, GROUPED, 8>), grid, dim3(kRowThreads), 0, st, p);
     else
-      hipLaunchKernelGGL((row_kernel<XT, DT, GROUPED, kRowMaxUnits>), grid, dim3(kRowThreads), 0, st, p, x, static_cast<int>(K));
+      hipLaunchKernelGGL((row_kernel<DT, GROUPED, kRowMaxUnits>), grid, dim3(kRowThreads), 0, st, p);
   });
   return launch_status();
 }
 
-// Whether int8_linear quantizes on the way.
-bool fuses(int64_t M, int64_t K) { return M <= 16 && K > 0 && K % 16 == 0 && K <= kRowMaxPitch; }
+constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
+
+// Whether the product goes to the single tokens' kernel, which quantizes on the
+// way where it is given values.
+bool single(int64_t M, int64_t K) { return M <= kDotTokens && K > 0 && pitch_of(K) <= kDotBlocks * 1024; }
+
+template <int XT, int DT, int MT>
+void launch_dot_blocks(const Product& p, const void* x, int64_t K, hipStream_t st) {
+  const int64_t tiles = (p.N + kDotRows - 1) / kDotRows, most = 2 * device_cus();
+  const dim3 grid(static_cast<uint32_t>(tiles < most ? tiles : most));
+  if (p.pitch <= 4 * 1024)
+    hipLaunchKernelGGL((dot_kernel<XT, DT, MT, 4>), grid, dim3(kDotThreads), 0, st, p, x, static_cast<int>(K));
+  else if (p.pitch <= 8 * 1024)
+    hipLaunchKernelGGL((dot_kernel<XT, DT, MT, 8>), grid, dim3(kDotThreads), 0, st, p, x, static_cast<int>(K));
+  else
+    hipLaunchKernelGGL((dot_kernel<XT, DT, MT, kDotBlocks>), grid, dim3(kDotThreads), 0, st, p, x,
+                       static_cast<int>(K));
+}
+
+// The tokens' codes (XT = kCodes) or the tokens at x.
+template <int XT>
+nf4_status launch_dot(const Product& p, const void* x, int64_t K, int32_t y_dtype, hipStream_t st) {
+  with_dtype(y_dtype, [&](auto d) {
+    constexpr int DT = decltype(d)::value;
+    if (p.M == 1)
+      launch_dot_blocks<XT, DT, 1>(p, x, K, st);
+    else
+      launch_dot_blocks<XT, DT, kDotTokens>(p, x, K, st);
+  });
+  return launch_status();
+}
 
 template <bool GROUPED>
 nf4_status launch(const Product& p, int32_t y_dtype, hipStream_t st) {
   const int64_t rows = GROUPED ? p.M / p.experts : p.M;
-  if (rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch) return launch_rows<kCodes, GROUPED>(p, nullptr, 0, y_dtype, st);
+  if constexpr (!GROUPED)
+    if (single(p.M, p.pitch)) return launch_dot<kCodes>(p, nullptr, 0, y_dtype, st);
+  if (rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch) return launch_rows<GROUPED>(p, y_dtype, st);
 #ifdef FORCE
   return FORCE;
 #endif
-  if (rows <= 32) return launch_stream<GROUPED, 1, 1, 4, 1, 1, 4>(p, y_dtype, st);
-  if (rows <= 64) return launch_stream<GROUPED, 2, 1, 2, 1, 1, 4>(p, y_dtype, st);
+  if (rows <= 32) return launch_stream<GROUPED, 1, 1, 4, 1, 1, 8>(p, y_dtype, st);
+  if (rows <= 64) return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
   if (rows <= 256) return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
-  if (rows <= 1024) return launch_stream<GROUPED, 2, 2, 1, 2, 2, 3>(p, y_dtype, st);
+  if (rows <= 1024) return launch_stream<GROUPED, 2, 2, 1, 2, 2, 4>(p, y_dtype, st);
   return launch_tiles<GROUPED, 256, 256>(p, y_dtype, st);
 }
 
@@ -740,7 +904,7 @@ nf4_status int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const 
 
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return 0;
-  if (fuses(M, K)) return 0;
+  if (single(M, K)) return 0;
   return codes_bytes(M, K) + (static_cast<size_t>(M) * 4 + 255) / 256 * 256 +
          int8_gemm_workspace_size(M, N, K);
 }
@@ -756,10 +920,10 @@ nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const f
   if (const nf4_status st = check_product(wq, ws, N, K, y, y_dtype)) return st;
   if (M > kMaxDim) return NF4_EUNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  if (fuses(M, K)) {
+  if (single(M, K)) {
     const Product p = {nullptr, nullptr, wq, ws, y, M, N, pitch_of(K), nullptr, nullptr, M, 1, 1};
     nf4_status result = NF4_OK;
-    with_dtype(x_dtype, [&](auto a) { result = launch_rows<decltype(a)::value, false>(p, x, K, y_dtype, st); });
+    with_dtype(x_dtype, [&](auto a) { result = launch_dot<decltype(a)::value>(p, x, K, y_dtype, st); });
     return result;
   }
   if (!workspace || workspace_bytes < int8_linear_workspace_size(M, N, K)) return NF4_EINVAL;
