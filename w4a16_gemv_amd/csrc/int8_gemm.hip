@@ -98,10 +98,10 @@ __device__ __forceinline__ int64_t source_row(const Product& p, int64_t i) {
   return s < p.x_rows ? s : -1;
 }
 
-// Tiles in an order whose neighbours share rows and channels, for the workgroup
-// that the hardware starts as number b: it deals workgroups out to the eight
-// dies in turn, so each die gets a range of its own, and within it bands of
-// kBand row tiles.  False past the last tile.
+// Tiles in an order whose neighbours share rows and channels: bands of kBand row
+// tiles.  The hardware deals workgroups out to the eight dies in turn, and each
+// die gets a range of its own; `at` is the place in the range of workgroup b's
+// die.  False past the last tile.
 constexpr uint32_t kDies = 8;
 constexpr uint32_t kBand = 8;
 
@@ -137,41 +137,43 @@ __device__ __forceinline__ uint32_t count_tiles(const Product& p) {
 
 // Scales a wave's 32 TM tokens from m0 on x 32 TN channels from n0 on and writes
 // them, 32 tokens x CHANNELS at a time through an LDS region of its own, so that
-// whole lines of y are written.  16-byte pieces of an LDS row lie at piece ^ row,
-// so that neither side meets in a bank.
-template <int DT, bool GROUPED, int TM, int TN, int CHANNELS>
-__device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, int64_t n0, int64_t m0,
-                                           const i32x16 (&acc)[TN][TM], int8_t* lds) {
-  constexpr int kB = dtype_bytes(DT), kRow = CHANNELS * kB, kSwap = kRow / 16 - 1;
-  constexpr int kTiles = CHANNELS / 32, kPieces = CHANNELS / 8;  // of eight channels, to a row
+// whole lines of y are written.  Channel(c) gives the scales of channels n0 + c ..
+// n0 + c + 3 (0 past the end), token(j) that of the lane's token of tile j.
+template <int DT, int TM, int TN, int CHANNELS, class Channel, class Token>
+__device__ __forceinline__ void write_tile(const Product& p, int64_t end, int64_t n0, int64_t m0,
+                                           const i32x16 (&acc)[TN][TM], int8_t* lds, Channel&& channel,
+                                           Token&& token) {
+  constexpr int kB = dtype_bytes(DT), kRow = CHANNELS * kB, kTiles = CHANNELS / 32;
+  constexpr int kPieces = CHANNELS / 8;          // of eight channels, to a row
+  constexpr int kChunks = kRow / 16;             // of 16 bytes, to a row
+  // 256 / kRow rows fill the banks; a row's chunks lie at chunk ^ swap(row), so
+  // that neither side meets in a bank
+  auto swap = [](int r) { return r / (16 / kChunks) & (kChunks - 1); };
   const int lane = threadIdx.x & 63;
-  const float* ws = p.ws + t.expert * p.N;
 #pragma unroll
   for (int i0 = 0; i0 < TN; i0 += kTiles) {
     const int64_t n1 = n0 + 32 * i0;
     const int64_t wide = min(p.N - n1, int64_t(CHANNELS));
-    float wscale[kTiles][16];
+    float4 ws[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const int64_t n = n1 + 32 * i + 8 * (c >> 2) + 4 * (lane >> 5) + (c & 3);
-        wscale[i][c] = n < p.N ? ws[n] : 0.0f;
-      }
+      for (int c = 0; c < 4; ++c) ws[i][c] = channel(32 * (i0 + i) + 8 * c + 4 * (lane >> 5));
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
-      const int64_t m1 = m0 + 32 * j, m = m1 + (lane & 31);
-      const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
-      const float xs = src >= 0 ? p.xs[src] : 0.0f;
+      const int64_t m1 = m0 + 32 * j;
+      const float xs = token(j);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          float f[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) f[e] = static_cast<float>(acc[i0 + i][j][c + e]) * xs * wscale[i][c + e];
-          const int at = (32 * i + 2 * c + 4 * (lane >> 5)) * kB;
-          int8_t* to = lds + (lane & 31) * kRow + (((at >> 4) ^ (lane & kSwap)) << 4) + (at & 15);
+        for (int c = 0; c < 4; ++c) {
+          const i32x16& v = acc[i0 + i][j];
+          const float f[4] = {static_cast<float>(v[4 * c]) * xs * ws[i][c].x,
+                              static_cast<float>(v[4 * c + 1]) * xs * ws[i][c].y,
+                              static_cast<float>(v[4 * c + 2]) * xs * ws[i][c].z,
+                              static_cast<float>(v[4 * c + 3]) * xs * ws[i][c].w};
+          const int at = (32 * i + 8 * c + 4 * (lane >> 5)) * kB;
+          int8_t* to = lds + (lane & 31) * kRow + (((at >> 4) ^ swap(lane & 31)) << 4) + (at & 15);
           if constexpr (DT == INT8_FP32)
             *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
           else
@@ -181,11 +183,11 @@ __device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, i
 #pragma unroll
       for (int i = lane; i < 32 * kPieces; i += 64) {
         const int r = i / kPieces, at = i % kPieces;
-        if (m1 + r >= t.end || 8 * at >= wide) continue;
+        if (m1 + r >= end || 8 * at >= wide) continue;
         Piece<DT> v;
 #pragma unroll
         for (int h = 0; h < kB / 2; ++h)
-          v.v[h] = *reinterpret_cast<const u32x4*>(lds + r * kRow + (((at * (kB / 2) + h) ^ (r & kSwap)) << 4));
+          v.v[h] = *reinterpret_cast<const u32x4*>(lds + r * kRow + (((at * (kB / 2) + h) ^ swap(r)) << 4));
         store_piece<DT>(static_cast<char*>(p.y) + ((m1 + r) * p.N + n1) * kB, 8 * at, wide, v);
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -194,15 +196,17 @@ __device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, i
 }
 
 // ---------------------------------------------------------------------------
-// Tiles through LDS.  Four waves, 2 x 2, share a tile of BN channels x BM
-// tokens; each holds its quarter in int32 accumulators.  128 bytes of K at a
-// time (a step): the tile's rows go from memory to registers one step ahead,
-// into one of two LDS buffers, and from there to the matrix cores, 32 bytes of
-// K at a time (a part) with the next 32 being read.  One barrier per step: it
-// stands before the last part, whose operands are in registers by then, so
-// that the other buffer's first operands are read while the matrix cores still
-// work.  The order of the instructions is given by hand (sched_group_barrier):
-// left alone the compiler reads operands right before their use.
+// Large tiles: 256 channels x 256 tokens.  Four waves, 2 x 2, each with 128 x 128
+// outputs in int32 accumulators, which takes all of a compute unit's registers
+// and LDS.
+//
+// 128 bytes of K at a time (a step): the tile's rows go from memory straight to
+// one of two LDS buffers, and from there to the matrix cores, 32 bytes of K at a
+// time (a part) with the next 32 being read.  One barrier per step: it stands
+// before the last part, whose operands are in registers by then, so that the
+// other buffer's first operands are read while the matrix cores still work.  The
+// order of the instructions is given by hand (sched_group_barrier): left alone
+// the compiler reads operands right before their use.
 //
 // LDS: two rows of eight 16-byte chunks fill the 64 banks; chunk c of row r is
 // stored at c ^ (r / 2 % 8), so that the sixteen lanes that are served at a
@@ -210,11 +214,13 @@ __device__ __forceinline__ void write_tile(const Product& p, const RowTile& t, i
 // banks once.
 //
 // Rows past the tile's end are zeros or whatever row is at hand (their outputs
-// are not stored); bytes past a row's pitch are zeros on the weights' side.
-// The step past the last is loaded too: zeros that nothing uses.
+// are not stored); bytes past a row's pitch are zeros on the weights' side.  The
+// steps past the last are loaded too: zeros that nothing uses.
 //
-// Out: 32 tokens at a time through LDS, so that whole lines of y are written.
+// Out: 32 tokens at a time through LDS, so that whole lines of y are written.  The
+// scales are asked for at the start: at the end each would be a wait of its own.
 // ---------------------------------------------------------------------------
+constexpr int kTile = 256;
 constexpr int kTileThreads = 256;
 constexpr int kDepth = 128;  // bytes of K per step
 // Offset of a load that is to give zeros: past every range, whatever row offset
@@ -222,8 +228,7 @@ constexpr int kDepth = 128;  // bytes of K per step
 // against that alone once a scalar offset passes it.)
 constexpr uint32_t kNever = 0x80000000u;
 
-// In the order of the program: one vector-memory load or LDS instruction
-// (kind), then `count` matrix instructions.
+// What sched_group_barrier names.
 constexpr int kSchedMfma = 0x8, kSchedLoad = 0x20, kSchedRead = 0x100;
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
@@ -239,86 +244,86 @@ __device__ __forceinline__ i32x4 range_words(const void* p, uint32_t bytes) {
 }
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
-template <int DT, bool GROUPED, int BM, int BN>
-__global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void tile_kernel(Product p) {
-  constexpr int TM = BM / 64, TN = BN / 64;          // 32 x 32 tiles of a wave
-  constexpr int LM = BM / 32, LN = BN / 32;          // 16-byte loads of a thread per step
+template <int DT, bool GROUPED>
+__global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
+  constexpr int T = kTile / 64;        // 32 x 32 tiles of a wave, each way
+  constexpr int L = kTile / 32;        // 16-byte loads of a thread per step and side
   constexpr int kB = dtype_bytes(DT);
   // two buffers that the compiler can tell apart: reads of one do not wait for
   // the loads into the other
-  __shared__ __attribute__((aligned(256))) int8_t s_a[(BM + BN) * kDepth], s_b[(BM + BN) * kDepth];
-  constexpr int kOutChannels = DT == INT8_FP32 && BN == 256 ? BN / 4 : BN / 2;  // of a wave at a time
-  __shared__ __attribute__((aligned(256))) int8_t s_out[4 * 32 * kOutChannels * kB];
+  __shared__ __attribute__((aligned(256))) int8_t s_a[2 * kTile * kDepth], s_b[2 * kTile * kDepth];
+  __shared__ __attribute__((aligned(256))) int8_t s_out[4 * 32 * 128];
+  __shared__ __attribute__((aligned(256))) float s_scale[2][kTile];  // of the channels, of the tokens
 
-  // --- which tile
-  const uint32_t tiles_n = static_cast<uint32_t>((p.N + BN - 1) / BN);
-  uint32_t tiles_m = static_cast<uint32_t>((p.M + BM - 1) / BM);
-  if constexpr (GROUPED) tiles_m = count_tiles<BM>(p);
-  uint32_t tm, tn;
-  if (!place_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
-  RowTile t = {static_cast<int64_t>(tm) * BM, min(p.M, static_cast<int64_t>(tm) * BM + BM), 0};
-  if constexpr (GROUPED) t = find_tile<BM>(p, tm);
-  const int64_t n0 = static_cast<int64_t>(tn) * BN;
-
-  // --- memory to LDS: a wave fills eight rows at a time
+  const uint32_t tiles_n = static_cast<uint32_t>((p.N + kTile - 1) / kTile);
+  uint32_t tiles_m = static_cast<uint32_t>((p.M + kTile - 1) / kTile);
+  if constexpr (GROUPED) tiles_m = count_tiles<kTile>(p);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = 8 * wave + (lane >> 3);
   const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
   const int pitch = static_cast<int>(p.pitch);
+  const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
+
+  uint32_t tm, tn;
+  if (!place_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
+  RowTile t = {static_cast<int64_t>(tm) * kTile, min(p.M, static_cast<int64_t>(tm) * kTile + kTile), 0};
+  if constexpr (GROUPED) t = find_tile<kTile>(p, tm);
+  const int64_t n0 = static_cast<int64_t>(tn) * kTile;
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
-  const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
+  const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(kTile), p.N - n0) * p.pitch));
   const auto rx = rsrc(GROUPED ? nullptr : p.xq + t.first * p.pitch,
                        static_cast<uint32_t>((t.end - t.first) * p.pitch));
-  const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
-  const int8_t* xrow[GROUPED ? LM : 1];
+  const int8_t* xrow[GROUPED ? L : 1];
   if constexpr (GROUPED) {
 #pragma unroll
-    for (int i = 0; i < LM; ++i) {
+    for (int i = 0; i < L; ++i) {
       const int64_t m = t.first + row + 32 * i;
       const int64_t src = m < t.end ? source_row<true>(p, m) : -1;
       xrow[i] = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
     }
   }
+
+  // --- memory to LDS: a wave fills eight rows at a time, the channels' first
   auto load = [&](int8_t* buf, int i, int k) {
     const bool in = k + chunk < pitch;
     const uint32_t v = in ? voff + k : kNever;
     const LdsPtr to = (LdsPtr)(buf + (32 * i + 8 * wave) * kDepth);
-    if (i < LN)
+    if (i < L)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, v + 32 * i * pitch, 0, 0, 0);
     else if constexpr (GROUPED)
-      __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - L : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v + 32 * (i - LN) * pitch, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v + 32 * (i - L) * pitch, 0, 0, 0);
   };
 
   // --- LDS to the matrix cores
-  const int wn = (wave & 1) * (BN / 2), wm = (wave >> 1) * (BM / 2);
-  i32x4 fw[2][TN], fx[2][TM];
+  const int wn = (wave & 1) * (kTile / 2), wm = (wave >> 1) * (kTile / 2);
+  i32x4 fw[2][T], fx[2][T];
   auto fetch = [&](int set, const int8_t* buf, int part) {
     const int at = (lane & 31) * kDepth + (((2 * part + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < T; ++i)
       fw[set][i] = *reinterpret_cast<const i32x4*>(buf + (wn + 32 * i) * kDepth + at);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      fx[set][i] = *reinterpret_cast<const i32x4*>(buf + (BN + wm + 32 * i) * kDepth + at);
+    for (int i = 0; i < T; ++i)
+      fx[set][i] = *reinterpret_cast<const i32x4*>(buf + (kTile + wm + 32 * i) * kDepth + at);
   };
-  i32x16 acc[TN][TM] = {};
+  i32x16 acc[T][T] = {};
   auto multiply = [&](int set) {
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+    for (int i = 0; i < T; ++i)
 #pragma unroll
-      for (int j = 0; j < TM; ++j)
+      for (int j = 0; j < T; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][i], fx[set][j], acc[i][j], 0, 0, 0);
   };
   // The step after the next one's loads may start when the barrier has freed its
   // buffer: they are spread over the parts 3, 0 and 1, one to two or more matrix
   // instructions, since four waves' loads in a row would hold up the issue.
-  constexpr int kMoves = LN + LM, kThree = (kMoves + 2) / 3, kZero = (kMoves - kThree + 1) / 2;
+  constexpr int kMoves = 2 * L, kThree = (kMoves + 2) / 3, kZero = (kMoves - kThree + 1) / 2;
   constexpr int kOne = kMoves - kThree - kZero;
   auto order = [&](int loads) {
 #pragma unroll
-    for (int i = 0; i < TN + TM; ++i) {
+    for (int i = 0; i < 2 * T; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
       if (i < loads) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
@@ -351,21 +356,28 @@ __global__ __launch_bounds__(kTileThreads, BM* BN >= 128 * 128 ? 1 : 2) void til
   };
 
   const int steps = (pitch + kDepth - 1) / kDepth;
-  if (steps > 0) {
 #pragma unroll
-    for (int i = 0; i < kMoves; ++i) load(s_a, i, 0);
-    __syncthreads();
+  for (int i = 0; i < kMoves; ++i) load(s_a, i, 0);
 #pragma unroll
-    for (int i = 0; i < kThree; ++i) load(s_b, i, kDepth);
-    fetch(0, s_a, 0);
-    for (int k = 0; k < steps; k += 2) {  // with an odd number the last step is one of zeros
-      step(s_a, s_b, k);
-      step(s_b, s_a, k + 1);
-    }
-    __syncthreads();
+  for (int i = 0; i < kThree; ++i) load(s_b, i, kDepth);
+  // the scales of channel and token threadIdx.x, for the end
+  const int64_t n = n0 + threadIdx.x, m = t.first + threadIdx.x;
+  const float wscale = n < p.N ? p.ws[t.expert * p.N + n] : 0.0f;
+  const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
+  const float xscale = src >= 0 ? p.xs[src] : 0.0f;
+  __syncthreads();
+  fetch(0, s_a, 0);
+  for (int k = 0; k < steps; k += 2) {  // with an odd number the last step is one of zeros
+    step(s_a, s_b, k);
+    step(s_b, s_a, k + 1);
   }
-
-  write_tile<DT, GROUPED, TM, TN, kOutChannels>(p, t, n0 + wn, t.first + wm, acc, s_out + wave * 32 * kOutChannels * kB);
+  s_scale[0][threadIdx.x] = wscale;
+  s_scale[1][threadIdx.x] = xscale;
+  __syncthreads();
+  write_tile<DT, T, T, 128 / kB>(
+      p, t.end, n0 + wn, t.first + wm, acc, s_out + wave * 32 * 128,
+      [&](int c) { return *reinterpret_cast<const float4*>(&s_scale[0][wn + c]); },
+      [&](int j) { return s_scale[1][wm + 32 * j + (lane & 31)]; });
 }
 
 template <int DT>
@@ -754,7 +766,19 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
         for (int e = 0; e < 4; ++e) acc[0][0][c + e] += o[e];
       }
   }
-  write_tile<DT, GROUPED, TM, TN, 32 * TN>(p, t, n0 + wn, t.first + wm, acc, s_out + wave / WK * (32 * 32 * TN * kB));
+  const float* ws = p.ws + t.expert * p.N;
+  write_tile<DT, TM, TN, 32 * TN>(
+      p, t.end, n0 + wn, t.first + wm, acc, s_out + wave / WK * (32 * 32 * TN * kB),
+      [&](int c) {
+        const int64_t n = n0 + wn + c;
+        return make_float4(n < p.N ? ws[n] : 0.0f, n + 1 < p.N ? ws[n + 1] : 0.0f, n + 2 < p.N ? ws[n + 2] : 0.0f,
+                           n + 3 < p.N ? ws[n + 3] : 0.0f);
+      },
+      [&](int j) {
+        const int64_t m = t.first + wm + 32 * j + (lane & 31);
+        const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
+        return src >= 0 ? p.xs[src] : 0.0f;
+      });
 }
 
 // Tiles of BM rows that p.M rows need at most: every expert ends in at most one
@@ -774,13 +798,12 @@ uint32_t tile_groups(const Product& p, int BM, int BN, int threads) {
   return groups * threads < (int64_t(1) << 32) ? static_cast<uint32_t>(groups) : 0;
 }
 
-template <bool GROUPED, int BM, int BN>
+template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
-  const uint32_t groups = tile_groups<GROUPED>(p, BM, BN, kTileThreads);
-  if (groups == 0) return NF4_EUNSUPPORTED;
+  const uint32_t tiles = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
+  if (tiles == 0) return NF4_EUNSUPPORTED;
   with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, BM, BN>), dim3(groups), dim3(kTileThreads), 0,
-                       st, p);
+    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED>), dim3(tiles), dim3(kTileThreads), 0, st, p);
   });
   return launch_status();
 }
@@ -865,7 +888,7 @@ nf4_status launch(const Product& p, int32_t y_dtype, hipStream_t st) {
   if (rows <= 64) return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
   if (rows <= 256) return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
   if (rows <= 1024) return launch_stream<GROUPED, 2, 2, 1, 2, 2, 4>(p, y_dtype, st);
-  return launch_tiles<GROUPED, 256, 256>(p, y_dtype, st);
+  return launch_tiles<GROUPED>(p, y_dtype, st);
 }
 
 // What the products check alike (the activations apart).
