@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "int8.h"
 #include "int8_product.h"
 #include "nf4_device.h"
@@ -39,6 +41,11 @@ struct Product {
   const int32_t* offsets;
   int64_t x_rows;
   int top_k, experts;
+  // K split over `splits` workgroups of a tile: int32 sums to planes of
+  // M x sums_pitch at `sums` instead of y (dense only)
+  int32_t* sums;
+  int64_t sums_pitch;
+  int splits;
 };
 
 template <int DT>
@@ -664,6 +671,13 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   const int row = 8 * wave + (lane >> 3);
   const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
   const int pitch = static_cast<int>(p.pitch);
+  // this workgroup's range of K, in bytes of a row
+  int begin = 0, end = pitch;
+  if constexpr (!GROUPED) {
+    const int each = ((pitch + kDepth - 1) / kDepth + p.splits - 1) / p.splits * kDepth;
+    begin = min(pitch, static_cast<int>(blockIdx.y) * each);
+    end = min(pitch, begin + each);
+  }
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
   const i32x4 rw = range_words(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
   const i32x4 rx = range_words(GROUPED ? nullptr : p.xq + t.first * p.pitch,
@@ -679,35 +693,29 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
     }
   }
   const uint32_t lds0 = lds_address(s_rows[0]) + 8 * wave * kDepth;
-  auto load = [&](int stage, int k) {
-    const bool in = k + chunk < pitch;
-    const uint32_t v = in ? voff + k : kNever, to = lds0 + stage * kStage;
-#pragma unroll
-    for (int i = 0; i < LN; ++i) lds_load(to + kRows * i * kDepth, rw, v + kRows * i * pitch);
-#pragma unroll
-    for (int i = 0; i < LM; ++i) {
-      if constexpr (GROUPED)
-        lds_load(to + (BN + kRows * i) * kDepth, xrow[i] + (in ? k + chunk : 0));
-      else
-        lds_load(to + (BN + kRows * i) * kDepth, rx, v + kRows * i * pitch);
-    }
+  // load i of a thread for step k / 128: the channels' rows first
+  auto load = [&](int stage, int i, int k) {
+    const bool in = k + chunk < end;
+    const uint32_t v = in ? voff + k : kNever, to = lds0 + stage * kStage + kRows * i * kDepth;
+    if (i < LN)
+      lds_load(to, rw, v + kRows * i * pitch);
+    else if constexpr (GROUPED)
+      lds_load(to, xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0));
+    else
+      lds_load(to, rx, v + kRows * (i - LN) * pitch);
   };
 
   const int wk = wave % WK, wn = wave / WK % WN * (32 * TN), wm = wave / (WK * WN) * (32 * TM);
   constexpr int kParts = 4 / WK;
   i32x16 acc[TN][TM] = {};
-  i32x4 fw[2][kParts][TN], fx[2][kParts][TM];
-  auto fetch = [&](int set, int stage) {
-    const int8_t* buf = s_rows[stage];
-#pragma unroll
-    for (int part = 0; part < kParts; ++part) {
-      const int at = (lane & 31) * kDepth + (((2 * (wk * kParts + part) + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
-#pragma unroll
-      for (int i = 0; i < TN; ++i) fw[set][part][i] = *reinterpret_cast<const i32x4*>(buf + (wn + 32 * i) * kDepth + at);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-        fx[set][part][i] = *reinterpret_cast<const i32x4*>(buf + (BN + wm + 32 * i) * kDepth + at);
-    }
+  constexpr int kReads = kParts * (TN + TM), kProducts = kParts * TN * TM;
+  i32x4 operand[2][kParts][TN + TM];
+  // read i of a step: of each part the channels' operands, then the tokens'
+  auto fetch = [&](int set, int stage, int i) {
+    const int part = i / (TN + TM), q = i % (TN + TM);
+    const int at = (lane & 31) * kDepth + (((2 * (wk * kParts + part) + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
+    const int first = q < TN ? wn + 32 * q : BN + wm + 32 * (q - TN);
+    operand[set][part][q] = *reinterpret_cast<const i32x4*>(s_rows[stage] + first * kDepth + at);
   };
   // Waits until this wave's operands have been read and its loads of the next
   // stage have landed; past the barrier both hold for all waves.
@@ -717,32 +725,42 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   };
   auto step = [&](int set, int stage, int k) {
     arrive();
-    load(stage, k + STAGES * kDepth);
-    fetch(set ^ 1, (stage + 1) % STAGES);
-    __builtin_amdgcn_sched_barrier(0);  // the reads first: the products are of the step before
+    // this step's products with the next one's reads and a later one's loads in
+    // between: in a row, four waves' reads would hold up the issue of the products
+    constexpr int kOthers = kReads + kLoads;
 #pragma unroll
-    for (int part = 0; part < kParts; ++part)
+    for (int m = 0; m < kProducts; ++m) {
+      const int part = m / (TN * TM), i = m / TM % TN, j = m % TM;
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(operand[set][part][i], operand[set][part][TN + j],
+                                                        acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < TN; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-          acc[i][j] =
-              __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][part][i], fx[set][part][j], acc[i][j], 0, 0, 0);
-    __builtin_amdgcn_sched_barrier(0);
+      for (int o = m * kOthers / kProducts; o < (m + 1) * kOthers / kProducts; ++o) {
+        if (o < kReads)
+          fetch(set ^ 1, (stage + 1) % STAGES, o);
+        else
+          load(stage, o - kReads, k + STAGES * kDepth);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   static_assert(STAGES % 2 == 0, "the operand sets alternate with the stages");
-  if (pitch > 0) {
+  if (begin < end) {
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) load(i, i * kDepth);
+    for (int q = 0; q < STAGES - 1; ++q)
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load(q, i, begin + q * kDepth);
     arrive();
-    load(STAGES - 1, (STAGES - 1) * kDepth);
-    fetch(0, 0);
-    for (int k = 0; k < pitch;) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(STAGES - 1, i, begin + (STAGES - 1) * kDepth);
+#pragma unroll
+    for (int i = 0; i < kReads; ++i) fetch(0, 0, i);
+    for (int k = begin; k < end;) {
       // the rows of a step past the last are zeros
 #pragma unroll
       for (int i = 0; i < STAGES; ++i) {
         step(i & 1, i, k);
-        if ((k += kDepth) >= pitch) break;
+        if ((k += kDepth) >= end) break;
       }
     }
     // nothing may be on its way to LDS when the workgroup ends
@@ -766,6 +784,26 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
         for (int e = 0; e < 4; ++e) acc[0][0][c + e] += o[e];
       }
   }
+  if constexpr (!GROUPED) {
+    if (p.splits > 1) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int64_t m = t.first + wm + 32 * j + (lane & 31);
+        if (m >= t.end) continue;
+        int32_t* to = p.sums + (blockIdx.y * p.M + m) * p.sums_pitch;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int c = 0; c < 16; c += 4) {
+            const int64_t n = n0 + wn + 32 * i + 2 * c + 4 * (lane >> 5);
+            if (n < p.sums_pitch)
+              *reinterpret_cast<i32x4*>(to + n) =
+                  i32x4{acc[i][j][c], acc[i][j][c + 1], acc[i][j][c + 2], acc[i][j][c + 3]};
+          }
+      }
+      return;
+    }
+  }
   const float* ws = p.ws + t.expert * p.N;
   write_tile<DT, TM, TN, 32 * TN>(
       p, t.end, n0 + wn, t.first + wm, acc, s_out + wave / WK * (32 * 32 * TN * kB),
@@ -779,6 +817,24 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
         const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
         return src >= 0 ? p.xs[src] : 0.0f;
       });
+}
+
+// The sums of a product whose K was split, four channels of a token to a thread.
+template <int DT>
+__global__ __launch_bounds__(256) void join_kernel(Product p) {
+  const int64_t fours = p.sums_pitch / 4, all = p.M * fours;
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < all; i += gridDim.x * int64_t(256)) {
+    const int64_t m = i / fours, n = i % fours * 4;
+    i32x4 sum = {};
+    for (int v = 0; v < p.splits; ++v)
+      sum += *reinterpret_cast<const i32x4*>(p.sums + (v * p.M + m) * p.sums_pitch + n);
+    const int left = static_cast<int>(min(p.N - n, int64_t(4)));
+    const float xs = p.xs[m];
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = static_cast<float>(sum[e]) * xs * p.ws[n + min(e, left - 1)];
+    store_four<DT>(p.y, m * p.N + n, left, f);
+  }
 }
 
 // Tiles of BM rows that p.M rows need at most: every expert ends in at most one
@@ -814,8 +870,14 @@ nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
   const uint32_t groups = tile_groups<GROUPED>(p, 32 * WM * TM, 32 * WN * TN, kThreads);
   if (groups == 0) return NF4_EUNSUPPORTED;
   with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((stream_kernel<decltype(d)::value, GROUPED, WM, WN, WK, TM, TN, STAGES>), dim3(groups),
-                       dim3(kThreads), 0, st, p);
+    constexpr int DT = decltype(d)::value;
+    hipLaunchKernelGGL((stream_kernel<DT, GROUPED, WM, WN, WK, TM, TN, STAGES>),
+                       dim3(groups, static_cast<uint32_t>(p.splits)), dim3(kThreads), 0, st, p);
+    if (p.splits > 1) {
+      const int64_t blocks = (p.M * (p.sums_pitch / 4) + 255) / 256;
+      hipLaunchKernelGGL((join_kernel<DT>), dim3(static_cast<uint32_t>(blocks < 4096 ? blocks : 4096)), dim3(256),
+                         0, st, p);
+    }
   });
   return launch_status();
 }
@@ -826,7 +888,6 @@ constexpr int64_t kRowMaxPitch = kRowMaxUnits * kRowWaves * 64;
 template <bool GROUPED>
 nf4_status launch_rows(const Product& p, int32_t y_dtype, hipStream_t st) {
   const int64_t tiles = (p.N + 15) / 16, rows = row_tiles<GROUPED>(p, 16);
-  if (rows > 65535) return NF4_EUNSUPPORTED;
   // two workgroups fit a compute unit
   const int64_t most = 2 * device_cus(), share = (most + rows - 1) / rows;
   const dim3 grid(static_cast<uint32_t>(tiles < share ? tiles : share), static_cast<uint32_t>(rows));
@@ -875,20 +936,101 @@ nf4_status launch_dot(const Product& p, const void* x, int64_t K, int32_t y_dtyp
   return launch_status();
 }
 
+// The tiled kernels, and what their steps of 128 bytes of K take (us, measured at
+// 4096 x 4096, 11008 x 4096, 4096 x 11008, 2048 x 2048 and 1024 x 11008 with 32 to
+// 2048 rows): while no compute unit has more than one tile, and for each tile of
+// a compute unit that has several.  Largest tiles load the least per product, but
+// leave compute units idle and take the longest for themselves: 512 x 4096 x 4096
+// takes 35 / 35 / 20 / 17 / 23 / 47 us from the smallest tiles to the largest,
+// 64 x 4096 x 4096 8.5 / 10 / 12 / 14 / 19 / 44, 1024 x 11008 x 4096 176 / 174 / 88
+// / 94 / 70 / 52.
+struct Tiling {
+  int BM, BN;        // tokens, channels
+  float alone, each; // us a step
+  float fixed;       // us a tile that no other's steps hide
+};
+constexpr Tiling kTilings[] = {{32, 32, 0.165f, 0.125f, 0.0f}, {64, 32, 0.19f, 0.25f, 0.0f},
+                               {64, 64, 0.27f, 0.255f, 0.0f},  {128, 64, 0.38f, 0.47f, 0.0f},
+                               {128, 128, 0.55f, 0.69f, 0.0f}, {256, 256, 1.25f, 1.5f, 8.0f}};
+constexpr int kLargest = 5;
+constexpr float kLaunchUs = 3.0f, kJoinUs = 4.5f;
+constexpr int kMaxSplits = 16;
+
+struct Plan {
+  int tiling, splits;
+};
+
+// The tiling with the least time by the figures above, with K split over
+// workgroups where that leaves compute units without a tile (64 x 1024 x 11008:
+// 15 us in one piece, 10 in four) and the workspace has room for the sums.  Rows
+// sorted by expert: every expert with rows ends in a tile that is half full.
 template <bool GROUPED>
-nf4_status launch(const Product& p, int32_t y_dtype, hipStream_t st) {
+Plan plan(const Product& p, size_t room) {
+  const int64_t cus = device_cus();
+  const double steps = static_cast<double>((p.pitch + kDepth - 1) / kDepth);
+  Plan best = {0, 1};
+  double least = 1e30;
+  for (int i = 0; i <= kLargest; ++i) {
+    const Tiling& t = kTilings[i];
+    double rows = static_cast<double>((p.M + t.BM - 1) / t.BM);
+    if (GROUPED)
+      rows = p.M >= int64_t(p.experts) * t.BM / 2 ? static_cast<double>(p.M) / t.BM + 0.5 * p.experts
+                                                  : static_cast<double>(p.M < p.experts ? p.M : p.experts);
+    const double tiles = rows * static_cast<double>((p.N + t.BN - 1) / t.BN);
+    const int most = GROUPED || i == kLargest ? 1 : kMaxSplits;
+    for (int splits = 1; splits <= most; ++splits) {
+      if (splits > 1 && (tiles * splits > cus || p.M * p.sums_pitch * 4 * splits > static_cast<int64_t>(room) ||
+                         steps < 4 * splits))
+        break;
+      const double turns = std::ceil(tiles * splits / cus);
+      const double step = t.alone > turns * t.each ? t.alone : turns * t.each;
+      const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs : 0.0);
+      if (us < least * (splits > 1 ? 0.85 : 1.0)) {
+        least = us;
+        best = {i, splits};
+      }
+    }
+  }
+  return best;
+}
+
+Product dense(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, void* y, int64_t M, int64_t N,
+              int64_t K) {
+  Product p = {};
+  p.xq = xq, p.xs = xs, p.wq = wq, p.ws = ws, p.y = y;
+  p.M = M, p.N = N, p.pitch = pitch_of(K), p.x_rows = M;
+  p.top_k = p.experts = p.splits = 1;
+  p.sums_pitch = (N + 3) / 4 * 4;
+  return p;
+}
+
+// Whether the row kernel takes the product: it reads an expert's weights once for
+// every 16 of its rows.
+template <bool GROUPED>
+bool few(const Product& p) {
   const int64_t rows = GROUPED ? p.M / p.experts : p.M;
+  return rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch && row_tiles<GROUPED>(p, 16) <= 65535;
+}
+
+template <bool GROUPED>
+nf4_status launch(Product p, int32_t y_dtype, void* workspace, size_t room, hipStream_t st) {
   if constexpr (!GROUPED)
     if (single(p.M, p.pitch)) return launch_dot<kCodes>(p, nullptr, 0, y_dtype, st);
-  if (rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch) return launch_rows<GROUPED>(p, y_dtype, st);
+  if (few<GROUPED>(p)) return launch_rows<GROUPED>(p, y_dtype, st);
+  const Plan plan_ = plan<GROUPED>(p, workspace ? room : 0);
+  p.splits = plan_.splits;
+  p.sums = static_cast<int32_t*>(workspace);
 #ifdef FORCE
-  return FORCE;
+  p.splits = 1; return FORCE;
 #endif
-  if (rows <= 32) return launch_stream<GROUPED, 1, 1, 4, 1, 1, 8>(p, y_dtype, st);
-  if (rows <= 64) return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
-  if (rows <= 256) return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
-  if (rows <= 1024) return launch_stream<GROUPED, 2, 2, 1, 2, 2, 4>(p, y_dtype, st);
-  return launch_tiles<GROUPED>(p, y_dtype, st);
+  switch (plan_.tiling) {
+    case 0: return launch_stream<GROUPED, 1, 1, 4, 1, 1, 8>(p, y_dtype, st);
+    case 1: return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
+    case 2: return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
+    case 3: return launch_stream<GROUPED, 2, 2, 1, 2, 1, 4>(p, y_dtype, st);
+    case 4: return launch_stream<GROUPED, 2, 2, 1, 2, 2, 4>(p, y_dtype, st);
+    default: return launch_tiles<GROUPED>(p, y_dtype, st);
+  }
 }
 
 // What the products check alike (the activations apart).
@@ -900,6 +1042,7 @@ nf4_status check_product(const int8_t* wq, const float* ws, int64_t N, int64_t K
   return NF4_OK;
 }
 
+size_t scales_bytes(int64_t M) { return static_cast<size_t>(M * 4 + 255) / 256 * 256; }
 size_t codes_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M * pitch_of(K) + 255) / 256 * 256; }
 
 }  // namespace
@@ -907,29 +1050,30 @@ size_t codes_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M * pitch_
 extern "C" {
 
 size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
-  (void)M, (void)N, (void)K;
-  return 0;
+  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return 0;
+  const Product p = dense(nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K);
+  if (single(M, p.pitch) || few<false>(p)) return 0;
+  const Plan best = plan<false>(p, static_cast<size_t>(1) << 62);
+  return best.splits > 1 ? static_cast<size_t>(M * p.sums_pitch * 4 * best.splits) : 0;
 }
 
 nf4_status int8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws,
                      int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,
                      size_t workspace_bytes, void* stream) {
-  (void)workspace_bytes;
   if (M < 0 || N < 0 || K < 0 || !known_dtype(y_dtype) || !aligned(workspace, 256))
     return NF4_EINVAL;
   if (M == 0 || N == 0) return NF4_OK;
   if (!xs || (K > 0 && !xq) || !aligned(xq, 16) || !aligned(xs, 4)) return NF4_EINVAL;
   if (const nf4_status st = check_product(wq, ws, N, K, y, y_dtype)) return st;
   if (M > kMaxDim) return NF4_EUNSUPPORTED;
-  const Product p = {xq, xs, wq, ws, y, M, N, pitch_of(K), nullptr, nullptr, M, 1, 1};
-  return launch<false>(p, y_dtype, reinterpret_cast<hipStream_t>(stream));
+  return launch<false>(dense(xq, xs, wq, ws, y, M, N, K), y_dtype, workspace, workspace_bytes,
+                       reinterpret_cast<hipStream_t>(stream));
 }
 
 size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return 0;
   if (single(M, K)) return 0;
-  return codes_bytes(M, K) + (static_cast<size_t>(M) * 4 + 255) / 256 * 256 +
-         int8_gemm_workspace_size(M, N, K);
+  return codes_bytes(M, K) + scales_bytes(M) + int8_gemm_workspace_size(M, N, K);
 }
 
 nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const float* ws,
@@ -944,7 +1088,7 @@ nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const f
   if (M > kMaxDim) return NF4_EUNSUPPORTED;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   if (single(M, K)) {
-    const Product p = {nullptr, nullptr, wq, ws, y, M, N, pitch_of(K), nullptr, nullptr, M, 1, 1};
+    const Product p = dense(nullptr, nullptr, wq, ws, y, M, N, K);
     nf4_status result = NF4_OK;
     with_dtype(x_dtype, [&](auto a) { result = launch_dot<decltype(a)::value>(p, x, K, y_dtype, st); });
     return result;
@@ -953,8 +1097,8 @@ nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const f
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(xq + codes_bytes(M, K));
   quantize_launch(x, x_dtype, M, K, xq, xs, st);
-  const Product p = {xq, xs, wq, ws, y, M, N, pitch_of(K), nullptr, nullptr, M, 1, 1};
-  return launch<false>(p, y_dtype, st);
+  const size_t used = codes_bytes(M, K) + scales_bytes(M);
+  return launch<false>(dense(xq, xs, wq, ws, y, M, N, K), y_dtype, xq + used, workspace_bytes - used, st);
 }
 
 nf4_status int8_gemm_grouped(const int8_t* xq, const float* xs, int64_t x_rows,
@@ -971,9 +1115,10 @@ nf4_status int8_gemm_grouped(const int8_t* xq, const float* xs, int64_t x_rows,
   if (!aligned(xq, 16) || !aligned(xs, 4)) return NF4_EINVAL;
   if (const nf4_status st = check_product(wq, ws, N, K, y, y_dtype)) return st;
   if (experts > kMaxExperts || rows > kMaxDim || x_rows > kMaxDim) return NF4_EUNSUPPORTED;
-  const Product p = {xq, xs, wq, ws, y, rows, N, pitch_of(K), order, offsets, x_rows,
-                     order ? top_k : 1, experts};
-  return launch<true>(p, y_dtype, reinterpret_cast<hipStream_t>(stream));
+  Product p = dense(xq, xs, wq, ws, y, rows, N, K);
+  p.order = order, p.offsets = offsets, p.x_rows = x_rows;
+  p.top_k = order ? top_k : 1, p.experts = experts;
+  return launch<true>(p, y_dtype, nullptr, 0, reinterpret_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"
