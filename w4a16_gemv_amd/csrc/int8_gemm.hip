@@ -46,6 +46,7 @@ struct Product {
   int32_t* sums;
   int64_t sums_pitch;
   int splits;
+  uint32_t cus;  // compute units
 };
 
 template <int DT>
@@ -105,26 +106,28 @@ __device__ __forceinline__ int64_t source_row(const Product& p, int64_t i) {
   return s < p.x_rows ? s : -1;
 }
 
-// Tiles in an order whose neighbours share rows and channels: bands of kBand row
-// tiles.  The hardware deals workgroups out to the eight dies in turn, and each
-// die gets a range of its own; `at` is the place in the range of workgroup b's
-// die.  False past the last tile.
+// The hardware deals workgroups out to the eight dies in turn; each die gets a
+// range of its own of the `count` tiles.  False past the last.
 constexpr uint32_t kDies = 8;
+
+__device__ __forceinline__ bool tile_of_group(uint32_t b, uint32_t count, uint32_t& i) {
+  const uint32_t each = (count + kDies - 1) / kDies, at = b / kDies;
+  i = b % kDies * each + at;
+  return at < each && i < count;
+}
+
+// Tiles in an order whose neighbours share rows and channels: bands of kBand row
+// tiles.
 constexpr uint32_t kBand = 8;
 
-__device__ __forceinline__ bool place_tile(uint32_t b, uint32_t tiles_m, uint32_t tiles_n,
-                                           uint32_t& tm, uint32_t& tn) {
-  const uint32_t all = tiles_m * tiles_n;  // < 2^24, by the grid's limit
-  const uint32_t each = (all + kDies - 1) / kDies;
-  const uint32_t at = b / kDies, i = b % kDies * each + at;
-  if (at >= each || i >= all) return false;
+__device__ __forceinline__ void locate_tile(uint32_t i, uint32_t tiles_m, uint32_t tiles_n, uint32_t& tm,
+                                            uint32_t& tn) {
   const uint32_t band = i / (kBand * tiles_n), in = i % (kBand * tiles_n);
   const uint32_t high = min(uint32_t(kBand), tiles_m - band * kBand);
   // the divisions run on the vector unit: back to scalars, so that what follows
   // from them (buffer resources among it) is one value per wave
   tm = __builtin_amdgcn_readfirstlane(band * kBand + in % high);
   tn = __builtin_amdgcn_readfirstlane(in / high);
-  return true;
 }
 
 // Row tiles over all experts.
@@ -203,9 +206,9 @@ __device__ __forceinline__ void write_tile(const Product& p, int64_t end, int64_
 }
 
 // ---------------------------------------------------------------------------
-// Large tiles: 256 channels x 256 tokens.  Four waves, 2 x 2, each with 128 x 128
-// outputs in int32 accumulators, which takes all of a compute unit's registers
-// and LDS.
+// Large tiles: 256 channels x 256 tokens (or 128).  Four waves, 2 x 2, each with 128
+// x 128 outputs in int32 accumulators, which takes all of a compute unit's
+// registers and LDS.
 //
 // 128 bytes of K at a time (a step): the tile's rows go from memory straight to
 // one of two LDS buffers, and from there to the matrix cores, 32 bytes of K at a
@@ -251,39 +254,64 @@ __device__ __forceinline__ i32x4 range_words(const void* p, uint32_t bytes) {
 }
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
-template <int DT, bool GROUPED>
+// How many of `all` tiles are computed whole where the rest, less than half a turn
+// of the compute units, is computed in halves.
+__device__ __host__ __forceinline__ uint32_t whole_tiles(uint32_t all, uint32_t cus) {
+  const uint32_t rest = all % cus;
+  return 2 * rest <= cus ? all - rest : all;
+}
+
+// Which tiles of 256 x 256 a launch computes: all of them in pieces of 64 TM
+// tokens, those that whole_tiles() counts, or the others, in halves.
+enum Share { kAll, kWhole, kHalves };
+
+template <int DT, bool GROUPED, int TM, Share SHARE>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
-  constexpr int T = kTile / 64;        // 32 x 32 tiles of a wave, each way
-  constexpr int L = kTile / 32;        // 16-byte loads of a thread per step and side
+  constexpr int TN = kTile / 64, BM = 64 * TM;     // 32 x 32 tiles of a wave, tokens of a tile
+  constexpr int LN = kTile / 32, LM = BM / 32;     // 16-byte loads of a thread per step
   constexpr int kB = dtype_bytes(DT);
   // two buffers that the compiler can tell apart: reads of one do not wait for
   // the loads into the other
-  __shared__ __attribute__((aligned(256))) int8_t s_a[2 * kTile * kDepth], s_b[2 * kTile * kDepth];
+  __shared__ __attribute__((aligned(256))) int8_t s_a[(kTile + BM) * kDepth], s_b[(kTile + BM) * kDepth];
   __shared__ __attribute__((aligned(256))) int8_t s_out[4 * 32 * 128];
   __shared__ __attribute__((aligned(256))) float s_scale[2][kTile];  // of the channels, of the tokens
 
   const uint32_t tiles_n = static_cast<uint32_t>((p.N + kTile - 1) / kTile);
-  uint32_t tiles_m = static_cast<uint32_t>((p.M + kTile - 1) / kTile);
-  if constexpr (GROUPED) tiles_m = count_tiles<kTile>(p);
+  constexpr int kCount = SHARE == kAll ? BM : kTile;  // tokens of the tiles that are counted
+  uint32_t tiles_m = static_cast<uint32_t>((p.M + kCount - 1) / kCount);
+  if constexpr (GROUPED) tiles_m = count_tiles<kCount>(p);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = 8 * wave + (lane >> 3);
   const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
   const int pitch = static_cast<int>(p.pitch);
   const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
 
-  uint32_t tm, tn;
-  if (!place_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
-  RowTile t = {static_cast<int64_t>(tm) * kTile, min(p.M, static_cast<int64_t>(tm) * kTile + kTile), 0};
-  if constexpr (GROUPED) t = find_tile<kTile>(p, tm);
+  uint32_t index, half = 0, tm, tn;
+  const uint32_t all = tiles_m * tiles_n, whole = whole_tiles(all, p.cus);
+  if constexpr (SHARE == kHalves) {
+    if (!tile_of_group(blockIdx.x, 2 * (all - whole), index)) return;
+    half = index & 1;
+    index = whole + index / 2;
+  } else {
+    if (!tile_of_group(blockIdx.x, SHARE == kWhole ? whole : all, index)) return;
+  }
+  locate_tile(index, tiles_m, tiles_n, tm, tn);
+  RowTile t = {static_cast<int64_t>(tm) * kCount, min(p.M, static_cast<int64_t>(tm) * kCount + kCount), 0};
+  if constexpr (GROUPED) t = find_tile<kCount>(p, tm);
+  if constexpr (SHARE == kHalves) {
+    t.first += half * BM;
+    t.end = min(t.end, t.first + BM);
+    if (t.end <= t.first) return;
+  }
   const int64_t n0 = static_cast<int64_t>(tn) * kTile;
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
   const auto rw = rsrc(w0, static_cast<uint32_t>(min(int64_t(kTile), p.N - n0) * p.pitch));
   const auto rx = rsrc(GROUPED ? nullptr : p.xq + t.first * p.pitch,
                        static_cast<uint32_t>((t.end - t.first) * p.pitch));
-  const int8_t* xrow[GROUPED ? L : 1];
+  const int8_t* xrow[GROUPED ? LM : 1];
   if constexpr (GROUPED) {
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
+    for (int i = 0; i < LM; ++i) {
       const int64_t m = t.first + row + 32 * i;
       const int64_t src = m < t.end ? source_row<true>(p, m) : -1;
       xrow[i] = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
@@ -295,46 +323,46 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
     const bool in = k + chunk < pitch;
     const uint32_t v = in ? voff + k : kNever;
     const LdsPtr to = (LdsPtr)(buf + (32 * i + 8 * wave) * kDepth);
-    if (i < L)
+    if (i < LN)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, to, 16, v + 32 * i * pitch, 0, 0, 0);
     else if constexpr (GROUPED)
-      __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - L : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((GlobalPtr)(xrow[GROUPED ? i - LN : 0] + (in ? k + chunk : 0)), to, 16, 0, 0);
     else
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v + 32 * (i - L) * pitch, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, v + 32 * (i - LN) * pitch, 0, 0, 0);
   };
 
   // --- LDS to the matrix cores
-  const int wn = (wave & 1) * (kTile / 2), wm = (wave >> 1) * (kTile / 2);
-  i32x4 fw[2][T], fx[2][T];
+  const int wn = (wave & 1) * (kTile / 2), wm = (wave >> 1) * (BM / 2);
+  i32x4 fw[2][TN], fx[2][TM];
   auto fetch = [&](int set, const int8_t* buf, int part) {
     const int at = (lane & 31) * kDepth + (((2 * part + (lane >> 5)) ^ (lane >> 1 & 7)) * 16);
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int i = 0; i < TN; ++i)
       fw[set][i] = *reinterpret_cast<const i32x4*>(buf + (wn + 32 * i) * kDepth + at);
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int i = 0; i < TM; ++i)
       fx[set][i] = *reinterpret_cast<const i32x4*>(buf + (kTile + wm + 32 * i) * kDepth + at);
   };
-  i32x16 acc[T][T] = {};
+  i32x16 acc[TN][TM] = {};
   auto multiply = [&](int set) {
 #pragma unroll
-    for (int i = 0; i < T; ++i)
+    for (int i = 0; i < TN; ++i)
 #pragma unroll
-      for (int j = 0; j < T; ++j)
+      for (int j = 0; j < TM; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][i], fx[set][j], acc[i][j], 0, 0, 0);
   };
   // The step after the next one's loads may start when the barrier has freed its
   // buffer: they are spread over the parts 3, 0 and 1, one to two or more matrix
   // instructions, since four waves' loads in a row would hold up the issue.
-  constexpr int kMoves = 2 * L, kThree = (kMoves + 2) / 3, kZero = (kMoves - kThree + 1) / 2;
+  constexpr int kMoves = LN + LM, kThree = (kMoves + 2) / 3, kZero = (kMoves - kThree + 1) / 2;
   constexpr int kOne = kMoves - kThree - kZero;
   auto order = [&](int loads) {
 #pragma unroll
-    for (int i = 0; i < 2 * T; ++i) {
+    for (int i = 0; i < TN + TM; ++i) {
       __builtin_amdgcn_sched_group_barrier(kSchedRead, 1, 0);
       __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
       if (i < loads) __builtin_amdgcn_sched_group_barrier(kSchedLoad, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (i < TN * TM - TN - TM) __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -371,7 +399,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
   const int64_t n = n0 + threadIdx.x, m = t.first + threadIdx.x;
   const float wscale = n < p.N ? p.ws[t.expert * p.N + n] : 0.0f;
   const int64_t src = m < t.end ? source_row<GROUPED>(p, m) : -1;
-  const float xscale = src >= 0 ? p.xs[src] : 0.0f;
+  const float xscale = src >= 0 ? p.xs[src] : 0.0f;  // (BM < 256: of tokens past the tile too, unused)
   __syncthreads();
   fetch(0, s_a, 0);
   for (int k = 0; k < steps; k += 2) {  // with an odd number the last step is one of zeros
@@ -381,7 +409,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
   s_scale[0][threadIdx.x] = wscale;
   s_scale[1][threadIdx.x] = xscale;
   __syncthreads();
-  write_tile<DT, T, T, 128 / kB>(
+  write_tile<DT, TM, TN, 128 / kB>(
       p, t.end, n0 + wn, t.first + wm, acc, s_out + wave * 32 * 128,
       [&](int c) { return *reinterpret_cast<const float4*>(&s_scale[0][wn + c]); },
       [&](int j) { return s_scale[1][wm + 32 * j + (lane & 31)]; });
@@ -661,8 +689,9 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   const uint32_t tiles_n = static_cast<uint32_t>((p.N + BN - 1) / BN);
   uint32_t tiles_m = static_cast<uint32_t>((p.M + BM - 1) / BM);
   if constexpr (GROUPED) tiles_m = count_tiles<BM>(p);
-  uint32_t tm, tn;
-  if (!place_tile(blockIdx.x, tiles_m, tiles_n, tm, tn)) return;
+  uint32_t index, tm, tn;
+  if (!tile_of_group(blockIdx.x, tiles_m * tiles_n, index)) return;
+  locate_tile(index, tiles_m, tiles_n, tm, tn);
   RowTile t = {static_cast<int64_t>(tm) * BM, min(p.M, static_cast<int64_t>(tm) * BM + BM), 0};
   if constexpr (GROUPED) t = find_tile<BM>(p, tm);
   const int64_t n0 = static_cast<int64_t>(tn) * BN;
@@ -854,13 +883,35 @@ uint32_t tile_groups(const Product& p, int BM, int BN, int threads) {
   return groups * threads < (int64_t(1) << 32) ? static_cast<uint32_t>(groups) : 0;
 }
 
+template <bool GROUPED, int TM, Share SHARE>
+void launch_share(const Product& p, int32_t y_dtype, uint32_t groups, hipStream_t st) {
+  with_dtype(y_dtype, [&](auto d) {
+    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, TM, SHARE>), dim3(groups), dim3(kTileThreads), 0,
+                       st, p);
+  });
+}
+
+// Tiles of 256 x 256.  A last turn of the compute units that is less than half
+// full is computed in halves of 128 tokens, in a second launch: 8192 x 11008 x
+// 4096 has 1376 tiles, five turns of 256 and 96 (342 us whole, 330 so).
 template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
-  const uint32_t tiles = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
-  if (tiles == 0) return NF4_EUNSUPPORTED;
-  with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED>), dim3(tiles), dim3(kTileThreads), 0, st, p);
-  });
+  const uint32_t groups = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
+  if (groups == 0) return NF4_EUNSUPPORTED;
+  launch_share<GROUPED, 4, kWhole>(p, y_dtype, groups, st);
+  // how many tiles experts' rows make only the GPU knows: the halves find out
+  const int64_t all = row_tiles<GROUPED>(p, kTile) * ((p.N + kTile - 1) / kTile);
+  if (GROUPED || whole_tiles(static_cast<uint32_t>(all), p.cus) < all)
+    launch_share<GROUPED, 2, kHalves>(p, y_dtype, (p.cus + kDies - 1) / kDies * kDies, st);
+  return launch_status();
+}
+
+// Tiles of 128 tokens x 256 channels.
+template <bool GROUPED>
+nf4_status launch_half_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
+  const uint32_t groups = tile_groups<GROUPED>(p, kTile / 2, kTile, kTileThreads);
+  if (groups == 0) return NF4_EUNSUPPORTED;
+  launch_share<GROUPED, 2, kAll>(p, y_dtype, groups, st);
   return launch_status();
 }
 
@@ -1001,6 +1052,7 @@ Product dense(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   p.M = M, p.N = N, p.pitch = pitch_of(K), p.x_rows = M;
   p.top_k = p.experts = p.splits = 1;
   p.sums_pitch = (N + 3) / 4 * 4;
+  p.cus = static_cast<uint32_t>(device_cus());
   return p;
 }
 
