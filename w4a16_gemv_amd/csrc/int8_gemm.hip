@@ -261,13 +261,14 @@ __device__ __host__ __forceinline__ uint32_t whole_tiles(uint32_t all, uint32_t 
   return 2 * rest <= cus ? all - rest : all;
 }
 
-// Which tiles of 256 x 256 a launch computes: all of them in pieces of 64 TM
-// tokens, those that whole_tiles() counts, or the others, in halves.
-enum Share { kAll, kWhole, kHalves };
+// Which tiles of 256 x 256 a launch computes: those that whole_tiles() counts, or
+// the others, in halves of 128 tokens.
+enum Share { kWhole, kHalves };
 
-template <int DT, bool GROUPED, int TM, Share SHARE>
+template <int DT, bool GROUPED, Share SHARE>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
-  constexpr int TN = kTile / 64, BM = 64 * TM;     // 32 x 32 tiles of a wave, tokens of a tile
+  constexpr int TN = kTile / 64, TM = SHARE == kHalves ? TN / 2 : TN;  // 32 x 32 tiles of a wave
+  constexpr int BM = 64 * TM;                      // tokens
   constexpr int LN = kTile / 32, LM = BM / 32;     // 16-byte loads of a thread per step
   constexpr int kB = dtype_bytes(DT);
   // two buffers that the compiler can tell apart: reads of one do not wait for
@@ -277,9 +278,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
   __shared__ __attribute__((aligned(256))) float s_scale[2][kTile];  // of the channels, of the tokens
 
   const uint32_t tiles_n = static_cast<uint32_t>((p.N + kTile - 1) / kTile);
-  constexpr int kCount = SHARE == kAll ? BM : kTile;  // tokens of the tiles that are counted
-  uint32_t tiles_m = static_cast<uint32_t>((p.M + kCount - 1) / kCount);
-  if constexpr (GROUPED) tiles_m = count_tiles<kCount>(p);
+  uint32_t tiles_m = static_cast<uint32_t>((p.M + kTile - 1) / kTile);
+  if constexpr (GROUPED) tiles_m = count_tiles<kTile>(p);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = 8 * wave + (lane >> 3);
   const int chunk = ((lane & 7) ^ (row >> 1 & 7)) * 16;
@@ -293,11 +293,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
     half = index & 1;
     index = whole + index / 2;
   } else {
-    if (!tile_of_group(blockIdx.x, SHARE == kWhole ? whole : all, index)) return;
+    if (!tile_of_group(blockIdx.x, whole, index)) return;
   }
   locate_tile(index, tiles_m, tiles_n, tm, tn);
-  RowTile t = {static_cast<int64_t>(tm) * kCount, min(p.M, static_cast<int64_t>(tm) * kCount + kCount), 0};
-  if constexpr (GROUPED) t = find_tile<kCount>(p, tm);
+  RowTile t = {static_cast<int64_t>(tm) * kTile, min(p.M, static_cast<int64_t>(tm) * kTile + kTile), 0};
+  if constexpr (GROUPED) t = find_tile<kTile>(p, tm);
   if constexpr (SHARE == kHalves) {
     t.first += half * BM;
     t.end = min(t.end, t.first + BM);
@@ -883,10 +883,10 @@ uint32_t tile_groups(const Product& p, int BM, int BN, int threads) {
   return groups * threads < (int64_t(1) << 32) ? static_cast<uint32_t>(groups) : 0;
 }
 
-template <bool GROUPED, int TM, Share SHARE>
+template <bool GROUPED, Share SHARE>
 void launch_share(const Product& p, int32_t y_dtype, uint32_t groups, hipStream_t st) {
   with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, TM, SHARE>), dim3(groups), dim3(kTileThreads), 0,
+    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, SHARE>), dim3(groups), dim3(kTileThreads), 0,
                        st, p);
   });
 }
@@ -898,20 +898,11 @@ template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
   const uint32_t groups = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
   if (groups == 0) return NF4_EUNSUPPORTED;
-  launch_share<GROUPED, 4, kWhole>(p, y_dtype, groups, st);
+  launch_share<GROUPED, kWhole>(p, y_dtype, groups, st);
   // how many tiles experts' rows make only the GPU knows: the halves find out
   const int64_t all = row_tiles<GROUPED>(p, kTile) * ((p.N + kTile - 1) / kTile);
   if (GROUPED || whole_tiles(static_cast<uint32_t>(all), p.cus) < all)
-    launch_share<GROUPED, 2, kHalves>(p, y_dtype, (p.cus + kDies - 1) / kDies * kDies, st);
-  return launch_status();
-}
-
-// Tiles of 128 tokens x 256 channels.
-template <bool GROUPED>
-nf4_status launch_half_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
-  const uint32_t groups = tile_groups<GROUPED>(p, kTile / 2, kTile, kTileThreads);
-  if (groups == 0) return NF4_EUNSUPPORTED;
-  launch_share<GROUPED, 2, kAll>(p, y_dtype, groups, st);
+    launch_share<GROUPED, kHalves>(p, y_dtype, (p.cus + kDies - 1) / kDies * kDies, st);
   return launch_status();
 }
 
@@ -989,8 +980,8 @@ nf4_status launch_dot(const Product& p, const void* x, int64_t K, int32_t y_dtyp
 
 // The tiled kernels, and what their steps of 128 bytes of K take (us, measured at
 // 4096 x 4096, 11008 x 4096, 4096 x 11008, 2048 x 2048 and 1024 x 11008 with 32 to
-// 2048 rows): while no compute unit has more than one tile, and for each tile of
-// a compute unit that has several.  Largest tiles load the least per product, but
+// 2048 rows): where few compute units have a tile, and for each of its tiles where
+// all have one or more (the memory behind them is busier then).  Largest tiles load the least per product, but
 // leave compute units idle and take the longest for themselves: 512 x 4096 x 4096
 // takes 35 / 35 / 20 / 17 / 23 / 47 us from the smallest tiles to the largest,
 // 64 x 4096 x 4096 8.5 / 10 / 12 / 14 / 19 / 44, 1024 x 11008 x 4096 176 / 174 / 88
@@ -998,11 +989,11 @@ nf4_status launch_dot(const Product& p, const void* x, int64_t K, int32_t y_dtyp
 struct Tiling {
   int BM, BN;        // tokens, channels
   float alone, each; // us a step
-  float fixed;       // us a tile that no other's steps hide
+  float fixed;       // us a turn that no step hides
 };
-constexpr Tiling kTilings[] = {{32, 32, 0.165f, 0.125f, 0.0f}, {64, 32, 0.19f, 0.25f, 0.0f},
-                               {64, 64, 0.27f, 0.255f, 0.0f},  {128, 64, 0.38f, 0.47f, 0.0f},
-                               {128, 128, 0.55f, 0.69f, 0.0f}, {256, 256, 1.25f, 1.5f, 8.0f}};
+constexpr Tiling kTilings[] = {{32, 32, 0.16f, 0.125f, 0.0f}, {64, 32, 0.215f, 0.25f, 0.0f},
+                               {64, 64, 0.28f, 0.255f, 0.0f}, {128, 64, 0.35f, 0.47f, 0.0f},
+                               {128, 128, 0.55f, 0.69f, 0.0f}, {256, 256, 1.05f, 1.6f, 4.0f}};
 constexpr int kLargest = 5;
 constexpr float kLaunchUs = 3.0f, kJoinUs = 4.5f;
 constexpr int kMaxSplits = 16;
@@ -1033,8 +1024,9 @@ Plan plan(const Product& p, size_t room) {
       if (splits > 1 && (tiles * splits > cus || p.M * p.sums_pitch * 4 * splits > static_cast<int64_t>(room) ||
                          steps < 4 * splits))
         break;
-      const double turns = std::ceil(tiles * splits / cus);
-      const double step = t.alone > turns * t.each ? t.alone : turns * t.each;
+      const double full = tiles * splits / cus, turns = std::ceil(full);
+      const double more = t.each > t.alone ? t.each - t.alone : 0.0;
+      const double step = turns > 1 ? turns * t.each : t.alone + more * full;
       const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs : 0.0);
       if (us < least * (splits > 1 ? 0.85 : 1.0)) {
         least = us;
