@@ -257,6 +257,86 @@ def test_gemm_empty_sizes(M, N, K):
     assert same(z, amd.int8_gemm(amd.int8_quantize(x16), wt, out_dtype=F32))
 
 
+def gpu_product(x, w, dtype):
+    """product() on the GPU, for larger sizes: the fp64 sums of whole numbers are exact."""
+    acc = x.data[:, :x.K].double() @ w.data[:, :w.K].double().t().contiguous()
+    return (acc.float() * x.scale[:, None] * w.scale[None, :]).to(dtype)
+
+
+# sizes for which each tiling is the fastest by the library's model, from the smallest tiles to the largest: whole
+# turns, halves in a last turn, halves alone; and sums split over workgroups
+TILINGS = [(17, 7, 64), (40, 500, 700), (33, 4099, 64), (120, 4100, 256), (100, 4099, 64), (128, 4096, 300), (200, 4099, 64),
+           (513, 4100, 1000), (2049, 1000, 64), (1030, 4100, 640), (4100, 4099, 1501), (4096, 4096, 2048), (2000, 4001, 2048),
+           (17, 7, 8192), (60, 64, 11000), (500, 30, 8192), (33, 1000, 8192), (65, 1000, 8192), (130, 513, 20000),
+           (65, 2100, 8192), (18, 64, 131071)]
+
+
+@pytest.mark.parametrize("M,N,K", TILINGS)
+def test_gemm_tilings(M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    _, _, x = random_tensor(rng, M, K)
+    _, _, w = random_tensor(rng, N, K)
+    for i, dtype in enumerate(TYPES):
+        want = gpu_product(x, w, dtype)
+        # the output aligned to nothing but its element in turn
+        whole = torch.full((M * N + 2 * GUARD + 1,), 7.25, dtype=dtype, device=dev())
+        y = whole[GUARD + i % 2:GUARD + i % 2 + M * N].view(M, N)
+        amd.int8_gemm(x, w, y=y)
+        assert same(y, want), dtype
+        assert bool((whole[:GUARD + i % 2] == 7.25).all() and (whole[GUARD + i % 2 + M * N:] == 7.25).all())
+        assert same(amd.int8_gemm(x, w, out_dtype=dtype, workspace=torch.empty(256, dtype=torch.uint8, device=dev())), want)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 333, 700), (2, 64, 5000), (2, 50, 11264), (7, 333, 700), (16, 100, 2048), (16, 70, 4096), (5, 130, 11264),
+                                   (13, 64, 11265), (90, 131, 700), (30, 64, 9000)])
+def test_gemm_alignment(M, N, K):
+    """Codes aligned to 16 bytes and no more, outputs to one element."""
+    rng = np.random.default_rng(M * N + K)
+    q, xs, x = random_tensor(rng, M, K)
+    w, ws, wt = random_tensor(rng, N, K)
+
+    def moved(t):
+        room = torch.zeros(t.data.numel() + 16, dtype=torch.int8, device=dev())
+        v = room[16:].view(t.data.shape)
+        v.copy_(t.data)
+        return amd.Int8Tensor(v, t.scale, t.K)
+
+    for dtype in TYPES:
+        whole = torch.full((M * N + 2 * GUARD + 1,), 7.25, dtype=dtype, device=dev())
+        y = whole[GUARD + 1:GUARD + 1 + M * N].view(M, N)
+        amd.int8_gemm(moved(x), moved(wt), y=y)
+        assert same(y, product(q, xs, w, ws, dtype))
+        assert bool((whole[:GUARD + 1] == 7.25).all() and (whole[GUARD + 1 + M * N:] == 7.25).all())
+
+
+def test_offsets_past_32_bits():
+    """Values, codes and outputs beyond the first 4 GiB (and 2^31 elements) of their tensors."""
+    rows, K = 70000, 62000
+    g = torch.Generator(device=dev()).manual_seed(3)
+    x = torch.empty(rows, K, dtype=BF, device=dev())
+    part = torch.randn(700, K, generator=g, device=dev()).to(BF)
+    for i in range(0, rows, 700):
+        x[i:i + 700] = part.roll(i // 700, 0)
+    t = amd.int8_quantize(x)
+    ends = [0, 1, 34639, 34640, 69998, 69999]
+    q, s = encode(x[ends].cpu())
+    assert torch.equal(t.data[ends].cpu(), padded(q)) and same(t.scale[ends], torch.from_numpy(s))
+    assert same(t.dequant()[ends], torch.from_numpy(q.astype(np.float32) * s[:, None]).to(BF))
+    del x
+    few = amd.Int8Tensor(t.data[ends].contiguous(), t.scale[ends].contiguous(), K)
+    y = amd.int8_gemm(few, t, out_dtype=F32)                    # 4.3 GB of weights
+    assert same(y[:, ends], product(q, s, q, s, F32))
+    y = amd.int8_gemm(t, few, out_dtype=F32)                    # of activations
+    assert same(y[ends], product(q, s, q, s, F32))
+    del t, y
+    rng = np.random.default_rng(8)
+    _, _, a = random_tensor(rng, 70000, 64)
+    y = amd.int8_gemm(a, a)                                     # 9.8 GB of outputs
+    b = amd.Int8Tensor(a.data[ends].contiguous(), a.scale[ends].contiguous(), 64)
+    assert same(y[ends][:, ends], gpu_product(b, b, BF))
+    assert same(y[:, ends], gpu_product(a, b, BF))
+
+
 # --- quantize and product in one call ----------------------------------------
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 4096, 4096), (1, 100, 11008), (2, 65, 300), (3, 17, 4097), (4, 300, 1501),
@@ -395,6 +475,30 @@ def test_gemm_grouped(T, k, E, N, K, kind):
     want = grouped(q2, xs2, w, ws, offsets, np.arange(T * k), y.cpu(), BF)
     amd.int8_gemm_grouped(x2, wt, plan, y=y, x_sorted=True)
     assert same(y, want) and untouched(whole, T * k * N)
+
+
+@pytest.mark.parametrize("rows,E,N,K", [(100, 1, 40, 64), (1500, 30, 130, 64), (900, 12, 1000, 256), (600, 1, 1030, 64), (6000, 1, 130, 64),
+                                        (2700, 30, 515, 64), (6000, 30, 1030, 1024), (4500, 3, 2100, 1024), (9000, 2, 2048, 1500)])
+def test_gemm_grouped_tilings(rows, E, N, K):
+    """Sizes of each tiling; uneven experts, slots dropped, k = 2."""
+    rng = np.random.default_rng(rows + E + N)
+    T = rows // 2
+    ids = np.minimum(rng.geometric(2.0 / (E + 1), (T, 2)) - 1, E - 1)
+    ids[rng.random((T, 2)) < 0.05] = -1
+    _, _, x = random_tensor(rng, T, K)
+    _, _, w = random_tensor(rng, E * N, K)
+    offsets, order, pos = route_of(ids, E)
+    plan = to_route((offsets, order, pos))
+    for dtype in TYPES:
+        whole, y = guarded(2 * T, N, dtype)
+        amd.int8_gemm_grouped(x, w, plan, y=y)
+        for e in range(E):
+            a, b = int(offsets[e]), int(offsets[e + 1])
+            token = torch.from_numpy(order[a:b] // 2).long().to(dev())
+            xe = amd.Int8Tensor(x.data[token], x.scale[token], K)
+            we = amd.Int8Tensor(w.data[e * N:(e + 1) * N], w.scale[e * N:(e + 1) * N], K)
+            assert same(y[a:b], gpu_product(xe, we, dtype)), (dtype, e)
+        assert bool((y[int(offsets[E]):] == 7.25).all()) and untouched(whole, 2 * T * N)
 
 
 @pytest.mark.parametrize("T", [6, 200])

@@ -217,6 +217,25 @@ def test_gradients_against_differences():
     assert inner(amd.moe_gather_grad(g, plan), xstep) == inner(g, moved)
 
 
+def test_offsets_past_32_bits():
+    """Rows beyond the first 4 GiB of their tensors."""
+    T, H = 50000, 48001
+    ids = torch.zeros(T, 1, dtype=torch.int32, device=dev())
+    plan = amd.moe_sort(ids, 1)
+    x = torch.empty(T, H, dtype=BF, device=dev())
+    part = torch.randn(500, H, device=dev()).to(BF)
+    for i in range(0, T, 500):
+        x[i:i + 500] = part.roll(i // 500, 0)
+    xs = amd.moe_gather(x, plan)
+    assert torch.equal(xs, x)                                   # one expert, one slot: the same order
+    assert torch.equal(amd.moe_gather_grad(xs, plan), x)
+    w = torch.full((T, 1), 2.0, device=dev())
+    dys, dw = amd.moe_combine_grad(x, xs, plan, w, dys=xs.clone())
+    assert torch.equal(dys[-5:], x[-5:] * 2) and torch.equal(dys[:5], x[:5] * 2)
+    v = x[-5:].double().cpu().numpy() ** 2
+    assert close(dw[-5:, 0], v.sum(1), v.sum(1), H / 64 + 24, F32)
+
+
 def test_positions_out_of_range_are_dropped():
     T, k, H = 6, 2, 70
     pos = np.arange(T * k, dtype=np.int32).reshape(T, k)

@@ -1019,14 +1019,17 @@ Plan plan(const Product& p, size_t room) {
       rows = p.M >= int64_t(p.experts) * t.BM / 2 ? static_cast<double>(p.M) / t.BM + 0.5 * p.experts
                                                   : static_cast<double>(p.M < p.experts ? p.M : p.experts);
     const double tiles = rows * static_cast<double>((p.N + t.BN - 1) / t.BN);
+    if (i < kLargest && tile_groups<GROUPED>(p, t.BM, t.BN, 256) == 0) continue;
     const int most = GROUPED || i == kLargest ? 1 : kMaxSplits;
     for (int splits = 1; splits <= most; ++splits) {
       if (splits > 1 && (tiles * splits > cus || p.M * p.sums_pitch * 4 * splits > static_cast<int64_t>(room) ||
                          steps < 4 * splits))
         break;
-      const double full = tiles * splits / cus, turns = std::ceil(full);
+      const double full = tiles * splits / cus, part = full - std::floor(full);
+      double turns = std::ceil(full);
+      if (i == kLargest && part > 0 && part <= 0.5) turns -= 0.3;  // halves in the last
       const double more = t.each > t.alone ? t.each - t.alone : 0.0;
-      const double step = turns > 1 ? turns * t.each : t.alone + more * full;
+      const double step = full > 1 || turns < 1 ? turns * t.each : t.alone + more * full;
       const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs : 0.0);
       if (us < least * (splits > 1 ? 0.85 : 1.0)) {
         least = us;
