@@ -25,59 +25,89 @@ using namespace int8dev;
 
 constexpr int kThreads = 256;
 
-// A grid may not have 2^32 threads: beyond this many rows a workgroup takes
-// several.
+// A grid may not have 2^32 threads: past this many workgroups each takes several
+// turns.
 constexpr int64_t kMaxGroups = 1 << 20;
 
-uint32_t groups_for(int64_t rows) { return static_cast<uint32_t>(rows < kMaxGroups ? rows : kMaxGroups); }
+uint32_t groups_for(int64_t n) { return static_cast<uint32_t>(n < kMaxGroups ? n : kMaxGroups); }
 
-// A workgroup per row: one pass for the maximum, one for the codes (the row
-// comes from the caches the second time).
-template <int DT>
-__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __restrict__ x,
-                                                                 int64_t rows, int64_t K,
-                                                                 int64_t pitch,
+// WAVES waves per row: a whole workgroup, or each of its waves a row of its own
+// where rows are short and many.  The row's values stay in registers from the
+// maximum to the codes: HOLD pieces of eight to a thread (0: the row is longer and
+// read a second time, from the caches).  Bound by memory: 4097 x 11008 bf16 takes
+// 26 us (135 MB, 5.2 TB/s).
+template <int DT, int WAVES, int HOLD>
+__global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __restrict__ x, int64_t rows,
+                                                                 int64_t K, int64_t pitch,
                                                                  int8_t* __restrict__ q,
                                                                  float* __restrict__ scale) {
-  __shared__ uint32_t s_max[kThreads / 64];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-  const char* xr = static_cast<const char*>(x) + row * K * dtype_bytes(DT);
-  uint32_t m = 0;
-  for (int64_t at = 8 * threadIdx.x; at < K; at += 8 * kThreads)
-    m = max(m, piece_peak<DT>(load_piece<DT>(xr, at, K)));
-  m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = m;
-  __syncthreads();
+  constexpr int kAtOnce = kThreads / 64 / WAVES, kWidth = 64 * WAVES;  // rows of a workgroup, threads of a row
+  __shared__ uint32_t s_max[WAVES];
+  const int t = threadIdx.x % kWidth;
+  for (int64_t row = int64_t(blockIdx.x) * kAtOnce + threadIdx.x / kWidth; row < rows;
+       row += int64_t(gridDim.x) * kAtOnce) {
+    const char* xr = static_cast<const char*>(x) + row * K * dtype_bytes(DT);
+    Piece<DT> held[HOLD > 0 ? HOLD : 1];
+    uint32_t m = 0;
+    if constexpr (HOLD > 0) {
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) m = max(m, s_max[i]);
-  const RowScale s = row_scale(m);
-  if (threadIdx.x == 0) scale[row] = s.scale;
-  int8_t* qr = q + row * pitch;
-  for (int64_t at = 8 * threadIdx.x; at < pitch; at += 8 * kThreads)
-    *reinterpret_cast<uint2*>(qr + at) = encode_piece<DT>(load_piece<DT>(xr, at, K), s);
-  __syncthreads();  // s_max is read before the next row's
+      for (int i = 0; i < HOLD; ++i) {
+        const int64_t at = 8 * (t + int64_t(i) * kWidth);
+        held[i] = at < K ? load_piece<DT>(xr, at, K) : Piece<DT>{};
+      }
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) m = max(m, piece_peak<DT>(held[i]));
+    } else {
+      for (int64_t at = 8 * t; at < K; at += 8 * kWidth) m = max(m, piece_peak<DT>(load_piece<DT>(xr, at, K)));
+    }
+    m = wave_max(m);
+    if constexpr (WAVES > 1) {
+      if ((threadIdx.x & 63) == 0) s_max[threadIdx.x >> 6] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WAVES; ++i) m = max(m, s_max[i]);
+      __syncthreads();  // before the next row's
+    }
+    const RowScale s = row_scale(m);
+    if (t == 0) scale[row] = s.scale;
+    int8_t* qr = q + row * pitch;
+    if constexpr (HOLD > 0) {
+#pragma unroll
+      for (int i = 0; i < HOLD; ++i) {
+        const int64_t at = 8 * (t + int64_t(i) * kWidth);
+        if (at < pitch) *reinterpret_cast<uint2*>(qr + at) = encode_piece<DT>(held[i], s);
+      }
+    } else {
+      for (int64_t at = 8 * t; at < pitch; at += 8 * kWidth)
+        *reinterpret_cast<uint2*>(qr + at) = encode_piece<DT>(load_piece<DT>(xr, at, K), s);
+    }
   }
 }
 
-template <int DT>
+// Threads of a row as above.  Bound by memory: 4097 x 11008 to bf16 takes 27 us.
+template <int DT, int WAVES>
 __global__ __launch_bounds__(kThreads) void dequant_rows_kernel(const int8_t* __restrict__ q,
-                                                                const float* __restrict__ scale,
-                                                                int64_t rows, int64_t K,
-                                                                int64_t pitch,
+                                                                const float* __restrict__ scale, int64_t rows,
+                                                                int64_t K, int64_t pitch,
                                                                 void* __restrict__ out) {
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-  const float s = scale[row];
-  char* o = static_cast<char*>(out) + row * K * dtype_bytes(DT);
-  for (int64_t at = 8 * threadIdx.x; at < K; at += 8 * kThreads) {
-    const uint2 c = *reinterpret_cast<const uint2*>(q + row * pitch + at);
-    float f[8];
+  constexpr int kAtOnce = kThreads / 64 / WAVES, kWidth = 64 * WAVES;
+  for (int64_t row = int64_t(blockIdx.x) * kAtOnce + threadIdx.x / kWidth; row < rows;
+       row += int64_t(gridDim.x) * kAtOnce) {
+    const float s = scale[row];
+    char* o = static_cast<char*>(out) + row * K * dtype_bytes(DT);
+    for (int64_t at = 8 * (threadIdx.x % kWidth); at < K; at += 8 * kWidth) {
+      const uint2 c = *reinterpret_cast<const uint2*>(q + row * pitch + at);
+      float f[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      f[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)))) * s;
-    store_piece<DT>(o, at, K, make_piece<DT>(f));
-  }
+      for (int i = 0; i < 8; ++i)
+        f[i] = static_cast<float>(static_cast<int8_t>((i < 4 ? c.x : c.y) >> (8 * (i & 3)))) * s;
+      store_piece<DT>(o, at, K, make_piece<DT>(f));
+    }
   }
 }
+
+// Short rows, and more of them than fill the card as workgroups: a wave each.
+bool wave_rows(int64_t rows, int64_t K) { return K <= 2048 && rows > 4 * device_cus(); }
 
 }  // namespace
 
@@ -86,8 +116,20 @@ namespace int8dev {
 void quantize_launch(const void* x, int32_t dt, int64_t rows, int64_t K, int8_t* q, float* scale,
                      hipStream_t st) {
   with_dtype(dt, [&](auto t) {
-    hipLaunchKernelGGL((quantize_rows_kernel<decltype(t)::value>), dim3(groups_for(rows)),
-                       dim3(kThreads), 0, st, x, rows, K, pitch_of(K), q, scale);
+    constexpr int DT = decltype(t)::value;
+    const int64_t pitch = pitch_of(K);
+#define INT8_QUANTIZE(WAVES, HOLD)                                                                     \
+  hipLaunchKernelGGL((quantize_rows_kernel<DT, WAVES, HOLD>), dim3(groups_for((rows * WAVES + 3) / 4)), \
+                     dim3(kThreads), 0, st, x, rows, K, pitch, q, scale)
+    if (wave_rows(rows, K))
+      INT8_QUANTIZE(1, 4);
+    else if (K <= 2 * 8 * kThreads)
+      INT8_QUANTIZE(4, 2);
+    else if (K <= 6 * 8 * kThreads)
+      INT8_QUANTIZE(4, 6);
+    else
+      INT8_QUANTIZE(4, 0);
+#undef INT8_QUANTIZE
   });
 }
 
@@ -116,10 +158,15 @@ nf4_status int8_dequant(const int8_t* q, const float* scale, int64_t rows, int64
   if (!aligned(out, dtype_bytes(out_dtype)) || !aligned(q, 16) || !aligned(scale, 4))
     return NF4_EINVAL;
   if (rows > kMaxDim || K > kMaxDim) return NF4_EUNSUPPORTED;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   with_dtype(out_dtype, [&](auto t) {
-    hipLaunchKernelGGL((dequant_rows_kernel<decltype(t)::value>), dim3(groups_for(rows)),
-                       dim3(kThreads), 0, reinterpret_cast<hipStream_t>(stream), q, scale, rows, K,
-                       pitch_of(K), out);
+    constexpr int DT = decltype(t)::value;
+    if (wave_rows(rows, K))
+      hipLaunchKernelGGL((dequant_rows_kernel<DT, 1>), dim3(groups_for((rows + 3) / 4)), dim3(kThreads), 0, st, q,
+                         scale, rows, K, pitch_of(K), out);
+    else
+      hipLaunchKernelGGL((dequant_rows_kernel<DT, 4>), dim3(groups_for(rows)), dim3(kThreads), 0, st, q, scale,
+                         rows, K, pitch_of(K), out);
   });
   return launch_status();
 }
