@@ -53,7 +53,11 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(const void* __r
 #pragma unroll
       for (int i = 0; i < HOLD; ++i) {
         const int64_t at = 8 * (t + int64_t(i) * kWidth);
-        held[i] = at < K ? load_piece<DT>(xr, at, K) : Piece<DT>{};
+        held[i] = Piece<DT>{};
+        if (at + 8 <= K)
+          held[i] = whole_piece<DT, true>(xr, at);
+        else if (at < K)
+          held[i] = load_piece<DT>(xr, at, K);
       }
 #pragma unroll
       for (int i = 0; i < HOLD; ++i) m = max(m, piece_peak<DT>(held[i]));

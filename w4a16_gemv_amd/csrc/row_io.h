@@ -32,16 +32,20 @@ struct Piece {
   u32x4 v[DT == INT8_FP32 ? 2 : 1];
 };
 
-// Elements [at, at + 8) of the row at p, all of which exist.
-template <int DT>
+// Elements [at, at + 8) of the row at p, all of which exist.  STREAM: read once, and
+// not worth a place in the caches.
+template <int DT, bool STREAM = false>
 __device__ __forceinline__ Piece<DT> whole_piece(const void* p, int64_t at) {
   Piece<DT> r;
   const char* a = static_cast<const char*>(p) + at * dtype_bytes(DT);
+  // (spelled out: a template would lose the types' alignment)
   if constexpr (DT == INT8_FP32) {
-    r.v[0] = *reinterpret_cast<const u32x4_a4*>(a);
-    r.v[1] = *reinterpret_cast<const u32x4_a4*>(a + 16);
+    const u32x4_a4* v = reinterpret_cast<const u32x4_a4*>(a);
+    r.v[0] = STREAM ? __builtin_nontemporal_load(v) : *v;
+    r.v[1] = STREAM ? __builtin_nontemporal_load(v + 1) : v[1];
   } else {
-    r.v[0] = *reinterpret_cast<const u32x4_a2*>(a);
+    const u32x4_a2* v = reinterpret_cast<const u32x4_a2*>(a);
+    r.v[0] = STREAM ? __builtin_nontemporal_load(v) : *v;
   }
   return r;
 }
@@ -65,17 +69,20 @@ __device__ __forceinline__ Piece<DT> load_piece(const void* p, int64_t at, int64
 }
 
 template <int DT>
+__device__ __forceinline__ void store_whole_piece(void* p, int64_t at, const Piece<DT>& r) {
+  char* a = static_cast<char*>(p) + at * dtype_bytes(DT);
+  if constexpr (DT == INT8_FP32) {
+    *reinterpret_cast<u32x4_a4*>(a) = r.v[0];
+    *reinterpret_cast<u32x4_a4*>(a + 16) = r.v[1];
+  } else {
+    *reinterpret_cast<u32x4_a2*>(a) = r.v[0];
+  }
+}
+
+template <int DT>
 __device__ __forceinline__ void store_piece(void* p, int64_t at, int64_t n, const Piece<DT>& r) {
   char* a = static_cast<char*>(p) + at * dtype_bytes(DT);
-  if (at + 8 <= n) {
-    if constexpr (DT == INT8_FP32) {
-      *reinterpret_cast<u32x4_a4*>(a) = r.v[0];
-      *reinterpret_cast<u32x4_a4*>(a + 16) = r.v[1];
-    } else {
-      *reinterpret_cast<u32x4_a2*>(a) = r.v[0];
-    }
-    return;
-  }
+  if (at + 8 <= n) return store_whole_piece<DT>(p, at, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (at + i < n) {
