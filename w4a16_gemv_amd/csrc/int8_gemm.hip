@@ -581,10 +581,16 @@ __global__ __launch_bounds__(kDotThreads, 4) void dot_kernel(Product p, const vo
 // Few rows: up to 16 tokens.  The eight waves of a workgroup share K, and each
 // holds the codes of its share, of all the tokens, in registers while the
 // workgroup goes through its channels, 16 at a time: the weights go from memory
-// straight to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g holds
-// A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]), each
-// byte read once, a whole tile of them in flight while the one before is used.
-// The waves' int32 sums meet in LDS.
+// through registers to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g
+// holds A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]),
+// each byte read once, a whole tile of them in flight while the one before is
+// used.  The waves' int32 sums meet in LDS.
+//
+// Bound by the weights' stream: 13 x 11008 x 4096 takes 11.6 us (45 MB, a plain
+// read of which takes 8.8), or 13.0 with each lane loading what it multiplies,
+// where four lanes read four rows.  The one- and two-token kernel at more tokens
+// is slower from four on (12.0 against 11.1 us at 4 x 11008 x 4096), and from 17 on
+// the tiled kernels' weights go to twice the tokens.
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 constexpr int kRowThreads = 64 * kRowWaves;
@@ -600,11 +606,20 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
   }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int pitch = static_cast<int>(p.pitch);
-  const int inside = (lane >> 4) * 16;
+  // a unit as it is loaded: lane 4 i + g has 16 bytes g of row i, so that four lanes
+  // read 64 bytes in a row; turned() hands them to lane i + 16 g
+  const int row = lane >> 2, inside = (lane & 3) * 16;
+  auto turned = [&](const i32x4& v) {
+    const int from = 4 * (4 * (lane & 15) + (lane >> 4));  // a lane's number times 4
+    i32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = __builtin_amdgcn_ds_bpermute(from, v[e]);
+    return r;
+  };
   // the wave's units of 64 bytes: pairs, so that two loads read whole lines
   const int units = pitch / 64;
   auto unit = [&](int u) { return 2 * wave + 2 * kRowWaves * (u >> 1) + (u & 1); };
-  const uint32_t voff = static_cast<uint32_t>((lane & 15) * pitch + inside);
+  const uint32_t voff = static_cast<uint32_t>(row * pitch + inside);
   const int8_t* w0 = p.wq + t.expert * p.N * p.pitch;
   i32x4 w[UNITS];
   auto load = [&](uint32_t tile) {
@@ -619,18 +634,22 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
 
   const int64_t m = t.first + (lane & 15);
   const int64_t src = source_row<GROUPED>(p, min(m, t.end - 1));
-  const int8_t* xr = (src >= 0 ? p.xq + src * p.pitch : w0) + inside;  // any row that may be read
   const float xs = src >= 0 ? p.xs[src] : 0.0f;
+  const int64_t from = source_row<GROUPED>(p, min(t.first + row, t.end - 1));
+  const int8_t* xr = (from >= 0 ? p.xq + from * p.pitch : w0) + inside;  // any row that may be read
   i32x4 codes[UNITS];
 #pragma unroll
   for (int u = 0; u < UNITS; ++u)  // past the row the weights are zeros
     codes[u] = *reinterpret_cast<const i32x4*>(xr + (unit(u) < units ? 64 * unit(u) : 0));
+#pragma unroll
+  for (int u = 0; u < UNITS; ++u) codes[u] = turned(codes[u]);
 
   int turn = 0;
   for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
     i32x4 acc = {};
 #pragma unroll
-    for (int u = 0; u < UNITS; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u], codes[u], acc, 0, 0, 0);
+    for (int u = 0; u < UNITS; ++u)
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(turned(w[u]), codes[u], acc, 0, 0, 0);
     if (tile + gridDim.x < tiles) load(tile + gridDim.x);
     s_sum[turn & 1][wave][lane] = acc;
     __syncthreads();
@@ -1067,9 +1086,6 @@ nf4_status launch(Product p, int32_t y_dtype, void* workspace, size_t room, hipS
   const Plan plan_ = plan<GROUPED>(p, workspace ? room : 0);
   p.splits = plan_.splits;
   p.sums = static_cast<int32_t*>(workspace);
-#ifdef FORCE
-  p.splits = 1; return FORCE;
-#endif
   switch (plan_.tiling) {
     case 0: return launch_stream<GROUPED, 1, 1, 4, 1, 1, 8>(p, y_dtype, st);
     case 1: return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
