@@ -210,6 +210,15 @@ __device__ __forceinline__ void write_tile(const Product& p, int64_t end, int64_
 // x 128 outputs in int32 accumulators, which takes all of a compute unit's
 // registers and LDS.
 //
+// Bound by the matrix pipe, the clock and the LDS together: 8192 x 8192 x 8192 takes
+// 430 us (2560 TOP/s), a step of 64 matrix instructions a wave about 1.45 us where
+// they alone take 1.08 (the clock sinks under them; on zeros the same program takes
+// 1.25), with the LDS reads 1.30.  8192 x 11008 x 4096 takes 330-340 us, a seventh of
+// it for the outputs' scaling and stores.  Measured and not kept: one workgroup for
+// several tiles, the next one's first loads before the stores (273 us against 246
+// at 8192 x 8192 x 4096: the loads' waits take in the stores), registers between
+// memory and LDS (the same time), all of a step's loads at its barrier (6% slower).
+//
 // 128 bytes of K at a time (a step): the tile's rows go from memory straight to
 // one of two LDS buffers, and from there to the matrix cores, 32 bytes of K at a
 // time (a part) with the next 32 being read.  One barrier per step: it stands
@@ -673,10 +682,16 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
 // ---------------------------------------------------------------------------
 // Small tiles: WM x WN x WK waves, each with TM x TN tiles of 32 x 32; the WK
 // waves of a tile share each step's K, 128 / WK bytes each.  Few steps are long
-// enough to hide anything, so the chain of a step is kept short: kStages buffers
-// in LDS, each asked for kStages steps ahead; operands read from LDS a step ahead
-// of the matrix instructions that use them; one barrier, at which a wave waits
-// for the next step's rows only.
+// enough to hide anything, so the chain of a step is kept short: STAGES buffers in
+// LDS, each asked for STAGES steps ahead; operands read from LDS a step ahead of
+// the matrix instructions that use them; one barrier, at which a wave waits for
+// the next step's rows only.  LDS is laid out as for the large tiles.
+//
+// What bounds them is how fast a compute unit gets its rows: 50-60 KB/us, against
+// 85-95 for the same loads alone, and 140 for loads that hit the L2 (64 x 64 tiles:
+// 16 KB and 0.28 us a step).  Measured and not kept: 64 bytes a step with twice the
+// stages (128 x 128 tiles, 512 x 4096 x 4096: 28 us against 23), and asking for the
+// lines that a die's workgroups share ahead of time (no change).
 // ---------------------------------------------------------------------------
 // Loads of 16 bytes a lane from memory to LDS, lane l's to byte 16 l from `to` on
 // (one address per wave).  The builtins for these would do, but for the waits: the
@@ -727,9 +742,12 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
     end = min(pitch, begin + each);
   }
   const int8_t* w0 = p.wq + (t.expert * p.N + n0) * p.pitch;
-  const i32x4 rw = range_words(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
-  const i32x4 rx = range_words(GROUPED ? nullptr : p.xq + t.first * p.pitch,
-                               static_cast<uint32_t>((t.end - t.first) * p.pitch));
+  i32x4 rw = range_words(w0, static_cast<uint32_t>(min(int64_t(BN), p.N - n0) * p.pitch));
+  i32x4 rx = range_words(GROUPED ? nullptr : p.xq + t.first * p.pitch,
+                         static_cast<uint32_t>((t.end - t.first) * p.pitch));
+  // scalars that the vector unit has written (range_words) may be read by a load
+  // five instructions later; the compiler sees to that for its own loads only
+  asm volatile("s_nop 4" : "+s"(rw), "+s"(rx));
   const uint32_t voff = static_cast<uint32_t>(row * pitch + chunk);
   const int8_t* xrow[GROUPED ? LM : 1];
   if constexpr (GROUPED) {
@@ -917,10 +935,11 @@ template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
   const uint32_t groups = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
   if (groups == 0) return NF4_EUNSUPPORTED;
-  launch_share<GROUPED, kWhole>(p, y_dtype, groups, st);
-  // how many tiles experts' rows make only the GPU knows: the halves find out
+  // how many tiles experts' rows make only the GPU knows: both launches find out
   const int64_t all = row_tiles<GROUPED>(p, kTile) * ((p.N + kTile - 1) / kTile);
-  if (GROUPED || whole_tiles(static_cast<uint32_t>(all), p.cus) < all)
+  const uint32_t whole = whole_tiles(static_cast<uint32_t>(all), p.cus);
+  if (GROUPED || whole > 0) launch_share<GROUPED, kWhole>(p, y_dtype, groups, st);
+  if (GROUPED || whole < all)
     launch_share<GROUPED, kHalves>(p, y_dtype, (p.cus + kDies - 1) / kDies * kDies, st);
   return launch_status();
 }
