@@ -19,7 +19,7 @@
  * The encoder works on each row alone:
  *
  *     a       = max(max_k |x_k|, 2^-100)
- *     scale   = fp32(a / 127),  inverse = fp32(127 / a)
+ *     scale   = a * (1 / 127),  inverse = 127 * (1 / a)   each step in fp32
  *     q_k     = x_k * inverse rounded to the nearest integer, ties to even
  *               (the product is not rounded before)
  *

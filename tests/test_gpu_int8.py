@@ -3,8 +3,9 @@ definitions in 64 bits.
 
 The codes and the integer sums are exact, and what follows them is a fixed
 sequence of fp32 operations, so the results are compared bit for bit: scale =
-fp32(a / 127), code = rint of the exact product x * fp32(127 / a), output =
-fp32(fp32(fp32(sum) * xs) * ws) rounded once to the output type."""
+fp32(a * fp32(1 / 127)), inverse = fp32(127 * fp32(1 / a)), code = rint of the
+exact product x * inverse, output = fp32(fp32(fp32(sum) * xs) * ws) rounded once
+to the output type."""
 import numpy as np
 import pytest
 import torch
@@ -45,10 +46,11 @@ def encode(x: torch.Tensor):
     finite = np.isfinite(v).all(1)
     a = np.abs(np.where(finite[:, None], v, 0.0)).max(1, initial=0.0)
     a = np.maximum(a, 2.0 ** -100).astype(np.float32)
-    inverse = (np.float32(127) / a).astype(np.float64)
+    one = np.float32(1)
+    inverse = (np.float32(127) * (one / a)).astype(np.float64)
     # both factors have 24 bits, so the fp64 product is exact; rint takes ties to even
     q = np.rint(np.where(finite[:, None], v, 0.0) * inverse[:, None]).astype(np.int64)
-    return q, np.where(finite, a / np.float32(127), np.float32(np.nan)).astype(np.float32)
+    return q, np.where(finite, a * (one / np.float32(127)), np.float32(np.nan)).astype(np.float32)
 
 
 def padded(q: np.ndarray) -> torch.Tensor:
@@ -88,7 +90,8 @@ def untouched(whole, n):
 # --- the encoder -------------------------------------------------------------
 
 QUANT = [(1, 1), (1, 7), (3, 8), (2, 63), (5, 64), (4, 65), (1, 4096), (7, 511), (9, 512), (3, 513), (2, 2047),
-         (6, 2049), (3, 4099), (2, 8193), (2, 11008), (300, 33), (2, 16385), (1, 40001), (1, 131071), (1030, 128)]
+         (6, 2049), (3, 4099), (2, 8193), (2, 11008), (300, 33), (2, 16385), (1, 40001), (1, 131071), (1030, 128),
+         (3, 12289), (2, 16384), (3, 20000), (2, 32768), (2, 32769), (1024, 2048), (2049, 1024), (2050, 70)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -114,8 +117,8 @@ def test_quantize(rows, K, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
 def test_quantize_rounding_borders(dtype):
-    """Rows whose values lie on and next to halves of a step: with the peak 127 the
-    inverse is 1 and ties are exact; with other peaks the products come near."""
+    """Rows whose values lie on and next to halves of a step: with peaks whose
+    inverse is a power of two the ties are exact; with others the products come near."""
     rows = []
     for peak in (127.0, 254.0, 63.5, 1.0, 3.0, 96.0):
         step = peak / 127
@@ -157,6 +160,21 @@ def test_quantize_extreme_rows(dtype):
     y = amd.int8_gemm(t, w, out_dtype=F32).cpu()
     assert torch.isnan(y).all(1).tolist() == [False] * 4 + [True] * 3 + [False] * 2
     assert not torch.isnan(y[[0, 1, 2, 3, 7, 8]]).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_quantize_equals_the_tensor_expressions(dtype):
+    """The codes and scales that a program gets from the same formulas in tensor
+    operations on the device; every value here is near a half of the row's peak,
+    where the quotient is next to a tie."""
+    g = torch.Generator(device=dev()).manual_seed(5)
+    x = torch.randn(4096, 96, generator=g, device=dev()).to(dtype)
+    x[:, ::3] = x.abs().amax(1, keepdim=True) / 2
+    a = x.float().abs().amax(1)
+    q = (x.double() * (127.0 / a).double()[:, None]).round()
+    t = amd.int8_quantize(x)
+    assert torch.equal(t.data[:, :96].double(), q)
+    assert same(t.scale, a / 127.0)
 
 
 def test_quantize_shapes_and_out():
@@ -268,7 +286,7 @@ def gpu_product(x, w, dtype):
 TILINGS = [(17, 7, 64), (40, 500, 700), (33, 4099, 64), (120, 4100, 256), (100, 4099, 64), (128, 4096, 300), (200, 4099, 64),
            (513, 4100, 1000), (2049, 1000, 64), (1030, 4100, 640), (4100, 4099, 1501), (4096, 4096, 2048), (2000, 4001, 2048),
            (17, 7, 8192), (60, 64, 11000), (500, 30, 8192), (33, 1000, 8192), (65, 1000, 8192), (130, 513, 20000),
-           (65, 2100, 8192), (18, 64, 131071)]
+           (65, 2100, 8192), (18, 64, 131071), (33, 1500, 8192), (47, 1030, 4096), (48, 130, 4100)]
 
 
 @pytest.mark.parametrize("M,N,K", TILINGS)
@@ -478,7 +496,8 @@ def test_gemm_grouped(T, k, E, N, K, kind):
 
 
 @pytest.mark.parametrize("rows,E,N,K", [(100, 1, 40, 64), (1500, 30, 130, 64), (900, 12, 1000, 256), (600, 1, 1030, 64), (6000, 1, 130, 64),
-                                        (2700, 30, 515, 64), (6000, 30, 1030, 1024), (4500, 3, 2100, 1024), (9000, 2, 2048, 1500)])
+                                        (2700, 30, 515, 64), (6000, 30, 1030, 1024), (4500, 3, 2100, 1024), (9000, 2, 2048, 1500), (520, 64, 300, 128), (300, 30, 1000, 64),
+                                        (200, 20, 130, 64), (1000, 64, 200, 192)])
 def test_gemm_grouped_tilings(rows, E, N, K):
     """Sizes of each tiling; uneven experts, slots dropped, k = 2."""
     rng = np.random.default_rng(rows + E + N)

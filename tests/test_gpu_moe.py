@@ -83,7 +83,8 @@ def test_sort_workspace():
 MOVES = [(1, 1, 1, 1, "all"), (1, 2, 8, 4096, "all"), (16, 4, 64, 2048, "all"), (5, 3, 4, 7, "drop"), (33, 2, 3, 8, "all"),
          (20, 8, 16, 129, "drop"), (64, 1, 5, 1001, "one"), (9, 2, 4, 2049, "drop"), (7, 5, 6, 8200, "all"),
          (10, 2, 3, 300, "none"), (0, 2, 3, 64, "all"), (6, 2, 3, 0, "all"), (300, 4, 8, 513, "drop"), (3, 12, 20, 264, "all"),
-         (4, 40, 50, 72, "drop"), (50, 3, 4, 1023, "all")]
+         (4, 40, 50, 72, "drop"), (50, 3, 4, 1023, "all"),
+         (7, 5, 8, 1024, "drop"), (9, 2, 4, 1025, "drop"), (2049, 2, 4, 520, "drop")]
 
 
 def problem(T, k, E, kind, seed):

@@ -593,13 +593,12 @@ __global__ __launch_bounds__(kDotThreads, 4) void dot_kernel(Product p, const vo
 // through registers to the matrix cores (v_mfma_i32_16x16x64_i8: lane i + 16 g
 // holds A[i][16 g .. + 15], B likewise with i the column, and D[4 g .. + 3][i]),
 // each byte read once, a whole tile of them in flight while the one before is
-// used.  The waves' int32 sums meet in LDS.
+// used.  The waves' int32 sums meet in LDS.  More rows than 16 go to more workgroups.
 //
 // Bound by the weights' stream: 13 x 11008 x 4096 takes 11.6 us (45 MB, a plain
 // read of which takes 8.8), or 13.0 with each lane loading what it multiplies,
 // where four lanes read four rows.  The one- and two-token kernel at more tokens
-// is slower from four on (12.0 against 11.1 us at 4 x 11008 x 4096), and from 17 on
-// the tiled kernels' weights go to twice the tokens.
+// is slower from four on (12.0 against 11.1 us at 4 x 11008 x 4096).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
 constexpr int kRowThreads = 64 * kRowWaves;
@@ -608,11 +607,9 @@ template <int DT, bool GROUPED, int UNITS>
 __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Product p) {
   __shared__ i32x4 s_sum[2][kRowWaves][64];
   const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16);
-  RowTile t = {0, p.M, 0};
-  if constexpr (GROUPED) {
-    t = find_tile<16>(p, blockIdx.y);
-    if (t.end <= t.first) return;
-  }
+  RowTile t = {int64_t(16) * blockIdx.y, min(p.M, int64_t(16) * blockIdx.y + 16), 0};
+  if constexpr (GROUPED) t = find_tile<16>(p, blockIdx.y);
+  if (t.end <= t.first) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int pitch = static_cast<int>(p.pitch);
   // a unit as it is loaded: lane 4 i + g has 16 bytes g of row i, so that four lanes
@@ -1019,11 +1016,11 @@ nf4_status launch_dot(const Product& p, const void* x, int64_t K, int32_t y_dtyp
 // The tiled kernels, and what their steps of 128 bytes of K take (us, measured at
 // 4096 x 4096, 11008 x 4096, 4096 x 11008, 2048 x 2048 and 1024 x 11008 with 32 to
 // 2048 rows): where few compute units have a tile, and for each of its tiles where
-// all have one or more (the memory behind them is busier then).  Largest tiles load the least per product, but
-// leave compute units idle and take the longest for themselves: 512 x 4096 x 4096
-// takes 35 / 35 / 20 / 17 / 23 / 47 us from the smallest tiles to the largest,
-// 64 x 4096 x 4096 8.5 / 10 / 12 / 14 / 19 / 44, 1024 x 11008 x 4096 176 / 174 / 88
-// / 94 / 70 / 52.
+// all have one or more (the memory behind them is busier then).  Largest tiles load
+// the least per product, but leave compute units idle and take the longest for
+// themselves: 512 x 4096 x 4096 takes 35 / 35 / 20 / 17 / 23 / 47 us from the smallest
+// tiles to the largest, 64 x 4096 x 4096 8.5 / 10 / 12 / 14 / 19 / 44, 1024 x 11008 x
+// 4096 176 / 174 / 88 / 94 / 70 / 52.
 struct Tiling {
   int BM, BN;        // tokens, channels
   float alone, each; // us a step
@@ -1042,8 +1039,11 @@ struct Plan {
 
 // The tiling with the least time by the figures above, with K split over
 // workgroups where that leaves compute units without a tile (64 x 1024 x 11008:
-// 15 us in one piece, 10 in four) and the workspace has room for the sums.  Rows
-// sorted by expert: every expert with rows ends in a tile that is half full.
+// 14.7 us in one piece, 12.0 in four) and the workspace has room for the sums.  Rows
+// sorted by expert: every expert with rows ends in a tile that is half full, and
+// where there are tiles for all compute units the weights' stream counts, which
+// tiles of 32 channels hold up (1024 rows over 64 experts of 1024 x 2048: 31.8 us
+// against 25.8).
 template <bool GROUPED>
 Plan plan(const Product& p, size_t room) {
   const int64_t cus = device_cus();
@@ -1058,6 +1058,7 @@ Plan plan(const Product& p, size_t room) {
                                                   : static_cast<double>(p.M < p.experts ? p.M : p.experts);
     const double tiles = rows * static_cast<double>((p.N + t.BN - 1) / t.BN);
     if (i < kLargest && tile_groups<GROUPED>(p, t.BM, t.BN, 256) == 0) continue;
+    if (GROUPED && t.BN == 32 && tiles > cus) continue;
     const int most = GROUPED || i == kLargest ? 1 : kMaxSplits;
     for (int splits = 1; splits <= most; ++splits) {
       if (splits > 1 && (tiles * splits > cus || p.M * p.sums_pitch * 4 * splits > static_cast<int64_t>(room) ||
@@ -1089,12 +1090,24 @@ Product dense(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
   return p;
 }
 
-// Whether the row kernel takes the product: it reads an expert's weights once for
-// every 16 of its rows.
+// Whether the row kernel takes the product: it reads weights once for every 16 rows.
+// Dense: 16 x 4096 x 4096 in 6.7 us, 8.4 in tiles; up to 48 rows where rows are short
+// and a workgroup has two tiles at most (32 x 4096 x 4096 in 8.2 us against 9.4, 48 x
+// 1024 x 4096 in 4.6 against 6.1; 48 x 4096 x 4096 would take 11.4 against 8.5, 17 x
+// 4096 x 11008 23.5 against 15.2).  By expert: with 64 experts of 4096 x 2048 two rows
+// each on average take 96 us against 107, four 103 against 111, six 114 against 110,
+// sixteen 157 against 111 (any with more than 16 is read twice); with fewer tiles
+// than compute units its shorter start counts to ten rows (16 experts of 256 x 512:
+// 4.5 us against 5.0).
 template <bool GROUPED>
 bool few(const Product& p) {
-  const int64_t rows = GROUPED ? p.M / p.experts : p.M;
-  return rows <= 16 && p.pitch > 0 && p.pitch <= kRowMaxPitch && row_tiles<GROUPED>(p, 16) <= 65535;
+  if (p.pitch <= 0 || p.pitch > kRowMaxPitch || row_tiles<GROUPED>(p, 16) > 65535) return false;
+  const int64_t cus = device_cus();
+  if (GROUPED) {
+    const int64_t rows = p.M / p.experts;
+    return rows <= 4 || (rows <= 10 && p.experts * ((p.N + 63) / 64) <= cus);
+  }
+  return p.M <= 16 || (p.M <= 48 && p.pitch <= 4096 && row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16) <= 2 * cus);
 }
 
 template <bool GROUPED>

@@ -40,10 +40,13 @@ struct RowScale {
 };
 
 // Of a row's largest magnitude; NaN and 0 for a row that is not finite, whose
-// codes are then all zero.
+// codes are then all zero.  Both by products with a rounded reciprocal: what the
+// tensor expressions a / 127 and 127 / a compute on this device, so that a program
+// that encodes with those gets the same codes, ties such as a / 2 included (1 ulp
+// from the quotients' own rounding).
 __device__ __forceinline__ RowScale row_scale(uint32_t peak) {
   const float a = fmaxf(__builtin_bit_cast(float, peak), 0x1p-100f);
-  RowScale s = {a / 127.0f, 127.0f / a};
+  RowScale s = {a * (1.0f / 127.0f), 127.0f * (1.0f / a)};
   if (peak >= 0x7F800000u) s = {__builtin_nanf(""), 0.0f};
   return s;
 }

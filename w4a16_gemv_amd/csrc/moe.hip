@@ -27,7 +27,8 @@ using namespace rowio;
 //
 // Up to one tile one workgroup does it all in one launch.  Beyond, a first
 // kernel writes each workgroup's counts per expert to the workspace and a
-// second one adds those of the workgroups before it to its own.
+// second one adds those of the workgroups before it to its own.  Latency bounds both:
+// 64 slots over 64 experts take 4.3 us, 32764 take 4.6 + 8.5.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -211,20 +212,25 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Rows.  2^WIDTH threads of a workgroup per token: all 256, or for short rows as
+// Rows.  2^width threads of a workgroup per token: all 256, or for short rows as
 // many as there are pieces of eight (at most a wave, so that a token's sums stay
 // within one).  Each row of the batch is read once and each sorted row read or
 // written once; all three kernels are bound by memory: 8191 tokens of 4096 bf16
-// with four slots gather in 71 us and combine in 71 (4.7 TB/s), and 8192 give
-// their gradients in 130 us (combine) and 67 (gather).
+// with four slots, a tenth of them dropped, gather in 48-63 us (309 MB) and combine
+// in 62 (5.0 TB/s), and 8192 with all slots give their gradients in 104-121 us
+// (combine, 604 MB) and 64 (gather, 5.2 TB/s); a large copy reaches 4.9.
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 constexpr int64_t kMaxRowGroups = 1 << 20;  // a grid may not have 2^32 threads: past this, several turns
 
+// Up to two pieces a lane a wave does better than the workgroup (8192 tokens with
+// four slots combine rows of 64 in 4.9 us against 10.3, of 640 in 13.3 against 17.2,
+// of 1024 in 16.6 against 19.0), with more it does not (gradients at 1536 54.7 against
+// 43.4, at 2048 76 against 54).
 int row_width(int64_t H) {
-  if (H > 8 * 64) return 8;
+  if (H > 16 * 64) return 8;
   int width = 3;
-  while ((8 << width) < H) ++width;
+  while (width < 6 && (8 << width) < H) ++width;
   return width;
 }
 
@@ -303,8 +309,8 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(RowArgs args, const
     });
 }
 
-// The sorted rows are read past the caches: 66 us with, 52 without, for 8192
-// tokens.  (Rows that gather writes gain nothing from that.)
+// The sorted rows are read past the caches: 62 us for 8191 tokens of 4096 with four
+// slots, 87 through them.  (Rows that gather writes gain nothing from that.)
 template <int DT, bool WIDE>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowArgs args, const void* __restrict__ ys,
                                                               const float* __restrict__ weights,
