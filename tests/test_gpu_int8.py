@@ -286,7 +286,8 @@ def gpu_product(x, w, dtype):
 TILINGS = [(17, 7, 64), (40, 500, 700), (33, 4099, 64), (120, 4100, 256), (100, 4099, 64), (128, 4096, 300), (200, 4099, 64),
            (513, 4100, 1000), (2049, 1000, 64), (1030, 4100, 640), (4100, 4099, 1501), (4096, 4096, 2048), (2000, 4001, 2048),
            (17, 7, 8192), (60, 64, 11000), (500, 30, 8192), (33, 1000, 8192), (65, 1000, 8192), (130, 513, 20000),
-           (65, 2100, 8192), (18, 64, 131071), (33, 1500, 8192), (47, 1030, 4096), (48, 130, 4100)]
+           (65, 2100, 8192), (18, 64, 131071), (33, 1500, 8192), (47, 1030, 4096), (48, 130, 4100),
+           (17, 7, 12000), (17, 4099, 64), (250, 600, 11300), (1030, 7, 20000), (511, 260, 4100), (8191, 1, 64)]
 
 
 @pytest.mark.parametrize("M,N,K", TILINGS)
@@ -306,7 +307,7 @@ def test_gemm_tilings(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 333, 700), (2, 64, 5000), (2, 50, 11264), (7, 333, 700), (16, 100, 2048), (16, 70, 4096), (5, 130, 11264),
-                                   (13, 64, 11265), (90, 131, 700), (30, 64, 9000)])
+                                   (13, 64, 11265), (90, 131, 700), (30, 64, 9000), (60, 64, 11300), (130, 1031, 700), (300, 1500, 130)])
 def test_gemm_alignment(M, N, K):
     """Codes aligned to 16 bytes and no more, outputs to one element."""
     rng = np.random.default_rng(M * N + K)

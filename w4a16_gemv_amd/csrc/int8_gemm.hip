@@ -981,6 +981,10 @@ nf4_status launch_rows(const Product& p, int32_t y_dtype, hipStream_t st) {
   return launch_status();
 }
 
+// Rows whose codes and weights leave room for two workgroups on a compute unit: eight
+// units of 64 bytes a wave.
+constexpr int64_t kShortPitch = 8 * 64 * kRowWaves;
+
 constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
 
 // Whether the product goes to the single tokens' kernel, which quantizes on the
@@ -1091,10 +1095,12 @@ Product dense(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
 }
 
 // Whether the row kernel takes the product: it reads weights once for every 16 rows.
-// Dense: 16 x 4096 x 4096 in 6.7 us, 8.4 in tiles; up to 48 rows where rows are short
-// and a workgroup has two tiles at most (32 x 4096 x 4096 in 8.2 us against 9.4, 48 x
-// 1024 x 4096 in 4.6 against 6.1; 48 x 4096 x 4096 would take 11.4 against 8.5, 17 x
-// 4096 x 11008 23.5 against 15.2).  By expert: with 64 experts of 4096 x 2048 two rows
+// Dense: 16 x 4096 x 4096 in 6.7 us, 8.4 in tiles; more rows where every workgroup that
+// the card holds at a time (two to a compute unit, one where rows are long) has one
+// tile of 16 x 16 at most, whose start is shorter than a larger tile's: 32 x 4096 x
+// 4096 in 8.3 us against 9.3, 64 x 1024 x 4096 in 4.2 against 6.4, 32 x 2048 x 11008
+// in 10.3 against 12.4, 512 x 256 x 4096 in 5.6 against 6.3; 48 x 4096 x 4096 would
+// take 11.4 against 8.5, 17 x 4096 x 11008 23.5 against 15.2.  By expert: with 64 experts of 4096 x 2048 two rows
 // each on average take 96 us against 107, four 103 against 111, six 114 against 110,
 // sixteen 157 against 111 (any with more than 16 is read twice); with fewer tiles
 // than compute units its shorter start counts to ten rows (16 experts of 256 x 512:
@@ -1107,7 +1113,7 @@ bool few(const Product& p) {
     const int64_t rows = p.M / p.experts;
     return rows <= 4 || (rows <= 10 && p.experts * ((p.N + 63) / 64) <= cus);
   }
-  return p.M <= 16 || (p.M <= 48 && p.pitch <= 4096 && row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16) <= 2 * cus);
+  return p.M <= 16 || row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16) <= (p.pitch <= kShortPitch ? 2 : 1) * cus;
 }
 
 template <bool GROUPED>
