@@ -287,7 +287,8 @@ TILINGS = [(17, 7, 64), (40, 500, 700), (33, 4099, 64), (120, 4100, 256), (100, 
            (513, 4100, 1000), (2049, 1000, 64), (1030, 4100, 640), (4100, 4099, 1501), (4096, 4096, 2048), (2000, 4001, 2048),
            (17, 7, 8192), (60, 64, 11000), (500, 30, 8192), (33, 1000, 8192), (65, 1000, 8192), (130, 513, 20000),
            (65, 2100, 8192), (18, 64, 131071), (33, 1500, 8192), (47, 1030, 4096), (48, 130, 4100),
-           (17, 7, 12000), (17, 4099, 64), (250, 600, 11300), (1030, 7, 20000), (511, 260, 4100), (8191, 1, 64)]
+           (17, 7, 12000), (17, 4099, 64), (250, 600, 11300), (1030, 7, 20000), (511, 260, 4100), (8191, 1, 64),
+           (65, 1000, 40000), (65, 4099, 12000), (17, 2100, 8192)]
 
 
 @pytest.mark.parametrize("M,N,K", TILINGS)

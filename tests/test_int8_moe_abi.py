@@ -191,6 +191,10 @@ def test_binding_refuses_shapes_and_types_first():
         amd.int8_quantize(torch.zeros(4, 64, dtype=torch.float64))
     with pytest.raises(ValueError, match="dimension"):
         amd.int8_quantize(torch.tensor(1.0))
+    with pytest.raises(ValueError, match="requires a gradient"):
+        amd.int8_quantize(torch.zeros(4, 64, requires_grad=True))
+    with torch.no_grad(), pytest.raises(ValueError, match="on the GPU"):
+        amd.int8_quantize(torch.zeros(4, 64, requires_grad=True))
     for ids in (torch.zeros(4, dtype=torch.int32), torch.zeros(4, 0, dtype=torch.int32)):
         with pytest.raises(ValueError, match="top_k"):
             amd.moe_sort(ids, 8)

@@ -3,7 +3,8 @@ channel, int32 sums.
 
 Argument marshalling only, as in _binding.py; work goes on torch's current
 stream of the tensors' device, whichever device is current.  Nothing here is
-recorded by autograd.
+recorded by autograd: tensors that require a gradient are refused while
+gradients are being recorded.
 """
 from __future__ import annotations
 
@@ -29,6 +30,9 @@ def _on(dev: torch.device, t: torch.Tensor, name: str) -> None:
 
 def _gpu(t: torch.Tensor, name: str) -> int:
     """The pointer of a contiguous GPU tensor (of a type that was checked)."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which autograd would not see; call this under "
+                         "torch.no_grad() or in a Function")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if not t.is_contiguous():

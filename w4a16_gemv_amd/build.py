@@ -50,6 +50,13 @@ NO_SPILL = (
     "dequant_vec_kernel<1, 4, 0>",
     "gemv_stream_kernel<4, 1, 4, 4, 0, true, 2, true>",
     "gemv_stream_kernel<8, 2, 4, 2, 0, true, 2, true>",
+    "tile_kernel<0, false, ",
+    "tile_kernel<0, true, ",
+    "::stream_kernel<0, false, ",
+    "::row_kernel<0, ",
+    "::dot_kernel<0, 0, 1, ",
+    "quantize_rows_kernel<0, ",
+    "combine_grad_kernel<0, ",
 )
 RESOURCES = os.path.join(PKG, "kernel_resources.txt")
 REMARKS = "-Rpass-analysis=kernel-resource-usage"

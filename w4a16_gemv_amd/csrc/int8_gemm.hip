@@ -447,7 +447,10 @@ __device__ __forceinline__ void store_four(void* y, int64_t i, int left, const f
 // weights, two at a time, 1024 contiguous bytes to a load, and multiplies them
 // by the tokens' codes, which its workgroup keeps in LDS, with v_dot4_i32_i8;
 // the lanes' sums are added at a row's end.  The weights of the next two rows
-// are asked for as soon as the registers are free.
+// are asked for as soon as the registers are free.  Bound by the weights' stream and
+// a start of about 2 us: quantization included, 1 x 4096 x 4096 takes 6.6 us and 1 x
+// 11008 x 4096 11.1 (a plain read of those weights 4.6 and 8.8), two launches 8.9 and
+// 14.0.
 //
 // XT is the tokens' type.  Codes (kCodes) are copied to LDS; tokens of other
 // types are quantized on the way there, after the workgroup's first weights have
@@ -988,7 +991,10 @@ constexpr int64_t kShortPitch = 8 * 64 * kRowWaves;
 constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
 
 // Whether the product goes to the single tokens' kernel, which quantizes on the
-// way where it is given values.
+// way where it is given values: 2 x 4096 x 4096 in 7.6 us against 9.2 in two launches,
+// 2 x 4096 x 11008 in 16.7 against 17.5; four tokens would take 15.0 against 14.4 at
+// 11008 x 4096 and 23.5 against 17.6 at 4096 x 11008.  Longer rows would not fit the
+// registers that are asked for ahead.
 bool single(int64_t M, int64_t K) { return M <= kDotTokens && K > 0 && pitch_of(K) <= kDotBlocks * 1024; }
 
 template <int XT, int DT, int MT>
@@ -1034,7 +1040,7 @@ constexpr Tiling kTilings[] = {{32, 32, 0.16f, 0.125f, 0.0f}, {64, 32, 0.215f, 0
                                {64, 64, 0.28f, 0.255f, 0.0f}, {128, 64, 0.35f, 0.47f, 0.0f},
                                {128, 128, 0.55f, 0.69f, 0.0f}, {256, 256, 1.05f, 1.6f, 4.0f}};
 constexpr int kLargest = 5;
-constexpr float kLaunchUs = 3.0f, kJoinUs = 4.5f;
+constexpr float kLaunchUs = 3.0f, kJoinUs = 4.5f, kSumUs = 8.0f / 3e6f;  // a sum there and back
 constexpr int kMaxSplits = 16;
 
 struct Plan {
@@ -1042,8 +1048,10 @@ struct Plan {
 };
 
 // The tiling with the least time by the figures above, with K split over
-// workgroups where that leaves compute units without a tile (64 x 1024 x 11008:
-// 14.7 us in one piece, 12.0 in four) and the workspace has room for the sums.  Rows
+// workgroups where that leaves compute units without a tile and the workspace has
+// room for the sums (128 x 1024 x 11008: 15.2 us in one piece, 12.9 in six; 88 x 999
+// x 34756: 39 and 20 in seven), unless writing and reading the sums costs as much
+// (65 x 2100 x 8192: 11 us in one piece, 21 in thirteen).  Rows
 // sorted by expert: every expert with rows ends in a tile that is half full, and
 // where there are tiles for all compute units the weights' stream counts, which
 // tiles of 32 channels hold up (1024 rows over 64 experts of 1024 x 2048: 31.8 us
@@ -1073,7 +1081,7 @@ Plan plan(const Product& p, size_t room) {
       if (i == kLargest && part > 0 && part <= 0.5) turns -= 0.3;  // halves in the last
       const double more = t.each > t.alone ? t.each - t.alone : 0.0;
       const double step = full > 1 || turns < 1 ? turns * t.each : t.alone + more * full;
-      const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs : 0.0);
+      const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs + p.M * p.sums_pitch * splits * kSumUs : 0.0);
       if (us < least * (splits > 1 ? 0.85 : 1.0)) {
         least = us;
         best = {i, splits};
