@@ -288,7 +288,8 @@ TILINGS = [(17, 7, 64), (40, 500, 700), (33, 4099, 64), (120, 4100, 256), (100, 
            (17, 7, 8192), (60, 64, 11000), (500, 30, 8192), (33, 1000, 8192), (65, 1000, 8192), (130, 513, 20000),
            (65, 2100, 8192), (18, 64, 131071), (33, 1500, 8192), (47, 1030, 4096), (48, 130, 4100),
            (17, 7, 12000), (17, 4099, 64), (250, 600, 11300), (1030, 7, 20000), (511, 260, 4100), (8191, 1, 64),
-           (65, 1000, 40000), (65, 4099, 12000), (17, 2100, 8192)]
+           (65, 1000, 40000), (65, 4099, 12000), (17, 2100, 8192),
+           (4111, 4225, 1501), (4352, 4096, 1300), (8500, 2100, 1472)]
 
 
 @pytest.mark.parametrize("M,N,K", TILINGS)
@@ -499,7 +500,8 @@ def test_gemm_grouped(T, k, E, N, K, kind):
 
 @pytest.mark.parametrize("rows,E,N,K", [(100, 1, 40, 64), (1500, 30, 130, 64), (900, 12, 1000, 256), (600, 1, 1030, 64), (6000, 1, 130, 64),
                                         (2700, 30, 515, 64), (6000, 30, 1030, 1024), (4500, 3, 2100, 1024), (9000, 2, 2048, 1500), (520, 64, 300, 128), (300, 30, 1000, 64),
-                                        (200, 20, 130, 64), (1000, 64, 200, 192)])
+                                        (200, 20, 130, 64), (1000, 64, 200, 192),
+                                        (4400, 3, 4000, 1501), (8000, 2, 2300, 1500), (9300, 5, 2000, 1400)])
 def test_gemm_grouped_tilings(rows, E, N, K):
     """Sizes of each tiling; uneven experts, slots dropped, k = 2."""
     rng = np.random.default_rng(rows + E + N)

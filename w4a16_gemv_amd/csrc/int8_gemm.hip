@@ -263,16 +263,20 @@ __device__ __forceinline__ i32x4 range_words(const void* p, uint32_t bytes) {
 }
 typedef const __attribute__((address_space(1))) void* GlobalPtr;
 
-// How many of `all` tiles are computed whole where the rest, less than half a turn
-// of the compute units, is computed in halves.
+// How many of `all` tiles are computed whole where the rest, half a turn of the
+// compute units at most, is computed in pieces.
 __device__ __host__ __forceinline__ uint32_t whole_tiles(uint32_t all, uint32_t cus) {
   const uint32_t rest = all % cus;
   return 2 * rest <= cus ? all - rest : all;
 }
 
+// Whether that rest is computed in quarters of 128 x 128 (stream_kernel): where the
+// compute units hold them in one turn.
+__device__ __host__ __forceinline__ bool in_quarters(uint32_t rest, uint32_t cus) { return 4 * rest <= cus; }
+
 // Which tiles of 256 x 256 a launch computes: those that whole_tiles() counts, or
-// the others, in halves of 128 tokens.
-enum Share { kWhole, kHalves };
+// the others, in halves of 128 tokens or in quarters.
+enum Share { kWhole, kHalves, kQuarters };
 
 template <int DT, bool GROUPED, Share SHARE>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(Product p) {
   uint32_t index, half = 0, tm, tn;
   const uint32_t all = tiles_m * tiles_n, whole = whole_tiles(all, p.cus);
   if constexpr (SHARE == kHalves) {
-    if (!tile_of_group(blockIdx.x, 2 * (all - whole), index)) return;
+    if (in_quarters(all - whole, p.cus) || !tile_of_group(blockIdx.x, 2 * (all - whole), index)) return;
     half = index & 1;
     index = whole + index / 2;
   } else {
@@ -706,7 +710,7 @@ __device__ __forceinline__ void lds_load(uint32_t to, const int8_t* from) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
 }
 
-template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES>
+template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES, bool QUARTERS = false>
 __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   constexpr int kWaves = WM * WN * WK, kThreads = 64 * kWaves;
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
@@ -720,15 +724,31 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
   __shared__ __attribute__((aligned(256))) int8_t s_out[WM * WN * 32 * 32 * TN * kB];
   __shared__ __attribute__((aligned(256))) i32x4 s_meet[WK > 1 ? (WK - 1) * WM * WN * 256 : 1];
 
-  const uint32_t tiles_n = static_cast<uint32_t>((p.N + BN - 1) / BN);
-  uint32_t tiles_m = static_cast<uint32_t>((p.M + BM - 1) / BM);
-  if constexpr (GROUPED) tiles_m = count_tiles<BM>(p);
-  uint32_t index, tm, tn;
-  if (!tile_of_group(blockIdx.x, tiles_m * tiles_n, index)) return;
+  // tiles of its own, or quarters of the large ones
+  constexpr int kM = QUARTERS ? 2 * BM : BM, kN = QUARTERS ? 2 * BN : BN;
+  static_assert(!QUARTERS || (kM == kTile && kN == kTile));
+  const uint32_t tiles_n = static_cast<uint32_t>((p.N + kN - 1) / kN);
+  uint32_t tiles_m = static_cast<uint32_t>((p.M + kM - 1) / kM);
+  if constexpr (GROUPED) tiles_m = count_tiles<kM>(p);
+  uint32_t index, quarter = 0, tm, tn;
+  const uint32_t all = tiles_m * tiles_n;
+  if constexpr (QUARTERS) {
+    const uint32_t whole = whole_tiles(all, p.cus);
+    if (!in_quarters(all - whole, p.cus) || !tile_of_group(blockIdx.x, 4 * (all - whole), index)) return;
+    quarter = index & 3;
+    index = whole + index / 4;
+  } else {
+    if (!tile_of_group(blockIdx.x, all, index)) return;
+  }
   locate_tile(index, tiles_m, tiles_n, tm, tn);
-  RowTile t = {static_cast<int64_t>(tm) * BM, min(p.M, static_cast<int64_t>(tm) * BM + BM), 0};
-  if constexpr (GROUPED) t = find_tile<BM>(p, tm);
-  const int64_t n0 = static_cast<int64_t>(tn) * BN;
+  RowTile t = {static_cast<int64_t>(tm) * kM, min(p.M, static_cast<int64_t>(tm) * kM + kM), 0};
+  if constexpr (GROUPED) t = find_tile<kM>(p, tm);
+  const int64_t n0 = static_cast<int64_t>(tn) * kN + (quarter & 1) * BN;
+  if constexpr (QUARTERS) {
+    t.first += (quarter >> 1) * BM;
+    t.end = min(t.end, t.first + BM);
+    if (t.end <= t.first || n0 >= p.N) return;
+  }
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = 8 * wave + (lane >> 3);
@@ -923,24 +943,32 @@ uint32_t tile_groups(const Product& p, int BM, int BN, int threads) {
 template <bool GROUPED, Share SHARE>
 void launch_share(const Product& p, int32_t y_dtype, uint32_t groups, hipStream_t st) {
   with_dtype(y_dtype, [&](auto d) {
-    hipLaunchKernelGGL((tile_kernel<decltype(d)::value, GROUPED, SHARE>), dim3(groups), dim3(kTileThreads), 0,
-                       st, p);
+    constexpr int DT = decltype(d)::value;
+    if constexpr (SHARE == kQuarters)
+      hipLaunchKernelGGL((stream_kernel<DT, GROUPED, 2, 2, 1, 2, 2, 4, true>), dim3(groups), dim3(256), 0, st, p);
+    else
+      hipLaunchKernelGGL((tile_kernel<DT, GROUPED, SHARE>), dim3(groups), dim3(kTileThreads), 0, st, p);
   });
 }
 
-// Tiles of 256 x 256.  A last turn of the compute units that is less than half
-// full is computed in halves of 128 tokens, in a second launch: 8192 x 11008 x
-// 4096 has 1376 tiles, five turns of 256 and 96 (342 us whole, 330 so).
+// Tiles of 256 x 256.  A last turn of the compute units that is half full at most is
+// computed in halves of 128 tokens, in a second launch (8192 x 11008 x 4096 has 1376
+// tiles, five turns of 256 and 96: 342 us whole, 331 so, 340 in quarters), and one
+// that is a quarter full at most in quarters, by the kernel for smaller tiles (4352 x
+// 4096 x 4096 with 272: 92 us in halves, 81 so; 576 tiles of eight experts' 4096 x
+// 4096: 162 and 154).  For experts each launch that finds nothing to do costs 1.7 us.
 template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
   const uint32_t groups = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
   if (groups == 0) return NF4_EUNSUPPORTED;
-  // how many tiles experts' rows make only the GPU knows: both launches find out
+  // how many tiles experts' rows make only the GPU knows: the launches find out
   const int64_t all = row_tiles<GROUPED>(p, kTile) * ((p.N + kTile - 1) / kTile);
   const uint32_t whole = whole_tiles(static_cast<uint32_t>(all), p.cus);
   if (GROUPED || whole > 0) launch_share<GROUPED, kWhole>(p, y_dtype, groups, st);
-  if (GROUPED || whole < all)
-    launch_share<GROUPED, kHalves>(p, y_dtype, (p.cus + kDies - 1) / kDies * kDies, st);
+  const uint32_t rest = static_cast<uint32_t>(all) - whole, turn = (p.cus + kDies - 1) / kDies * kDies;
+  const bool quarters = in_quarters(rest, p.cus);
+  if (GROUPED || (rest > 0 && !quarters)) launch_share<GROUPED, kHalves>(p, y_dtype, turn, st);
+  if (GROUPED || (rest > 0 && quarters)) launch_share<GROUPED, kQuarters>(p, y_dtype, turn, st);
   return launch_status();
 }
 
@@ -1078,7 +1106,7 @@ Plan plan(const Product& p, size_t room) {
         break;
       const double full = tiles * splits / cus, part = full - std::floor(full);
       double turns = std::ceil(full);
-      if (i == kLargest && part > 0 && part <= 0.5) turns -= 0.3;  // halves in the last
+      if (i == kLargest && part > 0 && part <= 0.5) turns -= full > 1 && part <= 0.25 ? 0.6 : 0.3;  // in pieces
       const double more = t.each > t.alone ? t.each - t.alone : 0.0;
       const double step = full > 1 || turns < 1 ? turns * t.each : t.alone + more * full;
       const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs + p.M * p.sums_pitch * splits * kSumUs : 0.0);
