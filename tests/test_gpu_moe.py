@@ -41,7 +41,8 @@ SORTS = [(1, 1, 1, "all"), (1, 2, 8, "all"), (0, 2, 8, "all"), (16, 4, 64, "all"
          (65, 1, 1, "all"), (128, 8, 1024, "all"), (100, 3, 7, "far"), (50, 2, 9, "none"), (511, 2, 5, "one"), (1000, 4, 64, "drop"),
          (1024, 4, 16, "all"), (1025, 4, 16, "all"), (4097, 1, 33, "drop"), (8191, 4, 64, "drop"), (3000, 8, 1024, "all"),
          (20000, 2, 1, "all"), (30000, 3, 100, "one"), (9000, 1, 6, "none"), (5000, 2, 0, "all"), (4, 2, 0, "all"),
-         (300000, 4, 128, "drop")]
+         (300000, 4, 128, "drop"), (1024, 1, 16, "drop"), (1025, 1, 16, "drop"), (512, 4, 1024, "drop"), (2049, 1, 40, "far"),
+         (4096, 1, 7, "drop"), (2049, 2, 64, "drop"), (8192, 4, 64, "drop"), (32769, 1, 12, "far"), (16383, 2, 1024, "all")]
 
 
 @pytest.mark.parametrize("T,k,E,kind", SORTS)

@@ -19,21 +19,21 @@ using namespace rowio;
 // ---------------------------------------------------------------------------
 // Sort.  A stable counting sort: the row of a slot is the number of slots with
 // a smaller expert, plus those of its expert before it.  A workgroup of 16
-// waves takes a tile of 4096 slots, wave w the 256 from 256 w on, 64 at a time:
-// the lanes of a wave find those with their own expert by one ballot per bit
+// waves takes a tile of 1024 STEPS slots, wave w the 64 STEPS from 64 STEPS w on, 64
+// at a time: the lanes of a wave find those with their own expert by one ballot per bit
 // of the id, which gives the rank among the 64; counters per wave and expert
 // in LDS carry it on.  After the tile, a sum over the waves and one over the
 // experts turn the counters into rows.
 //
-// Up to one tile one workgroup does it all in one launch.  Beyond, a first
+// Up to kSortOne slots one workgroup does it all in one launch.  Beyond, a first
 // kernel writes each workgroup's counts per expert to the workspace and a
 // second one adds those of the workgroups before it to its own.  Latency bounds both:
-// 64 slots over 64 experts take 4.3 us, 32764 take 4.6 + 8.5.
+// 64 slots over 64 experts take 3.2 us, 32764 take 10.7 (a gap between the launches
+// among it), 524288 38.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kSortSteps = 4;
-constexpr int kSortTile = kSortThreads * kSortSteps;
+constexpr int kSortOne = 4 * kSortThreads;
 constexpr int kMaxSortGroups = 256;
 constexpr int kMaxExperts = 1024;
 constexpr int64_t kMaxSlots = int64_t(1) << 30;
@@ -55,13 +55,14 @@ __device__ __forceinline__ int slot_expert(const void* ids, int id_bytes, int64_
 
 // Ranks the tile's slots within (wave, expert) and leaves the counters in
 // s.count.
-__device__ __forceinline__ void rank_tile(SortShared& s, const int (&e)[kSortSteps],
-                                          int (&rank)[kSortSteps], int experts, int bits) {
+template <int STEPS>
+__device__ __forceinline__ void rank_tile(SortShared& s, const int (&e)[STEPS], int (&rank)[STEPS], int experts,
+                                          int bits) {
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   for (int i = lane; i < experts; i += 64) s.count[wave][i] = 0;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-  for (int t = 0; t < kSortSteps; ++t) {
+  for (int t = 0; t < STEPS; ++t) {
     uint64_t same = __ballot(e[t] >= 0);
     for (int b = 0; b < bits; ++b) {
       const uint64_t set = __ballot((e[t] >> b) & 1);
@@ -131,10 +132,11 @@ struct SortArgs {
   int64_t per_group;   // slots of a workgroup, a multiple of the tile
 };
 
-__device__ __forceinline__ void load_tile(const SortArgs& a, int64_t tile, int (&e)[kSortSteps]) {
-  const int64_t first = tile + (threadIdx.x >> 6) * (64 * kSortSteps) + (threadIdx.x & 63);
+template <int STEPS>
+__device__ __forceinline__ void load_tile(const SortArgs& a, int64_t tile, int (&e)[STEPS]) {
+  const int64_t first = tile + (threadIdx.x >> 6) * (64 * STEPS) + (threadIdx.x & 63);
 #pragma unroll
-  for (int t = 0; t < kSortSteps; ++t)
+  for (int t = 0; t < STEPS; ++t)
     e[t] = slot_expert(a.ids, a.id_bytes, first + 64 * t, a.n, a.experts);
 }
 
@@ -154,10 +156,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs a) {
 }
 
 // ONE: the only workgroup, of a single tile; its own counts are the totals.
-template <bool ONE>
+template <bool ONE, int STEPS>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
   __shared__ SortShared s;
-  int e[kSortSteps], rank[kSortSteps];
+  int e[STEPS], rank[STEPS];
   const int wave = threadIdx.x >> 6;
   const int64_t begin = ONE ? 0 : a.per_group * blockIdx.x;
   const int64_t end = ONE ? a.n : min(a.n, begin + a.per_group);
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
       if (blockIdx.x == 0) a.offsets[threadIdx.x] = static_cast<int32_t>(row);
     }
   }
-  for (int64_t tile = begin; tile < end || (ONE && tile == 0); tile += kSortTile) {
+  for (int64_t tile = begin; tile < end || (ONE && tile == 0); tile += STEPS * kSortThreads) {
     load_tile(a, tile, e);
     rank_tile(s, e, rank, a.experts, a.bits);
     __syncthreads();
@@ -188,9 +190,9 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs a) {
       }
     }
     __syncthreads();
-    const int64_t first = tile + wave * (64 * kSortSteps) + (threadIdx.x & 63);
+    const int64_t first = tile + wave * (64 * STEPS) + (threadIdx.x & 63);
 #pragma unroll
-    for (int t = 0; t < kSortSteps; ++t) {
+    for (int t = 0; t < STEPS; ++t) {
       const int64_t i = first + 64 * t;
       if (i >= a.n) continue;
       int row = -1;
@@ -411,10 +413,19 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(RowArgs args,
   }
 }
 
+// Steps of a workgroup's tile.  One workgroup: no more than the slots fill (64 slots in
+// 3.2 us, with four steps 4.7).  Several: two for few slots, which more workgroups
+// then share (8192 in 7.5 us against 9.1, 32764 in 10.7 against 11.1), four for many,
+// whose workgroups would be too many to add up (131072 in 16.8 against 21.1).
+int sort_steps(int64_t n) {
+  if (n <= kSortOne) return n <= kSortThreads ? 1 : n <= 2 * kSortThreads ? 2 : 4;
+  return n <= 32768 ? 2 : 4;
+}
+
 int64_t sort_groups(int64_t n, int64_t* per_group) {
-  const int64_t tiles = (n + kSortTile - 1) / kSortTile;
+  const int64_t tile = int64_t(sort_steps(n)) * kSortThreads, tiles = (n + tile - 1) / tile;
   const int64_t per = (tiles + kMaxSortGroups - 1) / kMaxSortGroups;
-  *per_group = per * kSortTile;
+  *per_group = per * tile;
   return (tiles + per - 1) / per;
 }
 
@@ -436,7 +447,7 @@ extern "C" {
 
 size_t moe_sort_workspace_size(int64_t T, int32_t top_k, int32_t experts) {
   if (T <= 0 || top_k < 1 || experts < 1 || experts > kMaxExperts || !slots_fit(T, top_k)) return 0;
-  if (T * top_k <= kSortTile) return 0;
+  if (T * top_k <= kSortOne) return 0;
   int64_t per = 0;
   return static_cast<size_t>(sort_groups(T * top_k, &per)) * experts * sizeof(uint32_t);
 }
@@ -455,14 +466,21 @@ nf4_status moe_sort(const void* ids, int32_t id_bytes, int64_t T, int32_t top_k,
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   SortArgs a = {ids, id_bytes, T * top_k, experts, 0, offsets, order, pos, nullptr, 0};
   while ((1 << a.bits) < experts) ++a.bits;
-  if (a.n <= kSortTile) {
-    hipLaunchKernelGGL((sort_place_kernel<true>), dim3(1), dim3(kSortThreads), 0, st, a);
+  if (a.n <= kSortOne) {
+    switch (sort_steps(a.n)) {
+      case 1: hipLaunchKernelGGL((sort_place_kernel<true, 1>), dim3(1), dim3(kSortThreads), 0, st, a); break;
+      case 2: hipLaunchKernelGGL((sort_place_kernel<true, 2>), dim3(1), dim3(kSortThreads), 0, st, a); break;
+      default: hipLaunchKernelGGL((sort_place_kernel<true, 4>), dim3(1), dim3(kSortThreads), 0, st, a);
+    }
     return launch_status();
   }
   const uint32_t groups = static_cast<uint32_t>(sort_groups(a.n, &a.per_group));
   a.counts = static_cast<uint32_t*>(workspace);
   hipLaunchKernelGGL(sort_count_kernel, dim3(groups), dim3(kSortThreads), 0, st, a);
-  hipLaunchKernelGGL((sort_place_kernel<false>), dim3(groups), dim3(kSortThreads), 0, st, a);
+  if (sort_steps(a.n) == 2)
+    hipLaunchKernelGGL((sort_place_kernel<false, 2>), dim3(groups), dim3(kSortThreads), 0, st, a);
+  else
+    hipLaunchKernelGGL((sort_place_kernel<false, 4>), dim3(groups), dim3(kSortThreads), 0, st, a);
   return launch_status();
 }
 
