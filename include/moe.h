@@ -52,7 +52,9 @@ size_t moe_sort_workspace_size(int64_t T, int32_t top_k, int32_t experts);
  *  x             : device [T][H] of type dtype, contiguous.
  *  pos           : device int32 [T][top_k]; entries outside [0, rows) are
  *                  dropped slots.
- *  rows          : rows of xs.  Rows that no slot names are left as they were.
+ *  rows          : rows of xs.  Rows that no slot names are left as they were;
+ *                  a row that two slots name (moe_sort gives none) holds
+ *                  values of either.
  *  H             : 0 <= H < 2^31.
  * xs must not overlap x.  Returns NF4_EINVAL for negative sizes, an unknown
  * type, NULL or misaligned pointers; NF4_EUNSUPPORTED for T * top_k > 2^30 or
@@ -77,8 +79,8 @@ nf4_status moe_combine(const void* ys, int32_t dtype, const float* weights, cons
  * moe_combine_grad -- the gradients of moe_combine: for every slot with a row
  *     dys[pos[t][j]] = weights[t][j] * dy[t]        (rounded once to dtype)
  *     dweights[t][j] = sum_h ys[pos[t][j]][h] * dy[t][h]     (fp32 sums)
- * and dweights = 0 for a dropped slot; rows of dys that no slot names are
- * left as they were.  The order of each sum is fixed.
+ * and dweights = 0 for a dropped slot; rows of dys that no slot names, or two,
+ * are as in moe_gather.  The order of each sum is fixed.
  *  dy            : device [T][H];  ys, dys : device [rows][H]; of type dtype.
  *  weights       : device fp32 [T][top_k], or NULL for ones.
  *  dys, dweights : either may be NULL (not wanted); ys is read only for

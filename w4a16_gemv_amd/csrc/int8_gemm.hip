@@ -604,7 +604,11 @@ __global__ __launch_bounds__(kDotThreads, 4) void dot_kernel(Product p, const vo
 //
 // Bound by the weights' stream: 13 x 11008 x 4096 takes 11.6 us (45 MB, a plain
 // read of which takes 8.8), or 13.0 with each lane loading what it multiplies,
-// where four lanes read four rows.  The one- and two-token kernel at more tokens
+// where four lanes read four rows; 16 tokens' 41 of 64 experts of 1024 x 2048 take 25
+// from memory (86 MB).  Measured and not kept: two tiles of weights in flight (the
+// same times), the experts' tiles in equal shares over the workgroups (22 us for those
+// 41, but 37 against 28 for eight of 4096 x 4096: the turns between experts), three
+// to eight workgroups a compute unit (up to a third slower).  The one- and two-token kernel at more tokens
 // is slower from four on (12.0 against 11.1 us at 4 x 11008 x 4096).
 // ---------------------------------------------------------------------------
 constexpr int kRowWaves = 8;
