@@ -605,3 +605,65 @@ def test_captured_and_replayed():
             torch.cuda.synchronize()
             assert same(y, want) and same(z, want)
             assert same(amd.int8_linear(x, wt, out_dtype=F32), want)
+
+
+def test_captured_split_product():
+    """A product whose sums are split over workgroups, two kernels, replayed with other codes."""
+    rng = np.random.default_rng(19)
+    M, N, K = 128, 1024, 11008
+    assert amd.load().int8_gemm_workspace_size(M, N, K) > 0
+    _, _, w = random_tensor(rng, N, K)
+    x = amd.int8_quantize(torch.randn(M, K, device=dev()))
+    amd.int8_gemm(x, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = amd.int8_gemm(x, w)
+    for _ in range(4):
+        amd.int8_quantize(torch.randn(M, K, device=dev()), out=x)
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(y, gpu_product(x, w, BF))
+        assert same(amd.int8_gemm(x, w), y)
+
+
+def test_captured_grouped_tiles_follow_the_routing():
+    """Large tiles of a captured product: how many there are, and whether the last turn's are computed
+    whole, in halves or in quarters, follows each replay's routing."""
+    T, k, E, N, K = 2200, 2, 3, 4000, 1501
+    rng = np.random.default_rng(23)
+    _, _, w = random_tensor(rng, E * N, K)
+    _, _, x = random_tensor(rng, T, K)
+    ids = torch.from_numpy(rng.integers(0, E, (T, k))).to(dev())
+
+    def run(y):
+        plan = amd.moe_sort(ids, E)
+        return plan, amd.int8_gemm_grouped(x, w, plan, y=y)
+
+    y = torch.empty(T * k, N, dtype=BF, device=dev())
+    run(y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan, _ = run(y)
+    # tokens routed, and the share of slots sent to the first expert: from 18 row tiles (of 16 channel tiles) to none
+    for routed, share in ((T, 0.0), (T, 1.0), (1100, 0.0), (1650, 0.5), (3, 0.0), (0, 0.0)):
+        ids.random_(0, E)
+        ids[torch.rand(T, k, device=dev()) < share] = 0
+        ids[routed:] = -1
+        y.fill_(7.25)
+        graph.replay()
+        torch.cuda.synchronize()
+        offsets = plan.offsets.tolist()
+        assert offsets[E] == routed * k
+        for e in range(E):
+            a, b = offsets[e], offsets[e + 1]
+            token = plan.order[a:b].long() // k
+            xe = amd.Int8Tensor(x.data[token], x.scale[token], K)
+            we = amd.Int8Tensor(w.data[e * N:(e + 1) * N], w.scale[e * N:(e + 1) * N], K)
+            assert same(y[a:b], gpu_product(xe, we, BF)), (routed, e)
+        assert bool((y[offsets[E]:] == 7.25).all())
+        again = torch.full_like(y, 7.25)
+        run(again)
+        assert same(again, y)
