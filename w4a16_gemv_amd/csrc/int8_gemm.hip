@@ -705,14 +705,19 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void row_kernel(Pro
 // (one address per wave).  The builtins for these would do, but for the waits: the
 // compiler puts one for all of them before a loop's first LDS read, every time
 // round.  Nothing lands in a register, and arrive() in stream_kernel does all the
-// waiting.  (m0 holds the LDS address; nothing else in that kernel uses it.)
+// waiting.  m0 holds the LDS address.  It stands among the clobbers, so that the compiler
+// carries no value of its own in it across a load; the warning put off here says that
+// it does not save m0 around the statement either, which nothing asks for.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void lds_load(uint32_t to, i32x4 range, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(at), "s"(range)
-               : "memory");
+               : "m0", "memory");
 }
 __device__ __forceinline__ void lds_load(uint32_t to, const int8_t* from) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(to), "v"(from) : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES, bool QUARTERS = false>
 __global__ __launch_bounds__(64 * WM* WN* WK) void stream_kernel(Product p) {
