@@ -101,11 +101,16 @@ size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  * int8_linear -- int8_quantize of the activations followed by int8_gemm, with
  * the bits of those two calls (few rows take one launch instead of two).
  *  x, x_dtype    : device, M x K activations, contiguous, natural alignment.
- *  workspace     : DEVICE scratch, 256-byte aligned, any contents, of at
- *                  least int8_linear_workspace_size(M, N, K) bytes (may be
- *                  NULL where that is 0).  Used as in int8_gemm.
- * Everything else as in int8_gemm; also NF4_EINVAL for a workspace that is
- * too small.
+ *  workspace     : DEVICE scratch, 256-byte aligned, any contents (may be NULL
+ *                  where int8_linear_workspace_size is 0).  The codes and
+ *                  scales of the M rows need M * int8_pitch(K) bytes and
+ *                  4 * M, each rounded up to 256; what is left is used as in
+ *                  int8_gemm.  int8_linear_workspace_size bytes hold all that
+ *                  the product can use, and a workspace for one shape is large
+ *                  enough for every shape with no more rows and no larger K,
+ *                  without changing its bits.
+ * Everything else as in int8_gemm; also NF4_EINVAL for a workspace without
+ * room for the codes and scales.
  */
 nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const float* ws,
                        int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* workspace,

@@ -1,0 +1,37 @@
+"""What the headers and docstrings of the int8 products and of the routing promise
+beyond the values themselves, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+import w4a16_gemv_amd as amd
+from tests.test_gpu_int8 import BF, F32, dev, encode, product, random_tensor, same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    amd.load()
+
+
+# --- workspaces --------------------------------------------------------------
+
+@pytest.mark.parametrize("larger,shapes", [
+    ((139, 512, 8192), [(139, 512, 8192), (138, 512, 8192), (130, 512, 8000), (40, 512, 4097), (2, 512, 64), (1, 512, 0)]),
+    ((311, 512, 11008), [(310, 512, 11008), (128, 1024, 11008), (17, 4099, 300)]),
+    ((622, 256, 11008), [(621, 256, 11008), (65, 1000, 11000)])])
+def test_linear_takes_the_workspace_of_a_larger_shape(larger, shapes):
+    """A smaller M may split its sums more and so could use more room than the larger one has."""
+    work = amd.int8_linear_workspace(*larger)
+    assert any(amd.load().int8_linear_workspace_size(*s) > work.numel() for s in shapes)
+    rng = np.random.default_rng(sum(larger))
+    for M, N, K in shapes:
+        w, ws, wt = random_tensor(rng, N, K)
+        x = torch.from_numpy(rng.standard_normal((M, K))).to(BF)
+        work.fill_(255)
+        whole = torch.cat([work, torch.full((256,), 7, dtype=torch.uint8, device=dev())])
+        y = amd.int8_linear(x.to(dev()), wt, out_dtype=F32, workspace=whole[:work.numel()])
+        assert same(y + 0.0, product(*encode(x), w, ws, F32) + 0.0), (M, N, K)
+        assert bool((whole[work.numel():] == 7).all())

@@ -179,13 +179,16 @@ def _out(y, rows: int, N: int, dtype: torch.dtype, dev: torch.device):
 
 def int8_gemm_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | None:
     """A workspace for int8_gemm of an M x N x K product on `device` (None when
-    the product would not use one).  Reusable by later calls of the same or
-    smaller shapes on one stream (nothing is kept between calls)."""
+    the product would not use one).  Reusable by later calls of any shape on
+    one stream (nothing is kept between calls); a shape that could use more
+    splits its sums less, with the same bits."""
     return _workspace("int8_gemm_workspace_size", M, N, K, device)
 
 
 def int8_linear_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | None:
-    """A workspace for int8_linear, as int8_gemm_workspace."""
+    """A workspace for int8_linear of an M x N x K product on `device` (None
+    when the product would not use one).  Reusable by later calls with no more
+    rows and no larger K on one stream, as int8_gemm_workspace."""
     return _workspace("int8_linear_workspace_size", M, N, K, device)
 
 

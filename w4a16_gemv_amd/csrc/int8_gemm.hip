@@ -1032,7 +1032,7 @@ constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
 // 2 x 4096 x 11008 in 16.7 against 17.5; four tokens would take 15.0 against 14.4 at
 // 11008 x 4096 and 23.5 against 17.6 at 4096 x 11008.  Longer rows would not fit the
 // registers that are asked for ahead.
-bool single(int64_t M, int64_t K) { return M <= kDotTokens && K > 0 && pitch_of(K) <= kDotBlocks * 1024; }
+bool single(int64_t M, int64_t K) { return M <= kDotTokens && pitch_of(K) <= kDotBlocks * 1024; }
 
 template <int XT, int DT, int MT>
 void launch_dot_blocks(const Product& p, const void* x, int64_t K, hipStream_t st) {
@@ -1239,11 +1239,13 @@ nf4_status int8_linear(const void* x, int32_t x_dtype, const int8_t* wq, const f
     with_dtype(x_dtype, [&](auto a) { result = launch_dot<decltype(a)::value>(p, x, K, y_dtype, st); });
     return result;
   }
-  if (!workspace || workspace_bytes < int8_linear_workspace_size(M, N, K)) return NF4_EINVAL;
+  // the codes and scales have to have room; the rest is for the sums of a split, which
+  // a workspace made for another shape may not hold (a smaller M may split more)
+  const size_t used = codes_bytes(M, K) + scales_bytes(M);
+  if (!workspace || workspace_bytes < used) return NF4_EINVAL;
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(xq + codes_bytes(M, K));
   quantize_launch(x, x_dtype, M, K, xq, xs, st);
-  const size_t used = codes_bytes(M, K) + scales_bytes(M);
   return launch<false>(dense(xq, xs, wq, ws, y, M, N, K), y_dtype, xq + used, workspace_bytes - used, st);
 }
 
