@@ -35,3 +35,33 @@ def test_linear_takes_the_workspace_of_a_larger_shape(larger, shapes):
         y = amd.int8_linear(x.to(dev()), wt, out_dtype=F32, workspace=whole[:work.numel()])
         assert same(y + 0.0, product(*encode(x), w, ws, F32) + 0.0), (M, N, K)
         assert bool((whole[work.numel():] == 7).all())
+
+
+# --- gradients ---------------------------------------------------------------
+
+def test_learned_scales_under_no_grad():
+    rng = np.random.default_rng(3)
+    q, xs, x = random_tensor(rng, 5, 130)
+    w, ws, wt = random_tensor(rng, 40, 130)
+    wt.scale.requires_grad_()
+    for call in (lambda: amd.int8_gemm(x, wt, out_dtype=F32), lambda: amd.int8_gemm(wt, x, out_dtype=F32),
+                 lambda: amd.int8_linear(torch.ones(3, 130, device=dev()), wt), lambda: wt.dequant()):
+        with pytest.raises(ValueError, match="scale requires a gradient"):
+            call()
+    with torch.no_grad():
+        assert same(amd.int8_gemm(x, wt, out_dtype=F32), product(q, xs, w, ws, F32))
+
+    class Product(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, scale):
+            ctx.save_for_backward(scale)
+            return amd.int8_gemm(x, amd.Int8Tensor(wt.data, scale, 130), out_dtype=F32)
+
+        @staticmethod
+        def backward(ctx, g):
+            scale, = ctx.saved_tensors
+            return (g * amd.int8_gemm(x, amd.Int8Tensor(wt.data, torch.ones_like(scale), 130), out_dtype=F32)).sum(0)
+
+    y = Product.apply(wt.scale)                # inside a Function nothing is being recorded
+    y.backward(torch.ones_like(y))
+    assert same(y.detach(), product(q, xs, w, ws, F32)) and wt.scale.grad is not None

@@ -4,6 +4,7 @@ import os
 import re
 
 import pytest
+import torch
 
 import w4a16_gemv_amd as amd
 
@@ -48,3 +49,42 @@ def test_linear_needs_room_for_codes_and_scales(lib, M, N, K):
 @pytest.mark.parametrize("M,K", [(1, 0), (2, 0), (1, 64), (2, 11264)])
 def test_linear_of_one_or_two_tokens_needs_no_workspace(lib, M, K):
     assert lib.int8_linear_workspace_size(M, 300, K) == 0
+
+
+def _codes(rows, K, **kw):
+    """An Int8Tensor off the GPU, which only a call that has passed its first checks would notice."""
+    t = amd.Int8Tensor.__new__(amd.Int8Tensor)
+    t.data, t.scale, t.K = torch.zeros(rows, amd.int8_pitch(K), dtype=torch.int8), torch.ones(rows, **kw), K
+    return t
+
+
+def _route(T, k, E):
+    r = amd.MoeRoute.__new__(amd.MoeRoute)
+    r.offsets = torch.zeros(E + 1, dtype=torch.int32)
+    r.order, r.pos = torch.zeros(T * k, dtype=torch.int32), torch.zeros(T, k, dtype=torch.int32)
+    return r
+
+
+SCALES = {
+    "dequant": lambda leaf, other: amd.int8_dequant(leaf),
+    "method": lambda leaf, other: leaf.dequant(),
+    "gemm x": lambda leaf, other: amd.int8_gemm(leaf, other),
+    "gemm w": lambda leaf, other: amd.int8_gemm(other, leaf),
+    "linear w": lambda leaf, other: amd.int8_linear(torch.zeros(6, 70), leaf),
+    "vector w": lambda leaf, other: leaf.gemm(torch.zeros(70)),
+    "grouped x": lambda leaf, other: amd.int8_gemm_grouped(leaf, other, _route(6, 2, 3)),
+    "grouped w": lambda leaf, other: amd.int8_gemm_grouped(other, leaf, _route(6, 2, 3)),
+    "quantize out": lambda leaf, other: amd.int8_quantize(torch.zeros(6, 70), out=leaf),
+}
+
+
+@pytest.mark.parametrize("call", SCALES.values(), ids=SCALES.keys())
+def test_scales_that_require_a_gradient_are_refused(call):
+    """A learned scale would silently get none.  The flag may be set after the Int8Tensor was made."""
+    leaf, other = _codes(6, 70), _codes(6, 70)
+    leaf.scale.requires_grad_()
+    with pytest.raises(ValueError, match="scale requires a gradient"):
+        call(leaf, other)
+    with torch.no_grad(), pytest.raises(Exception) as e:
+        call(leaf, other)                      # past that check: these are not on the GPU
+    assert "requires a gradient" not in str(e.value)

@@ -28,11 +28,22 @@ def _on(dev: torch.device, t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _gpu(t: torch.Tensor, name: str) -> int:
-    """The pointer of a contiguous GPU tensor (of a type that was checked)."""
+def _no_grad(t: torch.Tensor, name: str) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which autograd would not see; call this under "
                          "torch.no_grad() or in a Function")
+
+
+def _scale(t: "Int8Tensor", name: str) -> int:
+    """The pointer of t's scales.  They were checked when t was made, but whether they
+    require a gradient can change at any time."""
+    _no_grad(t.scale, f"{name}.scale")
+    return t.scale.data_ptr()
+
+
+def _gpu(t: torch.Tensor, name: str) -> int:
+    """The pointer of a contiguous GPU tensor (of a type that was checked)."""
+    _no_grad(t, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if not t.is_contiguous():
@@ -134,6 +145,8 @@ def int8_quantize(x: torch.Tensor, out: Int8Tensor | None = None) -> Int8Tensor:
     for n in x.shape[:-1]:
         rows *= n
     code = _row_dtype(x.dtype, "x")
+    if out is not None:
+        _no_grad(out.scale, "out.scale")
     px, dev = _gpu(x, "x"), x.device
     if out is None:
         out = Int8Tensor.__new__(Int8Tensor)
@@ -151,7 +164,7 @@ def int8_quantize(x: torch.Tensor, out: Int8Tensor | None = None) -> Int8Tensor:
 def int8_dequant(t: Int8Tensor, out: torch.Tensor | None = None,
                  out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values of t's codes as [rows][K] in bf16, fp16 or fp32."""
-    dev, rows, K = t.data.device, t.data.shape[0], t.K
+    dev, rows, K, scale = t.data.device, t.data.shape[0], t.K, _scale(t, "t")
     if out is None:
         code = _row_dtype(out_dtype, "out_dtype")
         out = torch.empty((rows, K), dtype=out_dtype, device=dev)
@@ -160,7 +173,7 @@ def int8_dequant(t: Int8Tensor, out: torch.Tensor | None = None,
         if out.shape != (rows, K):
             raise ValueError(f"out must be [{rows}, {K}], got shape {tuple(out.shape)}")
         _on(dev, out, "out")
-    _run("int8_dequant", dev, t.data.data_ptr(), t.scale.data_ptr(), rows, K, _gpu(out, "out"), code)
+    _run("int8_dequant", dev, t.data.data_ptr(), scale, rows, K, _gpu(out, "out"), code)
     return out
 
 
@@ -211,13 +224,13 @@ def int8_gemm(x: Int8Tensor, w: Int8Tensor, y: torch.Tensor | None = None,
     allocator."""
     if x.K != w.K:
         raise ValueError(f"x has K={x.K}, w has K={w.K}")
+    xs, ws = _scale(x, "x"), _scale(w, "w")
     xd, wd = x.data, w.data
     M, N, dev = xd.shape[0], wd.shape[0], xd.device
     _on(dev, wd, "w")
     y, py, code = _out(y, M, N, out_dtype, dev)
     pw, wbytes, _keep = _scratch(workspace, "int8_gemm_workspace_size", dev, M, N, x.K)
-    _run("int8_gemm", dev, xd.data_ptr(), x.scale.data_ptr(), wd.data_ptr(), w.scale.data_ptr(), M, N,
-         x.K, py, code, pw, wbytes)
+    _run("int8_gemm", dev, xd.data_ptr(), xs, wd.data_ptr(), ws, M, N, x.K, py, code, pw, wbytes)
     return y
 
 
@@ -232,15 +245,14 @@ def int8_linear(x: torch.Tensor, w: Int8Tensor, y: torch.Tensor | None = None,
     one = x.dim() == 1
     if x.dim() > 2 or x.dim() < 1 or x.shape[-1] != w.K:
         raise ValueError(f"x must be [M, {w.K}] or [{w.K}], got shape {tuple(x.shape)}")
-    xcode = _row_dtype(x.dtype, "x")
+    xcode, ws = _row_dtype(x.dtype, "x"), _scale(w, "w")
     px, dev, wd = _gpu(x, "x"), x.device, w.data
     M, N = 1 if one else x.shape[0], wd.shape[0]
     _on(dev, wd, "w")
     flat = one and (y is None or y.dim() == 1)
     y2, py, code = _out(y.unsqueeze(0) if flat and y is not None else y, M, N, out_dtype, dev)
     pw, wbytes, _keep = _scratch(workspace, "int8_linear_workspace_size", dev, M, N, w.K)
-    _run("int8_linear", dev, px, xcode, wd.data_ptr(), w.scale.data_ptr(), M, N, w.K, py, code, pw,
-         wbytes)
+    _run("int8_linear", dev, px, xcode, wd.data_ptr(), ws, M, N, w.K, py, code, pw, wbytes)
     if y is not None:
         return y
     return y2.view(N) if one else y2
@@ -266,12 +278,13 @@ def int8_gemm_grouped(x: Int8Tensor, w: Int8Tensor, route, y: torch.Tensor | Non
     want = route.rows if x_sorted else route.T
     if x.rows != want:
         raise ValueError(f"x has {x.rows} rows, expected {want}")
+    xs, ws = _scale(x, "x"), _scale(w, "w")
     xd, wd, rows = x.data, w.data, route.rows
     N, dev = wd.shape[0] // E, xd.device
     _on(dev, wd, "w")
     _on(dev, route.offsets, "route")
     y, py, code = _out(y, rows, N, out_dtype, dev)
-    _run("int8_gemm_grouped", dev, xd.data_ptr(), x.scale.data_ptr(), xd.shape[0],
+    _run("int8_gemm_grouped", dev, xd.data_ptr(), xs, xd.shape[0],
          None if x_sorted else route.order.data_ptr(), route.top_k, wd.data_ptr(),
-         w.scale.data_ptr(), route.offsets.data_ptr(), E, rows, N, x.K, py, code)
+         ws, route.offsets.data_ptr(), E, rows, N, x.K, py, code)
     return y
