@@ -3,6 +3,7 @@ beyond the values themselves, on the GPU."""
 import numpy as np
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
 from tests.test_gpu_int8 import BF, F32, dev, encode, product, random_tensor, same
@@ -65,3 +66,30 @@ def test_learned_scales_under_no_grad():
     y = Product.apply(wt.scale)                # inside a Function nothing is being recorded
     y.backward(torch.ones_like(y))
     assert same(y.detach(), product(q, xs, w, ws, F32)) and wt.scale.grad is not None
+
+
+def test_forward_mode():
+    rng = np.random.default_rng(4)
+    _, _, wt = random_tensor(rng, 40, 96)
+    x, dx = torch.ones(3, 96, device=dev()), torch.randn(3, 96, device=dev())
+    want = amd.int8_linear(x, wt, out_dtype=F32)
+    route = amd.moe_sort(torch.tensor([[0], [1], [0]], device=dev()), 2)
+
+    class Gather(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            return amd.moe_gather(x, route)
+
+        @staticmethod
+        def jvp(ctx, t):
+            return amd.moe_gather(t, route)
+
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, dx)
+        for call in (lambda: amd.int8_linear(dual, wt), lambda: amd.int8_quantize(dual),
+                     lambda: amd.moe_gather(dual, route), lambda: amd.moe_combine(dual, route)):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+        assert same(amd.int8_linear(x, wt, out_dtype=F32), want)          # others go on as before
+        out = forward_ad.unpack_dual(Gather.apply(dual))
+        assert same(out.primal, x) and same(out.tangent, dx[[0, 2, 1]])

@@ -5,6 +5,7 @@ import re
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
 
@@ -88,3 +89,35 @@ def test_scales_that_require_a_gradient_are_refused(call):
     with torch.no_grad(), pytest.raises(Exception) as e:
         call(leaf, other)                      # past that check: these are not on the GPU
     assert "requires a gradient" not in str(e.value)
+
+
+@pytest.mark.parametrize("call", SCALES.values(), ids=SCALES.keys())
+def test_scales_with_a_tangent_are_refused(call):
+    leaf, other = _codes(6, 70), _codes(6, 70)
+    with forward_ad.dual_level(), torch.no_grad():
+        leaf.scale = forward_ad.make_dual(leaf.scale, torch.ones(6))
+        with pytest.raises(ValueError, match="scale has a forward-mode tangent"):
+            call(leaf, other)
+
+
+TANGENTS = {
+    "quantize": lambda x: amd.int8_quantize(x),
+    "linear": lambda x: amd.int8_linear(x, _codes(6, 8)),
+    "gather": lambda x: amd.moe_gather(x, _route(4, 2, 3)),
+    "combine": lambda x: amd.moe_combine(x, _route(2, 2, 3)),
+    "gather_grad": lambda x: amd.moe_gather_grad(x, _route(2, 2, 3)),
+    "combine_grad dy": lambda x: amd.moe_combine_grad(x, torch.zeros(8, 8), _route(4, 2, 3)),
+}
+
+
+@pytest.mark.parametrize("call", TANGENTS.values(), ids=TANGENTS.keys())
+def test_values_with_a_tangent_are_refused(call):
+    """The result would have none, in silence.  torch.no_grad() leaves forward mode on."""
+    x = torch.zeros(4, 8)
+    for context in (torch.enable_grad, torch.no_grad):
+        with forward_ad.dual_level(), context():
+            with pytest.raises(ValueError, match="forward-mode tangent"):
+                call(forward_ad.make_dual(x, torch.ones(4, 8)))
+            with pytest.raises(ValueError) as e:
+                call(x)                        # a level alone is no reason
+            assert "tangent" not in str(e.value)

@@ -4,11 +4,12 @@ channel, int32 sums.
 Argument marshalling only, as in _binding.py; work goes on torch's current
 stream of the tensors' device, whichever device is current.  Nothing here is
 recorded by autograd: tensors that require a gradient are refused while
-gradients are being recorded.
+gradients are being recorded, and so are those with a forward-mode tangent.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from ._binding import _check, _dev, _F32, load
 
@@ -28,10 +29,18 @@ def _on(dev: torch.device, t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
+def _tangent(t: torch.Tensor) -> bool:
+    """Whether t has a forward-mode tangent (which torch.no_grad() does not switch off)."""
+    return (forward_ad._current_level >= 0 and torch._C._is_fwd_grad_enabled()
+            and forward_ad.unpack_dual(t).tangent is not None)
+
+
 def _no_grad(t: torch.Tensor, name: str) -> None:
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which autograd would not see; call this under "
                          "torch.no_grad() or in a Function")
+    if _tangent(t):
+        raise ValueError(f"{name} has a forward-mode tangent, which the result would not; call this in a Function")
 
 
 def _scale(t: "Int8Tensor", name: str) -> int:

@@ -5,7 +5,8 @@ Argument marshalling only, as in _binding.py; work goes on torch's current
 stream of the tensors' device, whichever device is current.  Nothing here is
 recorded by autograd: a program that trains calls moe_combine_grad and
 moe_gather_grad in its backward pass, and tensors that require a gradient are
-refused while gradients are being recorded.
+refused while gradients are being recorded.  Those with a forward-mode tangent
+are refused too.
 """
 from __future__ import annotations
 
