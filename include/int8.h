@@ -129,7 +129,7 @@ size_t int8_linear_workspace_size(int64_t M, int64_t N, int64_t K);
  * sorted order is made.
  *  xq, xs        : codes and scales of x_rows rows.
  *  x_rows        : rows of xq; a row i whose s lies outside [0, x_rows) gives
- *                  zeros.
+ *                  zeros, whatever its expert's scales hold.
  *  order, top_k  : device int32[rows] or NULL; top_k >= 1 (ignored for NULL).
  *  wq, ws        : codes and scales of experts * N rows.
  *  offsets       : device int32[experts + 1], ascending from 0.  Values are

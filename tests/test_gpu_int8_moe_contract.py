@@ -6,7 +6,8 @@ import torch
 from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
-from tests.test_gpu_int8 import BF, F32, dev, encode, product, random_tensor, same
+from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, product, random_tensor, same, to_route,
+                                 untouched)
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +94,40 @@ def test_forward_mode():
         assert same(amd.int8_linear(x, wt, out_dtype=F32), want)          # others go on as before
         out = forward_ad.unpack_dual(Gather.apply(dual))
         assert same(out.primal, x) and same(out.tangent, dx[[0, 2, 1]])
+
+
+# --- rows sorted by expert ---------------------------------------------------
+
+# by kernel: few rows, tiles of each size, the largest with a last turn in halves and in quarters
+ABSENT = [(6, 2, 3, 70, 128), (100, 2, 2, 40, 64), (200, 2, 3, 70, 128), (600, 2, 4, 515, 64), (1500, 2, 2, 1030, 300),
+          (2200, 2, 3, 4000, 130), (4650, 2, 5, 2000, 140), (4000, 2, 2, 2300, 150)]
+
+
+@pytest.mark.parametrize("T,k,E,N,K", ABSENT)
+def test_rows_without_a_token_are_zeros_beside_scales_that_are_not_finite(T, k, E, N, K):
+    """A slot of a token that does not exist, and channels that the encoder marked as not finite (NaN scale)."""
+    rng = np.random.default_rng(T + N)
+    _, _, x = random_tensor(rng, T, K)
+    _, _, w = random_tensor(rng, E * N, K)
+    bad = torch.from_numpy(rng.random(E * N) < 0.2).to(dev())
+    bad[:2] = True
+    w.scale[bad] = float("nan")
+    w.scale[1], w.scale[2] = float("inf"), -w.scale[2]
+    order = rng.permutation(T * k).astype(np.int32)
+    gone = rng.random(T * k) < 0.1
+    gone[:3] = True
+    order[gone] = rng.choice(np.array([-1, -2 ** 31, T * k, 2 ** 31 - 1], np.int32), gone.sum())
+    offsets = np.linspace(0, T * k, E + 1).astype(np.int32)
+    plan = to_route((offsets, order, np.zeros((T, k), np.int32)))
+    gone = torch.from_numpy(gone).to(dev())
+    for dtype in TYPES:
+        whole, y = guarded(T * k, N, dtype)
+        amd.int8_gemm_grouped(x, w, plan, y=y)
+        assert bool((y[gone].float() == 0).all()) and untouched(whole, T * k * N), dtype
+        for e in range(E):
+            rows = torch.arange(int(offsets[e]), int(offsets[e + 1]), device=dev())
+            rows = rows[~gone[rows]]
+            token = plan.order[rows].long() // k
+            xe = amd.Int8Tensor(x.data[token], x.scale[token], K)
+            we = amd.Int8Tensor(w.data[e * N:(e + 1) * N], w.scale[e * N:(e + 1) * N], K)
+            assert same(y[rows], gpu_product(xe, we, dtype)), (dtype, e)
