@@ -83,8 +83,12 @@ nf4_status int8_dequant(const int8_t* q, const float* scale, int64_t rows, int64
  *                  Nothing is kept between calls; calls that may overlap in
  *                  time need separate workspaces.
  * The sum is exact; it is converted to fp32, multiplied by xs[m], then by
- * ws[n] (three fp32 roundings) and rounded to y_dtype: each output is within
- * (1 + 2^-24)^3 of the exact value, relative, before that last rounding.
+ * ws[n] (three fp32 roundings) and rounded to y_dtype.  Where the product with
+ * xs[m] and the one with ws[n] are both normal fp32 numbers (or the sum is 0),
+ * each output is within (1 + 2^-24)^3 of the exact value, relative, before
+ * that last rounding.  A product with xs[m] past fp32's range is an infinity
+ * whatever ws[n] is, and one below its normal range is a subnormal number, with
+ * the bits that those have.
  * K == 0 gives the sums 0.  Returns NF4_EINVAL for negative sizes, an unknown
  * type, NULL pointers with M * N > 0, codes that are not 16-byte aligned,
  * scales or y not naturally aligned, or a workspace that is not 256-byte

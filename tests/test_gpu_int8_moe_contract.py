@@ -96,6 +96,35 @@ def test_forward_mode():
         assert same(out.primal, x) and same(out.tangent, dx[[0, 2, 1]])
 
 
+# --- roundings ---------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N", [(1, 40), (2, 33), (7, 300), (40, 700), (300, 1030), (600, 2100)])
+def test_three_fp32_roundings_in_order(M, N):
+    """fp32(fp32(fp32(sum) xs) ws): within (1 + 2^-24)^3 of the exact value where both products are normal; past
+    fp32's range and below its normal numbers the first product has the last word."""
+    rng = np.random.default_rng(M)
+    K = 320
+    q, _, x = random_tensor(rng, M, K)
+    w, _, wt = random_tensor(rng, N, K)
+    xs = (2.0 ** rng.uniform(-148, 127, M)).astype(np.float32)
+    ws = (2.0 ** rng.uniform(-148, 127, N)).astype(np.float32)
+    xs[0], ws[:3] = 2.0 ** 126, (2.0 ** -100, 2.0 ** -140, 2.0 ** 3)
+    x.scale.copy_(torch.from_numpy(xs)), wt.scale.copy_(torch.from_numpy(ws))
+    got = amd.int8_gemm(x, wt, out_dtype=F32).cpu()
+    with np.errstate(over="ignore"):
+        assert same(got, product(q, xs, w, ws, F32))
+        acc = q.astype(np.float64) @ w.astype(np.float64).T
+        first = acc.astype(np.float32) * xs[:, None]
+    exact = acc * xs.astype(np.float64)[:, None] * ws.astype(np.float64)[None, :]
+    got = got.double().numpy()
+    tiny, top = 2.0 ** -126, float(np.finfo(np.float32).max)
+    normal = lambda a: (np.abs(a) >= tiny) & (np.abs(a) <= top)  # noqa: E731
+    good = (normal(first) & normal(got)) | (acc == 0)
+    assert (np.abs(got - exact)[good] <= np.abs(exact)[good] * ((1 + 2.0 ** -24) ** 3 - 1 + 2.0 ** -50)).all()
+    out = np.isinf(first)
+    assert out[0].any() and (M == 1 or good.any()) and np.isinf(got[out]).all() and (np.abs(exact[out]) < top).any()
+
+
 # --- rows sorted by expert ---------------------------------------------------
 
 # by kernel: few rows, tiles of each size, the largest with a last turn in halves and in quarters
