@@ -1,8 +1,9 @@
 /*
- * nf4_probe.h -- bandwidth probes of libnf4 (measurement helpers, not part of
- * the NF4 method).  They move bytes with the same access patterns as the hot
- * path's kernels and no arithmetic, so that the hot path's achieved
- * bandwidth can be set against what plain streaming reaches on the same GPU.
+ * nf4_probe.h -- bandwidth probes of libnf4 and a query of its choice of kernels
+ * (measurement and test helpers, not part of the NF4 method).  The probes move
+ * bytes with the same access patterns as the hot path's kernels and no
+ * arithmetic, so that the hot path's achieved bandwidth can be set against what
+ * plain streaming reaches on the same GPU.
  * Device pointers; asynchronous on `stream`; they allocate nothing.
  */
 #ifndef NF4_PROBE_H_
@@ -35,6 +36,25 @@ nf4_status nf4_probe_stream_read(const void* src, size_t bytes, uint32_t* sink, 
  * multiple of 4.  Returns NF4_EINVAL for NULL or misaligned pointers or sizes.
  */
 nf4_status nf4_probe_expand_copy(const void* src, size_t src_bytes, void* dst, void* stream);
+
+/*
+ * nf4_probe_int8_plan -- which kernel an int8 product of these sizes goes to on
+ * the current device (on 256 compute units where there is none); nothing is
+ * launched.  Tests use it to show that their sizes reach every variant.
+ *  M, N, K, experts : sizes as in int8_gemm (experts 0; M, N >= 1) or, with
+ *                  M rows, in int8_gemm_grouped.
+ *  room          : bytes of workspace (int8_gemm).
+ *  plan          : host; -2 the one- and two-token kernel, -1 the few-row
+ *                  kernel, 0-5 tiles, by size.
+ *  detail        : host; the variant: blocks of 1024 bytes to a row (-2), units
+ *                  of 64 bytes to a wave (-1), in how many pieces K is split
+ *                  (0-4 and grouped), or a sum of 1 (whole tiles), 2 (a last
+ *                  turn in halves) and 4 (in quarters) (5).
+ * Returns NF4_EINVAL for a NULL pointer or bad sizes, NF4_EUNSUPPORTED for
+ * sizes that the products refuse.
+ */
+nf4_status nf4_probe_int8_plan(int64_t M, int64_t N, int64_t K, int32_t experts, size_t room,
+                               int32_t* plan, int32_t* detail);
 
 #ifdef __cplusplus
 }

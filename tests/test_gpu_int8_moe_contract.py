@@ -1,13 +1,15 @@
 """What the headers and docstrings of the int8 products and of the routing promise
 beyond the values themselves, on the GPU."""
+import ctypes as C
+
 import numpy as np
 import pytest
 import torch
 from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
-from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, product, random_tensor, same, to_route,
-                                 untouched)
+from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, product, random_tensor, route_of, same,
+                                 to_route, untouched)
 
 pytestmark = pytest.mark.gpu
 
@@ -18,7 +20,52 @@ def _lib():
     amd.load()
 
 
+def plan(M, N, K, experts=0, room=1 << 62):
+    """(plan, detail) of include/nf4_probe.h: the kernel and variant that these sizes go to."""
+    a, b = C.c_int32(), C.c_int32()
+    assert amd.load().nf4_probe_int8_plan(M, N, K, experts, room, C.byref(a), C.byref(b)) == 0
+    return a.value, b.value
+
+
+DOT, ROWS, LARGEST = -2, -1, 5
+
 # --- workspaces --------------------------------------------------------------
+
+# products that split K over workgroups: every tiling that does
+SPLITS = [(17, 7, 12000), (18, 64, 131071), (130, 513, 20000), (1030, 7, 20000), (250, 600, 11300), (17, 2100, 8192),
+          (65, 1000, 8192), (65, 1000, 40000), (65, 4099, 12000), (128, 1024, 11008)]
+
+
+@pytest.mark.parametrize("M,N,K", SPLITS)
+def test_split_products_in_any_workspace(M, N, K):
+    """The bits with room for all pieces of K, for more, for fewer and for none; workspaces that held other values
+    and are not written past the pieces that fit."""
+    rng = np.random.default_rng(M + N + K)
+    _, _, x = random_tensor(rng, M, K)
+    _, _, w = random_tensor(rng, N, K)
+    plane = M * ((N + 3) // 4 * 4) * 4
+    splits = plan(M, N, K)[1]
+    work = amd.int8_gemm_workspace(M, N, K)
+    assert splits > 1 and work is not None and work.numel() == splits * plane
+    want = gpu_product(x, w, F32)
+    used = set()
+    for room in (work.numel(), work.numel() - 1, 2 * work.numel() + 256, (splits - 1) * plane, 2 * plane, plane, 256):
+        whole = torch.full((room + 256,), 255, dtype=torch.uint8, device=dev())
+        pieces = plan(M, N, K, room=room)[1]
+        assert pieces == 1 or pieces * plane <= room
+        used.add(pieces)
+        for _ in range(2):
+            assert same(amd.int8_gemm(x, w, out_dtype=F32, workspace=whole[:room]), want), room
+        edge = pieces * plane if pieces > 1 else 0
+        assert bool((whole[edge:] == 255).all()), room
+    assert len(used) > 1
+    assert same(amd.int8_gemm(x, w, out_dtype=F32), want)
+    # and in a workspace of int8_linear, behind the codes
+    a = torch.randn(M, K, device=dev())
+    work = amd.int8_linear_workspace(M, N, K)
+    work.fill_(255)
+    assert same(amd.int8_linear(a, w, workspace=work), gpu_product(amd.int8_quantize(a), w, BF))
+
 
 @pytest.mark.parametrize("larger,shapes", [
     ((139, 512, 8192), [(139, 512, 8192), (138, 512, 8192), (130, 512, 8000), (40, 512, 4097), (2, 512, 64), (1, 512, 0)]),
@@ -125,11 +172,76 @@ def test_three_fp32_roundings_in_order(M, N):
     assert out[0].any() and (M == 1 or good.any()) and np.isinf(got[out]).all() and (np.abs(exact[out]) < top).any()
 
 
+# --- every kernel ------------------------------------------------------------
+
+# (plan, detail) and sizes: variants that the sizes of test_gpu_int8.py leave out, and one of each other kind
+KERNELS = [((DOT, 4), (1, 100, 1000)), ((DOT, 8), (2, 77, 7000)), ((DOT, 8), (1, 130, 8001)), ((DOT, 11), (2, 50, 11201)),
+           ((ROWS, 4), (5, 130, 1000)), ((ROWS, 8), (13, 100, 4000)), ((ROWS, 22), (16, 100, 11201)),
+           ((0, 1), (128, 4096, 300)), ((1, 1), (33, 4099, 60)), ((2, 1), (100, 4099, 60)), ((3, 1), (200, 4099, 60)),
+           ((4, 1), (2049, 1000, 60)), ((0, 11), (17, 7, 12000)), ((2, 8), (65, 1000, 8190)),
+           ((LARGEST, 2), (2000, 4001, 2030)), ((LARGEST, 3), (4600, 5000, 1500)), ((LARGEST, 5), (4100, 4099, 1501))]
+
+
+@pytest.mark.parametrize("kind,size", KERNELS)
+def test_padding_of_either_operand_may_hold_anything(kind, size):
+    M, N, K = size
+    assert plan(M, N, K) == kind and K % 64
+    rng = np.random.default_rng(M + N + K)
+    for side in (0, 1):
+        _, _, x = random_tensor(rng, M, K)
+        _, _, w = random_tensor(rng, N, K)
+        want = gpu_product(x, w, BF)
+        t = (x, w)[side]
+        t.data[:, K:] = torch.from_numpy(rng.integers(-128, 128, (t.rows, t.data.shape[1] - K)).astype(np.int8)).to(dev())
+        assert same(amd.int8_gemm(x, w), want)
+        assert same(amd.int8_gemm(x, w, workspace=torch.empty(256, dtype=torch.uint8, device=dev())), want)
+
+
+# (plan, detail) and (rows, experts, N, K)
+GROUPED = [((ROWS, 4), (120, 40, 70, 1000)), ((ROWS, 8), (60, 20, 100, 4000)), ((ROWS, 22), (60, 20, 100, 11000)),
+           ((ROWS, 22), (8, 8, 515, 8100)), ((0, 1), (100, 1, 40, 60)), ((1, 1), (1500, 30, 130, 60)), ((2, 1), (600, 1, 1030, 60)),
+           ((3, 1), (900, 12, 1000, 250)), ((4, 1), (2700, 30, 515, 60)), ((LARGEST, 1), (4400, 3, 4000, 1501)),
+           ((LARGEST, 1), (8000, 2, 2300, 1500)), ((LARGEST, 1), (9300, 5, 2000, 1400))]
+
+
+@pytest.mark.parametrize("x_sorted", [False, True])
+@pytest.mark.parametrize("kind,size", GROUPED)
+def test_gemm_grouped_kernels(kind, size, x_sorted):
+    """Each kernel with the tokens' rows in either order, padding that holds anything, and uneven experts."""
+    rows, E, N, K = size
+    assert plan(rows, N, K, E) == kind and K % 64
+    rng = np.random.default_rng(rows + E + N)
+    T = rows // 2
+    ids = np.minimum(rng.geometric(2.0 / (E + 1), (T, 2)) - 1, E - 1)
+    ids[rng.random((T, 2)) < 0.05] = -1
+    _, _, x = random_tensor(rng, rows if x_sorted else T, K)
+    _, _, w = random_tensor(rng, E * N, K)
+    offsets, order, pos = route_of(ids, E)
+    route = to_route((offsets, order, pos))
+    source = torch.arange(rows, device=dev()) if x_sorted else route.order.long().clamp_min(0) // 2
+    want = torch.full((rows, N), 7.25, dtype=BF, device=dev())
+    for e in range(E):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        xe = amd.Int8Tensor(x.data[source[a:b]], x.scale[source[a:b]], K)
+        we = amd.Int8Tensor(w.data[e * N:(e + 1) * N], w.scale[e * N:(e + 1) * N], K)
+        want[a:b] = gpu_product(xe, we, BF)
+    for t in (None, x, w):
+        if t is not None:
+            kept = t.data[:, K:].clone()
+            t.data[:, K:] = 93
+        whole, y = guarded(rows, N, BF)
+        amd.int8_gemm_grouped(x, w, route, y=y, x_sorted=x_sorted)
+        assert same(y, want) and untouched(whole, rows * N)
+        if t is not None:
+            t.data[:, K:] = kept
+
+
 # --- rows sorted by expert ---------------------------------------------------
 
-# by kernel: few rows, tiles of each size, the largest with a last turn in halves and in quarters
+# by kernel: few rows, tiles of several sizes, the largest with a last turn in halves and in quarters
 ABSENT = [(6, 2, 3, 70, 128), (100, 2, 2, 40, 64), (200, 2, 3, 70, 128), (600, 2, 4, 515, 64), (1500, 2, 2, 1030, 300),
-          (2200, 2, 3, 4000, 130), (4650, 2, 5, 2000, 140), (4000, 2, 2, 2300, 150)]
+          (2200, 2, 3, 4000, 130), (4650, 2, 5, 2000, 140), (4000, 2, 2, 2300, 150),
+          (2200, 2, 3, 4000, 1500), (4650, 2, 5, 2000, 1400), (4000, 2, 2, 2300, 1500), (8, 2, 5, 70, 4000), (8, 2, 5, 70, 9000)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K", ABSENT)

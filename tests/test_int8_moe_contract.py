@@ -8,6 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
+from tests import test_gpu_int8, test_gpu_int8_moe_contract as on_gpu
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 EINVAL = 1
@@ -121,3 +122,38 @@ def test_values_with_a_tangent_are_refused(call):
             with pytest.raises(ValueError) as e:
                 call(x)                        # a level alone is no reason
             assert "tangent" not in str(e.value)
+
+
+# --- what the GPU tests reach ------------------------------------------------
+
+# every variant of the dense products (plan, detail), splits of K as one, and of the grouped ones
+DENSE = ({(-2, 4), (-2, 8), (-2, 11), (-1, 4), (-1, 8), (-1, 22)} | {(i, "whole K") for i in range(5)} |
+         {(i, "split K") for i in range(5)} | {(5, shares) for shares in (1, 2, 3, 5)})
+GROUPED = {(-1, 4), (-1, 8), (-1, 22)} | {(i, "whole K") for i in range(5)} | {(5, 1)}
+
+
+def _variant(plan, detail):
+    return (plan, detail) if plan < 0 or plan == 5 else (plan, "split K" if detail > 1 else "whole K")
+
+
+def test_the_gpu_tests_reach_every_variant(lib):
+    """A rule that is measured anew may send their sizes elsewhere; then they need others."""
+    sizes = test_gpu_int8.TILINGS + [size for _, size in on_gpu.KERNELS]
+    assert {_variant(*on_gpu.plan(*s)) for s in sizes} >= DENSE
+    # (that of test_gpu_int8.py lies in the test's marks)
+    marks = test_gpu_int8.test_gemm_grouped_tilings.pytestmark
+    sizes = [m.args[1] for m in marks if m.name == "parametrize"][0] + [size for _, size in on_gpu.GROUPED]
+    assert {_variant(*on_gpu.plan(rows, N, K, E)) for rows, E, N, K in sizes} >= GROUPED
+    assert {on_gpu.plan(T * k, N, K, E)[0] for T, k, E, N, K in on_gpu.ABSENT} >= {-1, 0, 2, 4, 5}
+    assert all(on_gpu.plan(*s)[1] > 1 for s in on_gpu.SPLITS)
+    assert {on_gpu.plan(*s)[0] for s in on_gpu.SPLITS} == set(range(5))
+
+
+def test_plan_arguments(lib):
+    a, b = C.c_int32(), C.c_int32()
+    ask = lambda M=4, N=8, K=64, E=0, a=C.byref(a), b=C.byref(b): lib.nf4_probe_int8_plan(M, N, K, E, 0, a, b)  # noqa: E731
+    assert ask() == 0 and (a.value, b.value) == (-1, 4)
+    for bad in (dict(M=0), dict(N=0), dict(K=-1), dict(E=-1), dict(a=None), dict(b=None)):
+        assert ask(**bad) == EINVAL
+    for large in (dict(M=1 << 31), dict(N=1 << 31), dict(K=131072), dict(E=1025)):
+        assert ask(**large) == 2

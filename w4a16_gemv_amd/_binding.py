@@ -24,7 +24,7 @@ EXPORTED = ("nf4_abi_version", "nf4_status_string", "nf4_dequant", "nf4_gemv", "
             "nf4_gemm_workspace_size",
             "nf4_dequant_absmax32", "nf4_gemv_absmax32", "nf4_gemv_grouped",
             "nf4_gemv_grouped_absmax32", "int4_gemv_grouped",
-            "nf4_probe_stream_read", "nf4_probe_expand_copy",
+            "nf4_probe_stream_read", "nf4_probe_expand_copy", "nf4_probe_int8_plan",
             "nf4_gemv_sched_size", "nf4_gemv_grouped_noalloc", "nf4_gemv_desc_check",
             "nf4_code2_linear", "nf4_quantize_workspace_size",
             "nf4_quantize", "nf4_quantize_absmax32", "int4_dequant", "int4_gemv",
@@ -78,6 +78,8 @@ def load() -> C.CDLL:
     lib.nf4_probe_stream_read.argtypes = [p, C.c_size_t, p, p]
     lib.nf4_probe_expand_copy.restype = C.c_int
     lib.nf4_probe_expand_copy.argtypes = [p, C.c_size_t, p, p]
+    lib.nf4_probe_int8_plan.restype = C.c_int
+    lib.nf4_probe_int8_plan.argtypes = [i64, i64, i64, i32, C.c_size_t, p, p]
     lib.int4_gemv_grouped.restype = C.c_int
     lib.int4_gemv_grouped.argtypes = [p, i32, i64, i64, i32, i32, p, C.c_size_t, p]
     lib.nf4_gemv_sched_size.restype = C.c_size_t

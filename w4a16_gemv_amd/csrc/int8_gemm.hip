@@ -15,6 +15,7 @@
 #include "int8.h"
 #include "int8_product.h"
 #include "nf4_device.h"
+#include "nf4_probe.h"
 #include "row_io.h"
 
 namespace {
@@ -1026,18 +1027,24 @@ nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
 constexpr int64_t kRowMaxUnits = 22;
 constexpr int64_t kRowMaxPitch = kRowMaxUnits * kRowWaves * 64;
 
+// The variant for rows of `pitch` bytes: units of 64 that a wave holds.
+int64_t row_units(int64_t pitch) {
+  const int64_t units = (pitch / 64 + kRowWaves - 1) / kRowWaves;
+  return units <= 4 ? 4 : units <= 8 ? 8 : kRowMaxUnits;
+}
+
 template <bool GROUPED>
 nf4_status launch_rows(const Product& p, int32_t y_dtype, hipStream_t st) {
   const int64_t tiles = (p.N + 15) / 16, rows = row_tiles<GROUPED>(p, 16);
   // two workgroups fit a compute unit
   const int64_t most = 2 * device_cus(), share = (most + rows - 1) / rows;
   const dim3 grid(static_cast<uint32_t>(tiles < share ? tiles : share), static_cast<uint32_t>(rows));
-  const int64_t units = (p.pitch / 64 + kRowWaves - 1) / kRowWaves;
+  const int64_t units = row_units(p.pitch);
   with_dtype(y_dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
-    if (units <= 4)
+    if (units == 4)
       hipLaunchKernelGGL((row_kernel<DT, GROUPED, 4>), grid, dim3(kRowThreads), 0, st, p);
-    else if (units <= 8)
+    else if (units == 8)
       hipLaunchKernelGGL((row_kernel<DT, GROUPED, 8>), grid, dim3(kRowThreads), 0, st, p);
     else
       hipLaunchKernelGGL((row_kernel<DT, GROUPED, kRowMaxUnits>), grid, dim3(kRowThreads), 0, st, p);
@@ -1058,13 +1065,17 @@ constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
 // registers that are asked for ahead.
 bool single(int64_t M, int64_t K) { return M <= kDotTokens && pitch_of(K) <= kDotBlocks * 1024; }
 
+// The variant for rows of `pitch` bytes: blocks of 1024 that it holds.
+int64_t dot_blocks(int64_t pitch) { return pitch <= 4 * 1024 ? 4 : pitch <= 8 * 1024 ? 8 : kDotBlocks; }
+
 template <int XT, int DT, int MT>
 void launch_dot_blocks(const Product& p, const void* x, int64_t K, hipStream_t st) {
   const int64_t tiles = (p.N + kDotRows - 1) / kDotRows, most = 2 * device_cus();
   const dim3 grid(static_cast<uint32_t>(tiles < most ? tiles : most));
-  if (p.pitch <= 4 * 1024)
+  const int64_t blocks = dot_blocks(p.pitch);
+  if (blocks == 4)
     hipLaunchKernelGGL((dot_kernel<XT, DT, MT, 4>), grid, dim3(kDotThreads), 0, st, p, x, static_cast<int>(K));
-  else if (p.pitch <= 8 * 1024)
+  else if (blocks == 8)
     hipLaunchKernelGGL((dot_kernel<XT, DT, MT, 8>), grid, dim3(kDotThreads), 0, st, p, x, static_cast<int>(K));
   else
     hipLaunchKernelGGL((dot_kernel<XT, DT, MT, kDotBlocks>), grid, dim3(kDotThreads), 0, st, p, x,
@@ -1185,12 +1196,23 @@ bool few(const Product& p) {
   return p.M <= 16 || row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16) <= (p.pitch <= kShortPitch ? 2 : 1) * cus;
 }
 
+// What a product goes to: the one- and two-token kernel, the few-row kernel, or tiles
+// as planned.
+constexpr int kToDot = -2, kToRows = -1;
+
+template <bool GROUPED>
+Plan choose(const Product& p, size_t room) {
+  if (!GROUPED && single(p.M, p.pitch)) return {kToDot, 1};
+  if (few<GROUPED>(p)) return {kToRows, 1};
+  return plan<GROUPED>(p, room);
+}
+
 template <bool GROUPED>
 nf4_status launch(Product p, int32_t y_dtype, void* workspace, size_t room, hipStream_t st) {
+  const Plan plan_ = choose<GROUPED>(p, workspace ? room : 0);
   if constexpr (!GROUPED)
-    if (single(p.M, p.pitch)) return launch_dot<kCodes>(p, nullptr, 0, y_dtype, st);
-  if (few<GROUPED>(p)) return launch_rows<GROUPED>(p, y_dtype, st);
-  const Plan plan_ = plan<GROUPED>(p, workspace ? room : 0);
+    if (plan_.tiling == kToDot) return launch_dot<kCodes>(p, nullptr, 0, y_dtype, st);
+  if (plan_.tiling == kToRows) return launch_rows<GROUPED>(p, y_dtype, st);
   p.splits = plan_.splits;
   p.sums = static_cast<int32_t*>(workspace);
   switch (plan_.tiling) {
@@ -1219,11 +1241,32 @@ size_t codes_bytes(int64_t M, int64_t K) { return static_cast<size_t>(M * pitch_
 
 extern "C" {
 
+nf4_status nf4_probe_int8_plan(int64_t M, int64_t N, int64_t K, int32_t experts, size_t room, int32_t* plan,
+                               int32_t* detail) {
+  if (!plan || !detail || M < 1 || N < 1 || K < 0 || experts < 0) return NF4_EINVAL;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxK || experts > kMaxExperts) return NF4_EUNSUPPORTED;
+  Product p = dense(nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K);
+  if (experts > 0) p.experts = experts;
+  const Plan best = experts > 0 ? choose<true>(p, 0) : choose<false>(p, room);
+  *plan = best.tiling;
+  if (best.tiling == kToDot) {
+    *detail = static_cast<int32_t>(dot_blocks(p.pitch));
+  } else if (best.tiling == kToRows) {
+    *detail = static_cast<int32_t>(row_units(p.pitch));
+  } else if (best.tiling < kLargest || experts > 0) {
+    *detail = best.splits;
+  } else {
+    const uint32_t all = static_cast<uint32_t>(row_tiles<false>(p, kTile) * ((N + kTile - 1) / kTile));
+    const uint32_t whole = whole_tiles(all, p.cus), rest = all - whole;
+    *detail = (whole > 0 ? 1 : 0) + (rest == 0 ? 0 : in_quarters(rest, p.cus) ? 4 : 2);
+  }
+  return NF4_OK;
+}
+
 size_t int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxK) return 0;
   const Product p = dense(nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K);
-  if (single(M, p.pitch) || few<false>(p)) return 0;
-  const Plan best = plan<false>(p, static_cast<size_t>(1) << 62);
+  const Plan best = choose<false>(p, static_cast<size_t>(1) << 62);
   return best.splits > 1 ? static_cast<size_t>(M * p.sums_pitch * 4 * best.splits) : 0;
 }
 
