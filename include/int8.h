@@ -24,7 +24,12 @@
  *               (the product is not rounded before)
  *
  * so |q| <= 127, a row of zeros has zero codes, and both scale and inverse are
- * normal numbers.  A row that holds a NaN or an infinity gets the scale NaN
+ * normal numbers.  They are not the quotients' nearest numbers but the ones that
+ * tensor expressions for a / 127 and 127 / a give on the device, within two
+ * roundings, (1 + 2^-24)^2, of the quotients; past a = 2^126, where 1 / a is
+ * subnormal, the inverse is within 2^-21.  So each code is within 1/2 + 2^-16 of
+ * 127 x_k / a (1/2 + 2^-14 there) and each value within (1/2 + 2^-14) a / 127 of
+ * x_k (1/2 + 2^-13).  A row that holds a NaN or an infinity gets the scale NaN
  * and zero codes: every output made from that row is NaN, and no other is.
  */
 #ifndef INT8_H_

@@ -145,6 +145,35 @@ def test_forward_mode():
 
 # --- roundings ---------------------------------------------------------------
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_encoder_against_quotients_in_64_bits(dtype):
+    """Scales, codes and values against a / 127, 127 x / a and x, over the whole range of peaks.
+
+    1 / a and the product with 127 are rounded once each, 2^-24 relative: 127 (2^-23 + 2^-48) < 2^-16 in a code.  For
+    a > 2^126 1 / a is a multiple of 2^-149 above 2^-128, 2^-22 relative, in all 127 (2^-22 + 2^-24 + 2^-46) < 2^-14.  A
+    value adds the scale's two roundings, 127 (2^-23 + 2^-48) more, and the product's, 127 2^-24."""
+    g = torch.Generator().manual_seed(11)
+    top = np.log2(torch.finfo(dtype).max)
+    rows, K = 6000, 96
+    exponent = torch.rand(rows, 1, generator=g, dtype=torch.float64) * (top + 99) - 99
+    exponent[:2000] = top - torch.rand(2000, 1, generator=g, dtype=torch.float64) * 2     # 1 / a may be subnormal
+    x = torch.rand(rows, K, generator=g, dtype=torch.float64) * 2 - 1
+    x[:, 0] = 1.0
+    x[:, 1::7] = torch.randint(-254, 255, (rows, 14), generator=g).double() / 254              # next to ties
+    x = (x * torch.exp2(exponent - 2.0 ** -20)).to(dtype)
+    t = amd.int8_quantize(x.to(dev()))
+    v, q, scale = x.double().numpy(), t.data[:, :K].cpu().double().numpy(), t.scale.cpu().double().numpy()
+    assert np.isfinite(v).all() and np.isfinite(scale).all()
+    a = np.maximum(np.abs(v).max(1), 2.0 ** -100)
+    high = (a > 2.0 ** 126)[:, None]
+    assert (np.abs(scale - a / 127) <= a / 127 * (2.0 ** -23 + 2.0 ** -47)).all()
+    slack = np.where(high, 2.0 ** -14, 2.0 ** -16)
+    assert (np.abs(q - 127 * v / a[:, None]) <= 0.5 + slack).all()
+    got = t.dequant(out_dtype=F32).cpu().double().numpy()
+    assert (np.abs(got - v) <= (0.5 + np.where(high, 2.0 ** -13, 2.0 ** -14)) * a[:, None] / 127).all()
+    assert dtype == torch.float16 or (high.any() and not high.all())
+
+
 @pytest.mark.parametrize("M,N", [(1, 40), (2, 33), (7, 300), (40, 700), (300, 1030), (600, 2100)])
 def test_three_fp32_roundings_in_order(M, N):
     """fp32(fp32(fp32(sum) xs) ws): within (1 + 2^-24)^3 of the exact value where both products are normal; past

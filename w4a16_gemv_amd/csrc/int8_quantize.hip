@@ -1,8 +1,9 @@
 // int8_quantize.hip -- the int8 encoder (activations per token, weights per
 // output channel) and its inverse.
 //
-// Encoder, per row: a = max(max|x|, 2^-100), scale = a / 127 and inverse =
-// 127 / a (both correctly rounded), code = x * inverse rounded half to even.
+// Encoder, per row: a = max(max|x|, 2^-100), scale = a * (1 / 127) and inverse =
+// 127 * (1 / a) (each step rounded: row_scale() says why), code = x * inverse rounded
+// half to even.
 // The rounding is one FMA: x * inverse + 1.5 * 2^23 has its last bit at one,
 // so the fused product and sum round the exact product to an integer, ties to
 // even, and the low byte of the result is the code.
