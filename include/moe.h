@@ -80,7 +80,7 @@ nf4_status moe_combine(const void* ys, int32_t dtype, const float* weights, cons
  *     dys[pos[t][j]] = weights[t][j] * dy[t]        (rounded once to dtype)
  *     dweights[t][j] = sum_h ys[pos[t][j]][h] * dy[t][h]     (fp32 sums)
  * and dweights = 0 for a dropped slot; rows of dys that no slot names, or two,
- * are as in moe_gather.  The order of each sum is fixed.
+ * are as in moe_gather.  The order of each sum follows from T and H alone.
  *  dy            : device [T][H];  ys, dys : device [rows][H]; of type dtype.
  *  weights       : device fp32 [T][top_k], or NULL for ones.
  *  dys, dweights : either may be NULL (not wanted); ys is read only for

@@ -8,6 +8,7 @@ import torch
 from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
+from tests import test_gpu_moe
 from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, product, random_tensor, route_of, same,
                                  to_route, untouched)
 
@@ -301,3 +302,15 @@ def test_rows_without_a_token_are_zeros_beside_scales_that_are_not_finite(T, k, 
             xe = amd.Int8Tensor(x.data[token], x.scale[token], K)
             we = amd.Int8Tensor(w.data[e * N:(e + 1) * N], w.scale[e * N:(e + 1) * N], K)
             assert same(y[rows], gpu_product(xe, we, dtype)), (dtype, e)
+
+
+# --- routing -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,H,kind", [(1024, 1, 5, 513, "drop"), (1025, 1, 5, 513, "drop"), (1024, 2, 9, 1024, "all"), (1025, 2, 9, 1024, "all"),
+                                          (1030, 5, 7, 1001, "drop"), (257, 2, 8, 1001, "all"), (1100, 1, 3, 512, "drop")])
+def test_rows_of_few_and_many_tokens(T, k, E, H, kind, dtype):
+    """On both sides of the number of tokens at which a token's row goes to a wave instead of a workgroup."""
+    test_gpu_moe.test_gather(T, k, E, H, kind, dtype)
+    test_gpu_moe.test_combine(T, k, E, H, kind, dtype)
+    test_gpu_moe.test_combine_grad(T, k, E, H, kind, dtype)

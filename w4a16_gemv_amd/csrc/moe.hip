@@ -228,9 +228,15 @@ constexpr int64_t kMaxRowGroups = 1 << 20;  // a grid may not have 2^32 threads:
 // Up to two pieces a lane a wave does better than the workgroup (8192 tokens with
 // four slots combine rows of 64 in 4.9 us against 10.3, of 640 in 13.3 against 17.2,
 // of 1024 in 16.6 against 19.0), with more it does not (gradients at 1536 54.7 against
-// 43.4, at 2048 76 against 54).
-int row_width(int64_t H) {
-  if (H > 16 * 64) return 8;
+// 43.4, at 2048 76 against 54).  With two pieces a lane that takes as many waves as the
+// card holds at once: 4096 tokens with two slots combine rows of 1024 in 8.0 us against
+// 8.5 (gradients 12.8 against 15.2), but where the tokens' waves leave a compute unit
+// one workgroup at most, a workgroup each is faster: 1024 tokens in 5.4 us against 4.3
+// (8.5 against 6.1), 257 of 1001 fp32 in 6.2 against 3.7 (8.9 against 6.6), 64 in 3.2
+// against 2.5.  (At 2048 it depends: 6.3 and 5.6 at 1024 bf16, gradients 15.5 and 17.2
+// at 1001 fp32.)
+int row_width(int64_t T, int64_t H) {
+  if (H > 16 * 64 || (H > 8 * 64 && T <= 4 * device_cus())) return 8;
   int width = 3;
   while (width < 6 && (8 << width) < H) ++width;
   return width;
@@ -490,7 +496,7 @@ nf4_status moe_gather(const void* x, int32_t dtype, const int32_t* pos, int64_t 
   if (T == 0 || rows == 0 || H == 0) return NF4_OK;
   if (!x || !xs || !aligned(x, dtype_bytes(dtype)) || !aligned(xs, dtype_bytes(dtype)))
     return NF4_EINVAL;
-  const RowArgs a = {pos, T, top_k, rows, H, row_width(H)};
+  const RowArgs a = {pos, T, top_k, rows, H, row_width(T, H)};
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     const dim3 grid(row_groups(T, a.width));
@@ -510,7 +516,7 @@ nf4_status moe_combine(const void* ys, int32_t dtype, const float* weights, cons
   if ((rows > 0 && !ys) || !y || !aligned(ys, dtype_bytes(dtype)) ||
       !aligned(y, dtype_bytes(dtype)) || !aligned(weights, 4))
     return NF4_EINVAL;
-  const RowArgs a = {pos, T, top_k, rows, H, row_width(H)};
+  const RowArgs a = {pos, T, top_k, rows, H, row_width(T, H)};
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     const dim3 grid(row_groups(T, a.width));
@@ -533,7 +539,7 @@ nf4_status moe_combine_grad(const void* dy, const void* ys, int32_t dtype, const
   if (!aligned(dy, b) || !aligned(ys, b) || !aligned(dys, b) || !aligned(weights, 4) ||
       !aligned(dweights, 4))
     return NF4_EINVAL;
-  const RowArgs a = {pos, T, top_k, rows, H, row_width(H)};
+  const RowArgs a = {pos, T, top_k, rows, H, row_width(T, H)};
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     const dim3 grid(row_groups(T, a.width));
