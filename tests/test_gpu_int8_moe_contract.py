@@ -9,7 +9,7 @@ from torch.autograd import forward_ad
 
 import w4a16_gemv_amd as amd
 from tests import test_gpu_moe
-from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, product, random_tensor, route_of, same,
+from tests.test_gpu_int8 import (BF, F32, TYPES, dev, encode, gpu_product, guarded, padded, product, random_tensor, route_of, same,
                                  to_route, untouched)
 
 pytestmark = pytest.mark.gpu
@@ -200,6 +200,22 @@ def test_three_fp32_roundings_in_order(M, N):
     assert (np.abs(got - exact)[good] <= np.abs(exact)[good] * ((1 + 2.0 ** -24) ** 3 - 1 + 2.0 ** -50)).all()
     out = np.isinf(first)
     assert out[0].any() and (M == 1 or good.any()) and np.isinf(got[out]).all() and (np.abs(exact[out]) < top).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows,K", [(1, 4096), (3, 4097), (300, 4160), (2, 6145), (5, 8191), (1200, 8192), (2, 8193), (3, 12288), (2, 12289), (2, 16385)])
+def test_encoder_on_both_sides_of_each_variant(rows, K, dtype):
+    g = torch.Generator().manual_seed(rows + K)
+    x = (torch.randn(rows, K, generator=g) * 3).to(dtype)
+    x[:, -1] = x.abs().amax(1) * 2                      # the peak in the last piece
+    room = torch.zeros(rows * K + 1, dtype=dtype, device=dev())
+    for shift in (0, 1):
+        view = room[shift:shift + rows * K].view(rows, K)
+        view.copy_(x)
+        t = amd.Int8Tensor(torch.full((rows, amd.int8_pitch(K)), 85, dtype=torch.int8, device=dev()), torch.zeros(rows, device=dev()), K)
+        amd.int8_quantize(view, out=t)
+        q, s = encode(x)
+        assert torch.equal(t.data.cpu(), padded(q)) and same(t.scale, torch.from_numpy(s))
 
 
 # --- every kernel ------------------------------------------------------------

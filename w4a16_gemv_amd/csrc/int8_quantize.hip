@@ -135,11 +135,16 @@ void quantize_launch(const void* x, int32_t dt, int64_t rows, int64_t K, int8_t*
   hipLaunchKernelGGL((quantize_rows_kernel<DT, WAVES, HOLD>), dim3(groups_for((rows * WAVES + 3) / 4)), \
                      dim3(kThreads), 0, st, x, rows, K, pitch, q, scale)
     // Held rows: 4097 x 11008 in 23.5 us against 37.5 read twice, 4097 x 14336 in 33
-    // against 47.5, 1000 x 32768 in 22.5 against 28.
+    // against 47.5, 1000 x 32768 in 22.5 against 28.  A row takes the least variant that
+    // holds it, since a thread's pieces past the row cost too: in four pieces instead of
+    // six 1 x 4160 takes 2.6 us against 2.9, 4097 x 4160 12.5 against 15.4, 4097 x 8192
+    // 18.6 against 19.6.
     if (encode_by_waves(rows, K))
       INT8_QUANTIZE(1, 4);
     else if (K <= 2 * 8 * kThreads)
       INT8_QUANTIZE(4, 2);
+    else if (K <= 4 * 8 * kThreads)
+      INT8_QUANTIZE(4, 4);
     else if (K <= 6 * 8 * kThreads)
       INT8_QUANTIZE(4, 6);
     else if (K <= 8 * 8 * kThreads)
