@@ -243,10 +243,32 @@ def test_padding_of_either_operand_may_hold_anything(kind, size):
         assert same(amd.int8_gemm(x, w, workspace=torch.empty(256, dtype=torch.uint8, device=dev())), want)
 
 
+# both sides of what sends few rows to the few-row kernel: the kernel and the size
+FEW = [(ROWS, (16, 4096, 4150)), (0, (16, 4097, 4150)), (0, (3, 8192, 8192)), (ROWS, (3, 8193, 8130)), (0, (3, 8193, 8120)),
+       (ROWS, (16, 12000, 11264)), (0, (16, 4500, 11265)), (ROWS, (16, 9000, 4096)), (ROWS, (17, 4096, 4096)), (0, (17, 2100, 4097))]
+
+
+@pytest.mark.parametrize("kernel,size", FEW)
+def test_both_sides_of_the_few_row_rule(kernel, size):
+    M, N, K = size
+    rng = np.random.default_rng(M + N + K)
+    _, _, x = random_tensor(rng, M, K)
+    _, _, w = random_tensor(rng, N, K)
+    assert (plan(M, N, K)[0] == ROWS) == (kernel == ROWS)
+    for dtype in TYPES:
+        whole, y = guarded(M, N, dtype)
+        amd.int8_gemm(x, w, y=y)
+        assert same(y, gpu_product(x, w, dtype)) and untouched(whole, M * N)
+    a = torch.randn(M, K, device=dev())
+    assert same(amd.int8_linear(a, w), gpu_product(amd.int8_quantize(a), w, BF))
+
+
 # (plan, detail) and (rows, experts, N, K)
 GROUPED = [((ROWS, 4), (120, 40, 70, 1000)), ((ROWS, 8), (60, 20, 100, 4000)), ((ROWS, 22), (60, 20, 100, 11000)),
-           ((ROWS, 22), (8, 8, 515, 8100)), ((0, 1), (100, 1, 40, 60)), ((1, 1), (1500, 30, 130, 60)), ((2, 1), (600, 1, 1030, 60)),
+           ((ROWS, 22), (8, 8, 515, 8300)), ((0, 1), (100, 1, 40, 60)), ((1, 1), (1500, 30, 130, 60)), ((2, 1), (600, 1, 1030, 60)),
            ((3, 1), (900, 12, 1000, 250)), ((4, 1), (2700, 30, 515, 60)), ((LARGEST, 1), (4400, 3, 4000, 1501)),
+           ((2, 1), (8, 8, 4096, 8100)), ((2, 1), (32, 16, 515, 9000)), ((0, 1), (8, 8, 515, 4200)),
+           ((ROWS, 22), (60, 20, 2910, 8150)), ((2, 1), (60, 20, 2800, 8150)),
            ((LARGEST, 1), (8000, 2, 2300, 1500)), ((LARGEST, 1), (9300, 5, 2000, 1400))]
 
 

@@ -1024,6 +1024,10 @@ nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
   return launch_status();
 }
 
+// The longest rows: a wave's weights and codes take 176 of its 256 registers.  Past them
+// tiles do better: with 24 units 16 x 4096 x 12288 takes 17.4 us against 14.7, with 28 x
+// 14336 27.7 against 16.0 (at 11264 13.3 against 14.6), 16 x 4 tokens of 64 experts of
+// 1024 x 14336 236 against 124.
 constexpr int64_t kRowMaxUnits = 22;
 constexpr int64_t kRowMaxPitch = kRowMaxUnits * kRowWaves * 64;
 
@@ -1056,13 +1060,17 @@ nf4_status launch_rows(const Product& p, int32_t y_dtype, hipStream_t st) {
 // units of 64 bytes a wave.
 constexpr int64_t kShortPitch = 8 * 64 * kRowWaves;
 
+// The longest rows fill the registers that 16 waves a compute unit leave to one: with
+// 12 blocks 1 x 4096 x 12288 takes 16.8 us against 15.0 in tiles, with 14 x 14336 24.4
+// against 15.7 (at 11264 11.5 against 14.3; codes given).
 constexpr int64_t kDotTokens = 2, kDotBlocks = 11;
 
 // Whether the product goes to the single tokens' kernel, which quantizes on the
 // way where it is given values: 2 x 4096 x 4096 in 7.6 us against 9.2 in two launches,
 // 2 x 4096 x 11008 in 16.7 against 17.5; four tokens would take 15.0 against 14.4 at
-// 11008 x 4096 and 23.5 against 17.6 at 4096 x 11008.  Longer rows would not fit the
-// registers that are asked for ahead.
+// 11008 x 4096 and 23.5 against 17.6 at 4096 x 11008.  (Past 4096 channels of more than
+// 8192 values two tokens do no better than in tiles: 2 x 8192 x 11264 26.8 against 22.7,
+// 2 x 11008 x 11008 without the codes 30.3 against 30.9.)
 bool single(int64_t M, int64_t K) { return M <= kDotTokens && pitch_of(K) <= kDotBlocks * 1024; }
 
 // The variant for rows of `pitch` bytes: blocks of 1024 that it holds.
@@ -1123,7 +1131,9 @@ struct Plan {
 // workgroups where that leaves compute units without a tile and the workspace has
 // room for the sums (128 x 1024 x 11008: 15.2 us in one piece, 12.9 in six; 88 x 999
 // x 34756: 39 and 20 in seven), unless writing and reading the sums costs as much
-// (65 x 2100 x 8192: 11 us in one piece, 21 in thirteen).  Rows
+// (65 x 2100 x 8192: 11 us in one piece, 21 in thirteen).  The model orders the tilings;
+// it is no time of long weights from memory, which it does not know (1 x 8192 x 28672:
+// 39 us by it, while its bytes take 48).  Rows
 // sorted by expert: every expert with rows ends in a tile that is half full, and
 // where there are tiles for all compute units the weights' stream counts, which
 // tiles of 32 channels hold up (1024 rows over 64 experts of 1024 x 2048: 31.8 us
@@ -1180,20 +1190,40 @@ Product dense(const int8_t* xq, const float* xs, const int8_t* wq, const float* 
 // tile of 16 x 16 at most, whose start is shorter than a larger tile's: 32 x 4096 x
 // 4096 in 8.3 us against 9.3, 64 x 1024 x 4096 in 4.2 against 6.4, 32 x 2048 x 11008
 // in 10.3 against 12.4, 512 x 256 x 4096 in 5.6 against 6.3; 48 x 4096 x 4096 would
-// take 11.4 against 8.5, 17 x 4096 x 11008 23.5 against 15.2.  By expert: with 64 experts of 4096 x 2048 two rows
-// each on average take 96 us against 107, four 103 against 111, six 114 against 110,
-// sixteen 157 against 111 (any with more than 16 is read twice); with fewer tiles
-// than compute units its shorter start counts to ten rows (16 experts of 256 x 512:
-// 4.5 us against 5.0).
+// take 11.4 against 8.5, 17 x 4096 x 11008 23.5 against 15.2.  By expert: with 64
+// experts of 4096 x 2048 two rows each on average take 96 us against 107, four 103
+// against 111, six 114 against 110, sixteen 157 against 111 (any with more than 16 is
+// read twice); with fewer tiles than compute units its shorter start counts to ten rows
+// (16 experts of 256 x 512: 4.5 us against 5.0).
+//
+// Long rows leave one workgroup to a compute unit, with nothing beside it while it
+// starts or turns to its next tile.  Up to 16 rows of a dense product: one tile each is
+// as good as before (16 x 4096 x 6144 in 9.3 us against 10.4, x 11264 in 13.3 against
+// 14.6; x 4160 in 8.4 against 8.9), a second turn is not (16 x 4608 x 4160 13.8 against
+// 9.0, 16 x 8192 x 7168 18.4 against 13.6, x 11264 24.0 against 19.4), and more turns
+// pay from 8192 on (16 x 11008 x 7168 21.4 against 20.9, x 8192 23.1 against 23.9, x
+// 11264 28.1 against 31.0; to 16384 channels 39.5 against 34.4).  By expert: tiles do
+// better (two tokens of eight experts of 4096 x 6144: 20.7 us against 11.9, 16 x 4 of
+// 64 of 1024 x 4160 65 against 38, x 8192 31 against 22 for 4 x 4), except past 8192
+// where the tiles here are about as many as the compute units (four rows of an expert
+// of 1024 x 11264 9.6 against 11.1, 64 x 4 of 64 of 64 15.3 against 17.5; 16 of 16
+// experts of 512 26.7 against 17.4), and with many of them and rows of 8192 bytes,
+// which suit the tiles the least (32 x 4 of 64 of 1024 90 against 104, 16 x 4 of 2048
+// 165 against 152; at 9216 97 against 97 and 176 against 150).
 template <bool GROUPED>
 bool few(const Product& p) {
   if (p.pitch <= 0 || p.pitch > kRowMaxPitch || row_tiles<GROUPED>(p, 16) > 65535) return false;
-  const int64_t cus = device_cus();
+  const int64_t cus = device_cus(), tiles = row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16);
+  const bool is_short = p.pitch <= kShortPitch;
   if (GROUPED) {
     const int64_t rows = p.M / p.experts;
+    if (!is_short && !(p.pitch > 2 * kShortPitch && 4 * tiles <= 5 * cus) &&
+        !(p.pitch == 2 * kShortPitch && tiles > 16 * cus))
+      return false;
     return rows <= 4 || (rows <= 10 && p.experts * ((p.N + 63) / 64) <= cus);
   }
-  return p.M <= 16 || row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16) <= (p.pitch <= kShortPitch ? 2 : 1) * cus;
+  if (tiles <= (is_short ? 2 : 1) * cus) return true;
+  return p.M <= 16 && (is_short || (p.pitch >= 2 * kShortPitch && tiles > 2 * cus));
 }
 
 // What a product goes to: the one- and two-token kernel, the few-row kernel, or tiles
