@@ -46,13 +46,16 @@ def _no_grad(t: torch.Tensor, name: str) -> None:
 def _scale(t: "Int8Tensor", name: str) -> int:
     """The pointer of t's scales.  They were checked when t was made, but whether they
     require a gradient can change at any time."""
-    _no_grad(t.scale, f"{name}.scale")
-    return t.scale.data_ptr()
+    s = t.scale
+    if s.requires_grad or forward_ad._current_level >= 0:
+        _no_grad(s, f"{name}.scale")
+    return s.data_ptr()
 
 
 def _gpu(t: torch.Tensor, name: str) -> int:
     """The pointer of a contiguous GPU tensor (of a type that was checked)."""
-    _no_grad(t, name)
+    if t.requires_grad or forward_ad._current_level >= 0:
+        _no_grad(t, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU, got {t.device}")
     if not t.is_contiguous():
