@@ -3,7 +3,8 @@
  * quantized per token, weights quantized per output channel, int32 sums, on
  * AMD Instinct MI355X (gfx950).  Status codes and all conventions (device
  * pointers owned by the caller, asynchronous work on `stream`, synchronous
- * argument validation, no allocation, thread safety) are those of nf4.h.
+ * argument validation, no allocation, thread safety) are those of nf4.h.  What a
+ * call writes (results, workspace) must not overlap what it reads.
  *
  * ---------------------------------------------------------------------------
  * The format (a matrix of `rows` rows of K elements: one token's activations

@@ -5,6 +5,7 @@ Argument marshalling only, as in _binding.py; work goes on torch's current
 stream of the tensors' device, whichever device is current.  Nothing here is
 recorded by autograd: tensors that require a gradient are refused while
 gradients are being recorded, and so are those with a forward-mode tangent.
+What a call writes (out, y, workspace) must not overlap its other tensors.
 """
 from __future__ import annotations
 

@@ -6,7 +6,8 @@ stream of the tensors' device, whichever device is current.  Nothing here is
 recorded by autograd: a program that trains calls moe_combine_grad and
 moe_gather_grad in its backward pass, and tensors that require a gradient are
 refused while gradients are being recorded.  Those with a forward-mode tangent
-are refused too.
+are refused too.  What a call writes (out, dys, workspace) must not overlap its
+other tensors.
 """
 from __future__ import annotations
 

@@ -229,11 +229,12 @@ __device__ __forceinline__ void write_tile(const Product& p, int64_t end, int64_
 // x 128 outputs in int32 accumulators, which takes all of a compute unit's
 // registers and LDS.
 //
-// Bound by the matrix pipe, the clock and the LDS together: 8192 x 8192 x 8192 takes
-// 430 us (2560 TOP/s), a step of 64 matrix instructions a wave about 1.45 us where
-// they alone take 1.08 (the clock sinks under them; on zeros the same program takes
-// 1.25), with the LDS reads 1.30.  8192 x 11008 x 4096 takes 330-340 us, a seventh of
-// it for the outputs' scaling and stores.  Measured and not kept: one workgroup for
+// Bound by the matrix pipe, the clock and the LDS together, none of them alone: 8192 x
+// 8192 x 8192 takes 430 us (2560 TOP/s), a step of 64 matrix instructions a wave about
+// 1.45 us where they alone take 1.08 (the clock sinks under them; on zeros the same
+// program takes 1.25), with the LDS reads 1.30.  8192 x 11008 x 4096 takes 322-344 us,
+// a seventh of it for the outputs' scaling and stores, with matrix instructions in 68%
+// of a tile's cycles (by expert 54%: two more tables are read before the first load).  Measured and not kept: one workgroup for
 // several tiles, the next one's first loads before the stores (273 us against 246
 // at 8192 x 8192 x 4096: the loads' waits take in the stores), registers between
 // memory and LDS (the same time), all of a step's loads at its barrier (6% slower).

@@ -27,9 +27,10 @@ using namespace rowio;
 //
 // Up to kSortOne slots one workgroup does it all in one launch.  Beyond, a first
 // kernel writes each workgroup's counts per expert to the workspace and a
-// second one adds those of the workgroups before it to its own.  Latency bounds both:
-// 64 slots over 64 experts take 3.2 us, 32764 take 10.7 (a gap between the launches
-// among it), 524288 38.
+// second one adds those of the workgroups before it to its own.  Latency bounds both,
+// that of the tiles and of the sum over all workgroups' counts, which each of them
+// takes for itself: 64 slots over 64 experts take 3.3 us, 32764 take 11.1 in a captured
+// graph (4.8 and 8.2 traced apart), 131072 17.9, 524288 38.
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
@@ -422,7 +423,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_grad_kernel(RowArgs args,
 // Steps of a workgroup's tile.  One workgroup: no more than the slots fill (64 slots in
 // 3.2 us, with four steps 4.7).  Several: two for few slots, which more workgroups
 // then share (8192 in 7.5 us against 9.1, 32764 in 10.7 against 11.1), four for many,
-// whose workgroups would be too many to add up (131072 in 16.8 against 21.1).
+// whose workgroups would be too many to add up (131072 in 16.8 against 21.1; each pair
+// from one run).
 int sort_steps(int64_t n) {
   if (n <= kSortOne) return n <= kSortThreads ? 1 : n <= 2 * kSortThreads ? 2 : 4;
   return n <= 32768 ? 2 : 4;
