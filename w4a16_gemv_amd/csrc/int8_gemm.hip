@@ -234,10 +234,10 @@ __device__ __forceinline__ void write_tile(const Product& p, int64_t end, int64_
 // 1.45 us where they alone take 1.08 (the clock sinks under them; on zeros the same
 // program takes 1.25), with the LDS reads 1.30.  8192 x 11008 x 4096 takes 322-344 us,
 // a seventh of it for the outputs' scaling and stores, with matrix instructions in 68%
-// of a tile's cycles (by expert 54%: two more tables are read before the first load).  Measured and not kept: one workgroup for
-// several tiles, the next one's first loads before the stores (273 us against 246
-// at 8192 x 8192 x 4096: the loads' waits take in the stores), registers between
-// memory and LDS (the same time), all of a step's loads at its barrier (6% slower).
+// of a tile's cycles (by expert 54%).  Measured and not kept: one workgroup for several
+// tiles, the next one's first loads before the stores (273 us against 246 at 8192 x
+// 8192 x 4096: the loads' waits take in the stores), registers between memory and LDS
+// (the same time), all of a step's loads at its barrier (6% slower).
 //
 // 128 bytes of K at a time (a step): the tile's rows go from memory straight to
 // one of two LDS buffers, and from there to the matrix cores, 32 bytes of K at a
