@@ -9,6 +9,9 @@ is the matrix-core product for batches past 8.  int8_quantize / int8_linear /
 int8_gemm / int8_gemm_grouped are the products with 8-bit activations and
 weights (include/int8.h); moe_sort / moe_gather / moe_combine and their
 gradients route token rows to experts and back (include/moe.h).
+mxfp4_quantize / mxfp4_linear / mxfp4_gemm / mxfp4_gemm_grouped are the products
+of 4-bit microscaled floats, mxfp4_gemv and mxfp4_moe_mlp those of a decode step
+with activations as they are (include/mxfp4.h).
 """
 from ._binding import (  # noqa: F401
     EXPORTED,
@@ -60,4 +63,18 @@ from ._moe import (  # noqa: F401
     moe_gather,
     moe_gather_grad,
     moe_sort,
+)
+from ._mxfp4 import (  # noqa: F401
+    Mxfp4Tensor,
+    mxfp4_dequant,
+    mxfp4_gemm,
+    mxfp4_gemm_grouped,
+    mxfp4_gemm_workspace,
+    mxfp4_gemv,
+    mxfp4_linear,
+    mxfp4_linear_workspace,
+    mxfp4_moe_mlp,
+    mxfp4_pitch,
+    mxfp4_quantize,
+    mxfp4_scale_size,
 )

@@ -1,6 +1,6 @@
 """ctypes binding of libnf4 (include/nf4.h, include/int4.h, include/int8.h,
-include/moe.h; the classes and functions of the last two are in _int8.py and
-_moe.py).
+include/moe.h, include/mxfp4.h; the classes and functions of the last three are
+in _int8.py, _moe.py and _mxfp4.py).
 
 Argument marshalling only: every step of the dequant and GEMV runs in the HIP
 kernels of libnf4.so.  Tensors must live on an AMD GPU; there is no CPU
@@ -33,7 +33,11 @@ EXPORTED = ("nf4_abi_version", "nf4_status_string", "nf4_dequant", "nf4_gemv", "
             "int8_gemm_workspace_size", "int8_linear", "int8_linear_workspace_size",
             "int8_gemm_grouped",
             "moe_sort", "moe_sort_workspace_size", "moe_gather", "moe_combine",
-            "moe_combine_grad")
+            "moe_combine_grad",
+            "nf4_probe_mxfp4_plan", "mxfp4_pitch", "mxfp4_scale_size", "mxfp4_quantize",
+            "mxfp4_dequant", "mxfp4_gemm", "mxfp4_gemm_workspace_size", "mxfp4_linear",
+            "mxfp4_linear_workspace_size", "mxfp4_gemv", "mxfp4_gemm_grouped",
+            "mxfp4_moe_mlp", "mxfp4_moe_mlp_workspace_size")
 
 _lib = None
 
@@ -129,6 +133,32 @@ def load() -> C.CDLL:
     lib.moe_combine.argtypes = [p, i32, p, p, i64, i32, i64, i64, p, p]
     lib.moe_combine_grad.restype = C.c_int
     lib.moe_combine_grad.argtypes = [p, p, i32, p, p, i64, i32, i64, i64, p, p, p]
+    lib.nf4_probe_mxfp4_plan.restype = C.c_int
+    lib.nf4_probe_mxfp4_plan.argtypes = [i64, i64, i64, i32, size, p, p]
+    lib.mxfp4_pitch.restype = i64
+    lib.mxfp4_pitch.argtypes = [i64]
+    lib.mxfp4_scale_size.restype = i64
+    lib.mxfp4_scale_size.argtypes = [i64, i64]
+    lib.mxfp4_quantize.restype = C.c_int
+    lib.mxfp4_quantize.argtypes = [p, i32, i64, i64, p, p, p]
+    lib.mxfp4_dequant.restype = C.c_int
+    lib.mxfp4_dequant.argtypes = [p, p, i64, i64, p, i32, p]
+    lib.mxfp4_gemm.restype = C.c_int
+    lib.mxfp4_gemm.argtypes = [p, p, p, p, i64, i64, i64, p, i32, p, size, p]
+    lib.mxfp4_gemm_workspace_size.restype = size
+    lib.mxfp4_gemm_workspace_size.argtypes = [i64, i64, i64]
+    lib.mxfp4_linear.restype = C.c_int
+    lib.mxfp4_linear.argtypes = [p, i32, p, p, i64, i64, i64, p, i32, p, size, p]
+    lib.mxfp4_linear_workspace_size.restype = size
+    lib.mxfp4_linear_workspace_size.argtypes = [i64, i64, i64]
+    lib.mxfp4_gemv.restype = C.c_int
+    lib.mxfp4_gemv.argtypes = [p, i32, p, p, i64, i64, i64, p, i32, p]
+    lib.mxfp4_gemm_grouped.restype = C.c_int
+    lib.mxfp4_gemm_grouped.argtypes = [p, p, i64, p, i32, p, p, p, i32, i64, i64, i64, p, i32, p]
+    lib.mxfp4_moe_mlp.restype = C.c_int
+    lib.mxfp4_moe_mlp.argtypes = [p, i32, p, p, p, p, p, i32, p, i64, i32, i32, i64, i64, i32, p, p, size, p]
+    lib.mxfp4_moe_mlp_workspace_size.restype = size
+    lib.mxfp4_moe_mlp_workspace_size.argtypes = [i64, i32, i64, i32]
     _lib = lib
     return lib
 

@@ -21,7 +21,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f)
         for f in ("nf4_kernels.hip", "nf4_gemm.hip", "nf4_quantize.hip", "nf4_probe.hip",
-                  "int8_quantize.hip", "int8_gemm.hip", "moe.hip")]
+                  "int8_quantize.hip", "int8_gemm.hip", "moe.hip",
+                  "mxfp4_quantize.hip", "mxfp4_few.hip", "mxfp4_gemm.hip", "mxfp4_gemv.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libnf4.so")
 
