@@ -203,7 +203,9 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
                          const float* weights, int64_t T, int32_t top_k, int32_t experts, int64_t H,
                          int64_t F, int32_t gated, void* y, void* workspace, size_t workspace_bytes,
                          void* stream);
-size_t mxfp4_moe_mlp_workspace_size(int64_t T, int32_t top_k, int64_t F, int32_t dtype);
+/* Bytes of workspace mxfp4_moe_mlp needs on the current device. */
+size_t mxfp4_moe_mlp_workspace_size(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F,
+                                    int32_t dtype);
 
 #ifdef __cplusplus
 } /* extern "C" */

@@ -138,8 +138,11 @@ def test_workspace_sizes(lib):
         assert lib.mxfp4_linear(P, 0, P, P, M, N, K, P, 0, P, need - 1, None) == EINVAL
     assert lib.mxfp4_linear_workspace_size(1, 4096, 4096) == 0
     size = lib.mxfp4_moe_mlp_workspace_size
-    assert size(65, 2, 64, 0) == size(4, 33, 64, 0) == size(-1, 2, 64, 0) == size(4, 2, 64, 3) == 0
-    assert size(3, 2, 129, 0) == 6 * 2 * 256 * 2 and size(3, 2, 129, 2) == 6 * 3 * 256 * 2
+    for bad in ((65, 2, 4, 64, 64, 0), (4, 33, 4, 64, 64, 0), (-1, 2, 4, 64, 64, 0), (4, 2, 4, 64, 64, 3),
+                (4, 2, 1025, 64, 64, 0), (4, 2, 4, (1 << 20) + 1, 64, 0), (4, 2, 4, 64, -1, 0)):
+        assert size(*bad) == 0
+    # what lies between the products (two bf16 numbers of each, three for fp32)
+    assert size(3, 2, 4, 8192, 129, 0) == 6 * 2 * 256 * 2 and size(3, 2, 4, 8192, 129, 2) == 6 * 3 * 256 * 2
 
 
 def _codes(rows, K):

@@ -158,7 +158,7 @@ def load() -> C.CDLL:
     lib.mxfp4_moe_mlp.restype = C.c_int
     lib.mxfp4_moe_mlp.argtypes = [p, i32, p, p, p, p, p, i32, p, i64, i32, i32, i64, i64, i32, p, p, size, p]
     lib.mxfp4_moe_mlp_workspace_size.restype = size
-    lib.mxfp4_moe_mlp_workspace_size.argtypes = [i64, i32, i64, i32]
+    lib.mxfp4_moe_mlp_workspace_size.argtypes = [i64, i32, i32, i64, i64, i32]
     _lib = lib
     return lib
 

@@ -325,7 +325,7 @@ def mxfp4_moe_mlp(x: torch.Tensor, w1: Mxfp4Tensor, w2: Mxfp4Tensor, ids: torch.
     if y is not None and y.dtype != x.dtype:
         raise ValueError(f"y must be {x.dtype}, got {y.dtype}")
     y, py, _ = _out(y, T, H, x.dtype, dev)
-    ps, nbytes, _keep = _scratch(workspace, "mxfp4_moe_mlp_workspace_size", dev, T, top_k, F, code)
+    ps, nbytes, _keep = _scratch(workspace, "mxfp4_moe_mlp_workspace_size", dev, T, top_k, E, H, F, code)
     _run("mxfp4_moe_mlp", dev, px, code, w1.data.data_ptr(), w1.scale.data_ptr(), w2.data.data_ptr(),
          w2.scale.data_ptr(), _gpu(ids, "ids"), _IDS[ids.dtype], pw, T, top_k, E, H, F, int(w1.rows != E * F), py, ps,
          nbytes)

@@ -30,9 +30,10 @@ __device__ __forceinline__ int64_t scale_at(int64_t row, int64_t steps, int64_t 
   return ((row >> 5) * steps + (group >> 1)) * 256 + (group & 1) * 128 + (row & 31) * 4;
 }
 
-// 2^(E - 127) as the conversions take it: NaN for 255, and for 0 the subnormal number.
+// 2^(E - 127) as the conversions take it: they see the exponent field alone, and with the
+// mantissa's first bit that is a NaN for 255 and 2^-127 for 0.
 __device__ __forceinline__ float scale_value(uint32_t e) {
-  return __builtin_bit_cast(float, e == 0 ? 0x00400000u : e == 255 ? 0x7FC00000u : e << 23);
+  return __builtin_bit_cast(float, e << 23 | 0x00400000u);
 }
 
 // E of a block whose largest magnitude has these bits: the exponent field less two;

@@ -55,6 +55,22 @@ template <int DT>
 __device__ __forceinline__ void split_piece(const Piece<DT>& p, u32x4 (&out)[parts_of(DT)]) {
   if constexpr (DT == INT8_BF16) {
     out[0] = p.v[0];
+  } else if constexpr (DT == INT8_FP16) {
+    // without the last three bits, and these, both exact in fp16 and in bf16; an infinity
+    // is its own first part
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = p.v[0][i], high = w & 0xFFF8FFF8u;
+      const f16x2 h = __builtin_bit_cast(f16x2, high), low = __builtin_bit_cast(f16x2, w) - h;
+      const float h0 = static_cast<float>(h[0]), h1 = static_cast<float>(h[1]);
+      const float l0 = static_cast<float>(low[0]), l1 = static_cast<float>(low[1]);
+      out[0][i] = upper_halves(h0, h1);
+      out[1][i] = upper_halves(fabsf(h0) < __builtin_inff() ? l0 : 0.0f, fabsf(h1) < __builtin_inff() ? l1 : 0.0f);
+      // (a NaN whose bits are among the last three)
+      if (w != high) {
+        out[0][i] |= ((w & 0x7FFF) > 0x7C00 ? 0x0040u : 0u) | ((w >> 16 & 0x7FFF) > 0x7C00 ? 0x00400000u : 0u);
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -94,6 +110,11 @@ __device__ __forceinline__ Channels channels(const uint8_t* q, const uint8_t* s,
                   scale_from(c0, c0 + (lane & 15), steps, 0)};
 }
 
+template <int CT>
+struct Tiles {
+  Channels ch[CT];
+};
+
 struct Loaded {
   i32x4 codes;
   uint32_t scales;
@@ -116,136 +137,181 @@ __device__ __forceinline__ void operands(const Loaded& l, bf16x8 (&a)[4]) {
   }
 }
 
-// The rows that a wave's products are made with: `count` (16 at most) of them, rows of
-// `width` values of type DT (or, for kSplit + parts, that many rows of bf16 numbers each,
-// `width` numbers long, zeros past the data).
-constexpr int kSplit = 8;
-__device__ __host__ constexpr int source_parts(int dt) { return dt >= kSplit ? dt - kSplit : parts_of(dt); }
+// ---------------------------------------------------------------------------
+// Rows in LDS (gemv and up): a workgroup keeps `rows` rows' parts, `width` elements of
+// them at a time, for its waves' products: [part][row][width + 8] bf16 numbers, the
+// eight so that a chunk of 16 rows lies in different banks.
+// ---------------------------------------------------------------------------
+__device__ __host__ __forceinline__ int lds_row(int width) { return 2 * width + 16; }
 
-// A lane's share of a unit: lane c + 16 r has elements 8 c .. + 7 of rows r, r + 4, ...
-template <int DT, int RU>
-struct Share {
-  static constexpr int kParts = source_parts(DT);
-  u32x4 v[RU][DT >= kSplit ? kParts : DT == INT8_FP32 ? 2 : 1];
+// Elements first .. first + width - 1 of rows row(0), row(1), ... of K each (zeros from K
+// on), by all threads of the workgroup, several loads of each in flight.
+template <int XT, class Row>
+__device__ __forceinline__ void stage_rows(uint8_t* lds, int rows, int64_t first, int width, int64_t K, Row&& row) {
+  constexpr int kParts = parts_of(XT), kAtOnce = XT == INT8_FP32 ? 4 : 8;
+  const int pieces = width / 8, all = rows * pieces, pitch = lds_row(width);
+  for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kThreads) {
+    Piece<XT> v[kAtOnce];
+    int to[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * kThreads;
+      v[k] = Piece<XT>{};
+      if (i >= all) continue;
+      const int r = i / pieces, c = i - r * pieces;
+      to[k] = r * pitch + 16 * c;
+      const int64_t at = first + 8 * c;
+      if (at < K) v[k] = load_piece<XT>(row(r), at, K);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (i0 + k * kThreads >= all) break;
+      u32x4 part[kParts];
+      split_piece<XT>(v[k], part);
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) *reinterpret_cast<u32x4*>(lds + q * rows * pitch + to[k]) = part[q];
+    }
+  }
+}
+
+// The units of a wave in its own order: it starts `turn` units after the first, so that
+// waves of other channels read other memory channels than it (a power of two from one
+// row to the next leads a unit's 16 rows to few of them).
+struct Order {
+  int from, count, turn;
+  __device__ __forceinline__ int operator()(int i) const {
+    const int u = i + turn;
+    return from + (u < count ? u : u - count);
+  }
 };
 
-// LDS of a wave: rows of a unit at a pitch of 272 bytes (so that a chunk of 16 rows lies
-// in different banks), the parts one after the other.
-constexpr int kLdsRow = 2 * kUnit + 16;
-
-template <int DT, int RU>
-__device__ __forceinline__ void stage(const Share<DT, RU>& x, uint8_t* lds, int count) {
-  constexpr int kParts = source_parts(DT);
-  const int lane = threadIdx.x & 63;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+// Adds to the rows' columns those of their other parts, where these stand beside them.
+template <int PARTS, int CT>
+__device__ __forceinline__ void join_parts(f32x4 (&v)[CT], bool together, int rows) {
+  if constexpr (PARTS > 1) {
+    if (!together) return;
 #pragma unroll
-  for (int j = 0; j < RU; ++j) {
-    if (4 * j >= count) break;
-    u32x4 part[kParts];
-    if constexpr (DT >= kSplit) {
+    for (int c = 0; c < CT; ++c) {
+      const float each[4] = {v[c][0], v[c][1], v[c][2], v[c][3]};
 #pragma unroll
-      for (int k = 0; k < kParts; ++k) part[k] = x.v[j][k];
-    } else {
-      Piece<DT> p;
-      p.v[0] = x.v[j][0];
-      if constexpr (DT == INT8_FP32) p.v[1] = x.v[j][1];
-      split_piece<DT>(p, part);
-    }
-#pragma unroll
-    for (int k = 0; k < kParts; ++k)
-      *reinterpret_cast<u32x4*>(lds + (k * 4 * RU + 4 * j + (lane >> 4)) * kLdsRow + (lane & 15) * 16) = part[k];
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-}
-
-// Part k's operand e of the lane's column.
-template <int RU>
-__device__ __forceinline__ bf16x8 staged(const uint8_t* lds, int k, int e, int column) {
-  const int g = (threadIdx.x & 63) >> 4;
-  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lds + (k * 4 * RU + column) * kLdsRow + 64 * g + 16 * e));
-}
-
-// Loads a unit's share of the rows row(0), row(1) ... (pointers; asked for below `count`
-// only).
-template <int DT, int RU, class Row>
-__device__ __forceinline__ Share<DT, RU> load_share(int unit, bool in, int64_t width, int count, Row&& row) {
-  Share<DT, RU> x;
-  const int lane = threadIdx.x & 63;
-  const int64_t at = int64_t(kUnit) * unit + 8 * (lane & 15);
-#pragma unroll
-  for (int j = 0; j < RU; ++j) {
-    constexpr int kWords = sizeof(x.v[0]) / 16;
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) x.v[j][k] = u32x4{0, 0, 0, 0};
-    if (!in || 4 * j >= count) continue;
-    const char* r = row(min(4 * j + (lane >> 4), count - 1));
-    if constexpr (DT >= kSplit) {
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) x.v[j][k] = *reinterpret_cast<const u32x4*>(r + 2 * (k * width + at));
-    } else {
-      Piece<DT> p = {};
-      if (int64_t(kUnit) * (unit + 1) <= width)
-        p = whole_piece<DT>(r, at);
-      else if (at < width)
-        p = load_piece<DT>(r, at, width);
-#pragma unroll
-      for (int k = 0; k < kWords; ++k) x.v[j][k] = p.v[k];
+      for (int k = 1; k < PARTS; ++k) {
+        const int from = (threadIdx.x & 63) + k * rows;
+        v[c] += f32x4{__shfl(each[0], from), __shfl(each[1], from), __shfl(each[2], from), __shfl(each[3], from)};
+      }
     }
   }
-  return x;
 }
 
-// acc[c] += the products of CT tiles of channels with the rows over the units first ..
-// last - 1, DEPTH units in flight.
-template <int DT, int RU, int CT, int DEPTH, class Row>
-__device__ __forceinline__ void run_units(const Channels (&ch)[CT], int first, int last, int64_t width, int count,
-                                          uint8_t* lds, Row&& row, f32x4 (&acc)[CT]) {
-  constexpr int kParts = source_parts(DT);
-  const int column = min(static_cast<int>(threadIdx.x & 15), count - 1);
-  Loaded w[DEPTH][CT];
-  Share<DT, RU> x[DEPTH];
-  auto load = [&](int d, int unit) {
-    const bool in = unit < last;
+// Streams tiles of 16 channels (CT of each, which share the rows) through a workgroup,
+// kWaves / SPLIT of them at a time, whose SPLIT waves share K: a step is UNITS units of
+// each wave, neighbouring waves' next to each other, so that the workgroup reads its rows
+// of weights in a row.  While a step is multiplied the next one's weights, of the next tile
+// at a tile's end, are asked for.
+//
+//  tiles, first, apart : the workgroup takes the groups of tiles first, first + apart, ...
+//                        below tiles
+//  tile(t)             : the channels of tile t
+//  rows_at(unit)       : has the rows' elements from this unit on put into LDS (between
+//                        barriers), `width` of them (whole steps), zeros past K
+//  done(t, acc)        : takes a tile's sums, in one wave (t < tiles)
+template <int PARTS, int CT, int SPLIT, int UNITS, class Tile, class RowsAt, class Done>
+__device__ __forceinline__ void stream_tiles(int units, int64_t tiles, int64_t first, int64_t apart, const uint8_t* lds,
+                                             int rows, int width, f32x4 (&sums)[2][kWaves][CT][64], Tile&& tile,
+                                             RowsAt&& rows_at, Done&& done) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  constexpr int kStep = SPLIT * UNITS, kGroup = kWaves / SPLIT;
+  const int part = wave % SPLIT;
+  const int steps = max(1, (units + kStep - 1) / kStep), held = width / kUnit;
+  // a wave's units of a step: from `mine` on, apart_of(u) further
+  const int mine = UNITS == 1 ? part : 2 * part;
+  auto apart_of = [](int u) { return 2 * SPLIT * (u >> 1) + (u & 1); };
+  Loaded w[UNITS][CT];
+  auto load = [&](const Channels (&ch)[CT], int u, int step, bool in) {
+    const int at = kStep * step + mine + apart_of(u);
 #pragma unroll
-    for (int c = 0; c < CT; ++c) w[d][c] = load_unit(ch[c], unit, in);
-    x[d] = load_share<DT, RU>(unit, in, width, count, row);
+    for (int c = 0; c < CT; ++c) w[u][c] = load_unit(ch[c], at, in && at < units);
   };
+  // t: the wave's tile; the workgroup goes on while the group's first is one
+  int64_t t = first * kGroup + wave / SPLIT;
+  auto some = [&](int64_t at) { return at - wave / SPLIT < tiles; };
+  Tiles<CT> next = tile(t);
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) load(d, first + d);
-  for (int u = first; u < last; u += DEPTH) {
+  for (int u = 0; u < UNITS; ++u) load(next.ch, u, 0, true);
+  // the rows' parts are columns of one product each where there are 16 at most; else each
+  // part is multiplied by itself
+  const int pitch = lds_row(width), columns = PARTS * rows <= 16 ? PARTS * rows : rows;
+  const bool together = PARTS > 1 && columns > rows;
+  const uint8_t* x = lds + min(lane & 15, columns - 1) * pitch + 64 * (lane >> 4) + 2 * kUnit * mine;
+  f32x4 acc[CT] = {};
+  int step = 0, turn = 0, base = -1;
+  while (some(t)) {
+    if (kStep * step - base >= held || kStep * step < base || base < 0) {  // (once where all are held)
+      base = kStep * step;
+      rows_at(base);
+    }
+    const bool last = step + 1 == steps;
+    const int64_t next_t = last ? t + apart * kGroup : t;
+    if (last) next = tile(next_t);
+    const uint8_t* xs = x + 2 * kUnit * (kStep * step - base);
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      if (u + d >= last) break;
-      stage<DT, RU>(x[d], lds, count);
+    for (int u = 0; u < UNITS; ++u) {
       bf16x8 a[CT][4];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) operands(w[d][c], a[c]);
+      for (int c = 0; c < CT; ++c) operands(w[u][c], a[c]);
 #pragma unroll
-      for (int k = 0; k < kParts; ++k)
+      for (int k = 0; k < PARTS; ++k) {
+        if (k == 0 || !together) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bf16x8 b = staged<RU>(lds, k, e, column);
+          for (int e = 0; e < 4; ++e) {
+            const bf16x8 b = *reinterpret_cast<const bf16x8*>(xs + k * rows * pitch + 2 * kUnit * apart_of(u) + 16 * e);
 #pragma unroll
-          for (int c = 0; c < CT; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[c][e], b, acc[c], 0, 0, 0);
+            for (int c = 0; c < CT; ++c) acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[c][e], b, acc[c], 0, 0, 0);
+          }
         }
+      }
+      // the products first, then the loads into the registers that they free: the
+      // other way round the compiler takes twice the registers
       __builtin_amdgcn_sched_barrier(0);
-      load(d, u + d + DEPTH);
+      load(next.ch, u, last ? 0 : step + 1, some(next_t));
     }
+    if (!last) {
+      ++step;
+      continue;
+    }
+    if constexpr (SPLIT == 1) {
+      join_parts<PARTS>(acc, together, rows);
+      if (t < tiles) done(t, acc);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = f32x4{};
+    } else {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        sums[turn & 1][wave][c][lane] = acc[c];
+        acc[c] = f32x4{};
+      }
+      __syncthreads();
+      // one of a tile's waves a turn adds up, in the waves' order; its buffer is written
+      // again two turns later, after a barrier that this wave reaches when it is through
+      if (part == (turn & (SPLIT - 1)) && t < tiles) {
+        f32x4 sum[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          sum[c] = sums[turn & 1][wave - part][c][lane];
+#pragma unroll
+          for (int v = 1; v < SPLIT; ++v) sum[c] += sums[turn & 1][wave - part + v][c][lane];
+        }
+        join_parts<PARTS>(sum, together, rows);
+        done(t, sum);
+      }
+    }
+    t = next_t;
+    step = 0;
+    ++turn;
   }
-}
-
-// The units of a wave: pairs (whole lines), as even over the waves as they go.
-__device__ __forceinline__ void share_of(int units, int wave, int& first, int& last) {
-  const int each = 2 * ((units + 2 * kWaves - 1) / (2 * kWaves));
-  first = min(units, wave * each);
-  last = min(units, first + each);
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 rows.  A workgroup goes through the channels 16 at a time; its eight waves
-// share K.  The weights go from memory through registers to the matrix cores, the rows
-// through registers and the wave's own piece of LDS, several units of both in flight.  The
-// waves' sums meet in LDS and are added in the waves' order.
+// Up to 16 rows: `width` elements of them at a time in LDS, all where they have room.
 // ---------------------------------------------------------------------------
 struct Gemv {
   const void* x;
@@ -253,43 +319,30 @@ struct Gemv {
   const uint8_t* ws;
   void* y;
   int64_t M, N, K, pitch, steps;
+  int width;
 };
 
-template <int XT, int RU>
-constexpr int stage_bytes() {
-  return source_parts(XT) * 4 * RU * kLdsRow;
-}
-
-template <int XT, int DT, int RU>
+template <int XT, int DT, int SPLIT, int UNITS>
 __global__ __launch_bounds__(kThreads, 4) void mx_gemv_kernel(Gemv p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[kWaves][stage_bytes<XT, RU>()];
-  __shared__ f32x4 s_sum[2][kWaves][64];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16);
-  const int units = static_cast<int>(p.pitch / 64), count = static_cast<int>(p.M);
-  int first, last;
-  share_of(units, wave, first, last);
-  auto row = [&](int r) { return static_cast<const char*>(p.x) + r * p.K * dtype_bytes(XT); };
-  int turn = 0;
-  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
-    const int64_t n0 = int64_t(16) * tile;
-    const Channels ch[1] = {channels(p.wq, p.ws, n0, p.N - n0, p.pitch, p.steps)};
-    f32x4 acc[1] = {};
-    run_units<XT, RU, 1, 4>(ch, first, last, p.K, count, s_x[wave], row, acc);
-    s_sum[turn & 1][wave][lane] = acc[0];
-    __syncthreads();
-    // one wave a turn adds up; its buffer is written again two turns later, after
-    // a barrier that this wave reaches when it is through
-    if (wave != (turn & (kWaves - 1))) continue;
-    f32x4 sum = s_sum[turn & 1][0][lane];
-#pragma unroll
-    for (int v = 1; v < kWaves; ++v) sum += s_sum[turn & 1][v][lane];
-    const int64_t n = n0 + 4 * (lane >> 4);
-    const int left = static_cast<int>(min(p.N - n, int64_t(4)));
-    if ((lane & 15) >= count || left <= 0) continue;
-    const float f[4] = {sum[0], sum[1], sum[2], sum[3]};
-    store_four<DT>(p.y, (lane & 15) * p.N + n, left, f);
-  }
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
+  __shared__ f32x4 s_sum[2][kWaves][1][64];
+  const int lane = threadIdx.x & 63, rows = static_cast<int>(p.M);
+  stream_tiles<parts_of(XT), 1, SPLIT, UNITS>(
+      static_cast<int>(p.pitch / 64), (p.N + 15) / 16, blockIdx.x, gridDim.x, s_x, rows, p.width, s_sum,
+      [&](int64_t t) { return Tiles<1>{{channels(p.wq, p.ws, 16 * t, p.N - 16 * t, p.pitch, p.steps)}}; },
+      [&](int unit) {
+        __syncthreads();  // every wave is through with the rows before
+        stage_rows<XT>(s_x, rows, int64_t(kUnit) * unit, p.width, p.K,
+                       [&](int r) { return static_cast<const char*>(p.x) + r * p.K * dtype_bytes(XT); });
+        __syncthreads();
+      },
+      [&](int64_t t, const f32x4 (&sum)[1]) {
+        const int64_t n = 16 * t + 4 * (lane >> 4);
+        const int left = static_cast<int>(min(p.N - n, int64_t(4)));
+        if ((lane & 15) >= rows || left <= 0) return;
+        const float f[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+        store_four<DT>(p.y, (lane & 15) * p.N + n, left, f);
+      });
 }
 
 // ---------------------------------------------------------------------------
@@ -298,11 +351,12 @@ __global__ __launch_bounds__(kThreads, 4) void mx_gemv_kernel(Gemv p) {
 // order, and their (expert, token) pairs too: these are the rows of what lies between the
 // two products (h).
 //
-//  up:    a workgroup takes an expert's 16 channels (of the gate and of the others) and
-//         its tokens; eight waves share H.  act(v) times the router's weight goes to h as
-//         parts.
-//  down:  a workgroup takes 16 channels of y; its waves share the experts' F, an expert
-//         after the other, and add each's sums to those of the tokens that it has.
+//  up:    a workgroup takes tiles of an expert's 16 channels (of the gate and of the
+//         others) and its tokens, as the kernel above.  act(v) times the router's weight
+//         goes to h as parts.
+//  down:  a workgroup takes 16 channels of y.  Its waves share the experts' F, one expert
+//         after the other without a pause in their weights' stream, and add each's sums
+//         to those of the tokens that it has.
 // ---------------------------------------------------------------------------
 constexpr int kMaxTokens = 64, kMaxTopK = 32;
 
@@ -319,6 +373,7 @@ struct Mlp {
   int64_t H, F, h_width;
   int64_t pitch1, steps1, pitch2, steps2;
   int T, top_k, experts, id_bytes, gated;
+  int rows, lds;  // of up: rows at a time (16 at most), bytes for them
 };
 
 // What h is kept in: 16 bits of each number, or all of fp32.
@@ -348,211 +403,367 @@ __device__ __forceinline__ uint64_t mask_of(const Routing& r, int e) {
   return static_cast<uint64_t>(r.masks[e][1]) << 32 | r.masks[e][0];
 }
 
-// The n'th token of a mask (n below their number).
-__device__ __forceinline__ int nth_token(uint64_t mask, int n) {
-  for (int i = 0; i < n; ++i) mask &= mask - 1;
-  return __builtin_ctzll(mask);
+// The experts' tokens in segments of ROWS at most, in order: the expert, the segment's
+// first row among the expert's, and that row's place in h.
+template <int ROWS>
+struct Segments {
+  static constexpr int kMost = kMaxExperts + (ROWS < kMaxTokens ? kMaxTokens * kMaxTopK / ROWS : 0);
+  uint16_t expert[kMost], first[kMost], place[kMost];
+  int count;
+};
+
+// Past it every wave may read the masks and the segments.
+template <int ROWS>
+__device__ __forceinline__ void read_segments(const Mlp& p, Routing& r, Segments<ROWS>& s) {
+  read_routing(p, r);
+  const int lane = threadIdx.x;
+  if (lane < 64) {
+    int segments = 0, rows = 0;
+    for (int base = 0; base < p.experts; base += 64) {
+      const int mine = base + lane < p.experts ? __builtin_popcountll(mask_of(r, base + lane)) : 0;
+      const int own = (mine + ROWS - 1) / ROWS;
+      int in = own << 16 | mine;  // (2048 pairs at most)
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(in, d);
+        if (lane >= d) in += o;
+      }
+      for (int i = 0; i < own; ++i) {
+        const int at = segments + (in >> 16) - own + i;
+        s.expert[at] = static_cast<uint16_t>(base + lane);
+        s.first[at] = static_cast<uint16_t>(ROWS * i);
+        s.place[at] = static_cast<uint16_t>(rows + (in & 0xFFFF) - mine + ROWS * i);
+      }
+      const int all = __shfl(in, 63);
+      segments += all >> 16;
+      rows += all & 0xFFFF;
+    }
+    if (lane == 0) s.count = segments;
+  }
+  __syncthreads();
 }
 
-template <int DT, int RU>
-__global__ __launch_bounds__(kThreads, 2) void mx_up_kernel(Mlp p) {
-  __shared__ __attribute__((aligned(16))) uint8_t s_x[kWaves][stage_bytes<DT, RU>()];
-  __shared__ f32x4 s_sum[kWaves][2][64];
+template <int DT, bool GATED, int SPLIT, int UNITS>
+__global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
+  constexpr int CT = GATED ? 2 : 1;
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
+  __shared__ f32x4 s_sum[2][kWaves][CT][64];
   __shared__ Routing s_routing;
+  __shared__ int s_token[kMaxTokens];  // the expert's
   read_routing(p, s_routing);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   // the blockIdx.y'th expert that has tokens, and the pairs before it
-  int expert = -1, rows = 0;
+  int expert = -1, pairs = 0;
   {
     int seen = 0;
     for (int base = 0; base < p.experts && expert < 0; base += 64) {
       const uint64_t mine = base + lane < p.experts ? mask_of(s_routing, base + lane) : 0;
       uint64_t live = __ballot(mine != 0);
       const int n = __builtin_popcountll(live), want = static_cast<int>(blockIdx.y) - seen;
-      int pairs = __builtin_popcountll(mine);
+      int count = __builtin_popcountll(mine);
       if (want < n) {
         for (int i = 0; i < want; ++i) live &= live - 1;
         const int at = __builtin_ctzll(live);
         expert = base + at;
-        if (lane >= at) pairs = 0;
+        if (lane >= at) count = 0;
       }
 #pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) pairs += __shfl_xor(pairs, d);
-      rows += pairs;
+      for (int d = 32; d >= 1; d >>= 1) count += __shfl_xor(count, d);
+      pairs += count;
       seen += n;
     }
   }
   if (expert < 0) return;
   expert = __builtin_amdgcn_readfirstlane(expert);
-  rows = __builtin_amdgcn_readfirstlane(rows);
+  pairs = __builtin_amdgcn_readfirstlane(pairs);
   const uint64_t mask = mask_of(s_routing, expert);
   const int tokens = __builtin_amdgcn_readfirstlane(__builtin_popcountll(mask));
+  if (wave == 0 && (mask >> lane & 1)) s_token[__builtin_popcountll(mask & ((uint64_t(1) << lane) - 1))] = lane;
+  __syncthreads();
 
-  const int64_t n0 = int64_t(16) * blockIdx.x, each = p.gated ? 2 * p.F : p.F, c0 = expert * each + n0;
-  const Channels ch[2] = {channels(p.w1q, p.w1s, c0, p.F - n0, p.pitch1, p.steps1),
-                          channels(p.w1q, p.w1s, p.gated ? c0 + p.F : c0, p.gated ? p.F - n0 : 0, p.pitch1, p.steps1)};
-  int first, last;
-  share_of(static_cast<int>(p.pitch1 / 64), wave, first, last);
-  for (int t0 = 0; t0 < tokens; t0 += 16) {
-    const int count = min(tokens - t0, 16);
-    // the token of the lane's column, as a place among the expert's
-    const int token = nth_token(mask, t0 + min(lane & 15, count - 1));
-    auto row = [&](int r) {
-      return static_cast<const char*>(p.x) + __shfl(token, r) * p.H * dtype_bytes(DT);
-    };
-    f32x4 acc[2] = {};
-    run_units<DT, RU, 2, 2>(ch, first, last, p.H, count, s_x[wave], row, acc);
-    __syncthreads();  // the sums before have been read
-    s_sum[wave][0][lane] = acc[0];
-    s_sum[wave][1][lane] = acc[1];
-    __syncthreads();
-    if (wave != 0) continue;
-    f32x4 v[2] = {s_sum[0][0][lane], s_sum[0][1][lane]};
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) {
-      v[0] += s_sum[w][0][lane];
-      v[1] += s_sum[w][1][lane];
-    }
-    if ((lane & 15) >= count) continue;
+  const int units = static_cast<int>(p.pitch1 / 64);
+  for (int t0 = 0; t0 < tokens; t0 += p.rows) {
+    const int rows = min(tokens - t0, p.rows);
+    const int token = s_token[t0 + min(lane & 15, rows - 1)];  // of the lane's column
     float weight = 0.0f;
     for (int j = 0; j < p.top_k; ++j) {
       const int s = token * p.top_k + j;
       if (id_of(p, s) == expert) weight += p.weights ? p.weights[s] : 1.0f;
     }
-    constexpr int kParts = h_parts(DT);
-    uint32_t out[kParts][2];
+    // as many steps of the rows as there are and have room
+    constexpr int kStep = SPLIT * UNITS;
+    const int room = (p.lds / (rows * parts_of(DT)) - 16) / (2 * kUnit) / kStep, steps = (units + kStep - 1) / kStep;
+    const int width = kUnit * kStep * min(room, steps);
+    if (t0 > 0) __syncthreads();  // the sums before have been read
+    stream_tiles<parts_of(DT), CT, SPLIT, UNITS>(
+        units, p.h_width / 16, blockIdx.x, gridDim.x, s_x, rows, width, s_sum,
+        [&](int64_t t) {
+          Tiles<CT> r;
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
-      float part[2][3];
+          for (int c = 0; c < CT; ++c)
+            r.ch[c] = channels(p.w1q, p.w1s, expert * (CT * p.F) + c * p.F + 16 * t, p.F - 16 * t, p.pitch1, p.steps1);
+          return r;
+        },
+        [&](int unit) {
+          __syncthreads();  // every wave is through with the rows before
+          stage_rows<DT>(s_x, rows, int64_t(kUnit) * unit, width, p.H, [&](int r) {
+            return static_cast<const char*>(p.x) + s_token[t0 + r] * p.H * dtype_bytes(DT);
+          });
+          __syncthreads();
+        },
+        [&](int64_t t, const f32x4 (&sum)[CT]) {
+          if ((lane & 15) >= rows) return;
+          constexpr int kParts = h_parts(DT);
+          uint32_t out[kParts][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float gate = v[0][e + i], other = v[1][e + i];
-        const float a = gate / (1.0f + expf(-gate));
-        split((p.gated ? a * other : a) * weight, part[i]);
-        // the last of the parts that are kept is rounded
-        if constexpr (kParts == 2) part[i][1] = part[i][1] + part[i][2];
-      }
+          for (int e = 0; e < 4; e += 2) {
+            float part[2][3];
 #pragma unroll
-      for (int k = 0; k < kParts; ++k)
-        out[k][e / 2] = k + 1 < kParts ? upper_halves(part[0][k], part[1][k]) : pack_pair<NF4_BF16>(part[0][k], part[1][k]);
-    }
-    const int64_t n = n0 + 4 * (lane >> 4);
-    uint16_t* to = p.h + (rows + t0 + (lane & 15)) * (kParts * p.h_width) + n;
+            for (int i = 0; i < 2; ++i) {
+              const float gate = sum[0][e + i], other = sum[CT - 1][e + i];
+              const float a = gate / (1.0f + expf(-gate));
+              split((GATED ? a * other : a) * weight, part[i]);
+              // the last of the parts that are kept is rounded
+              if constexpr (kParts == 2) part[i][1] = part[i][1] + part[i][2];
+            }
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) {
-      // (n is below h_width, which the channels' tiles fill; past F all is zero)
-      const bool live = n < p.F;
-      const uint2 two = {live ? out[k][0] : 0u, live ? out[k][1] : 0u};
-      *reinterpret_cast<uint2*>(to + k * p.h_width) = two;
-    }
+            for (int k = 0; k < kParts; ++k)
+              out[k][e / 2] =
+                  k + 1 < kParts ? upper_halves(part[0][k], part[1][k]) : pack_pair<NF4_BF16>(part[0][k], part[1][k]);
+          }
+          // (past F all is zero)
+          uint16_t* to = p.h + (pairs + t0 + (lane & 15)) * (kParts * p.h_width) + 16 * t + 4 * (lane >> 4);
+#pragma unroll
+          for (int k = 0; k < kParts; ++k)
+            *reinterpret_cast<uint2*>(to + k * p.h_width) = make_uint2(out[k][0], out[k][1]);
+        });
   }
 }
 
-template <int DT, int RU, int TT>
-__global__ __launch_bounds__(kThreads, 2) void mx_down_kernel(Mlp p) {
-  constexpr int kParts = h_parts(DT), kFrom = kSplit + kParts;
-  __shared__ __attribute__((aligned(16))) uint8_t s_h[kWaves][stage_bytes<kFrom, RU>()];
-  __shared__ f32x4 s_sum[kWaves][TT][64];
+// A wave's piece of LDS in down: rows of a unit at a pitch of 272 bytes (so that a chunk
+// of 16 rows lies in different banks), the parts one after the other.
+constexpr int kLdsRow = 2 * kUnit + 16;
+template <int DT, int RU>
+constexpr int wave_lds() {
+  return h_parts(DT) * 4 * RU * kLdsRow;
+}
+
+// An expert's rows of h, 4 RU at most, and its channels.
+struct Segment {
+  Channels ch[1];
+  const uint16_t* h;
+  int count;
+};
+
+// WAVES: of a workgroup; RU: loads of a lane for a unit's rows (four rows each); TT: tiles
+// of 16 tokens.
+template <int DT, int WAVES, int RU, int TT>
+__global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Mlp p) {
+  constexpr int kParts = h_parts(DT), kRows = 4 * RU, kAhead = 2;  // pairs of units in flight
+  constexpr int kSumBytes = WAVES * TT * 64 * 16, kHBytes = WAVES * wave_lds<DT, RU>();
+  __shared__ __attribute__((aligned(16))) uint8_t s_h[kHBytes > kSumBytes ? kHBytes : kSumBytes];
   __shared__ Routing s_routing;
-  __shared__ int s_list[kMaxExperts][2];  // the experts with tokens, and the pairs before each
-  __shared__ int s_live;
-  read_routing(p, s_routing);
+  __shared__ Segments<kRows> s_segments;
+  read_segments(p, s_routing, s_segments);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (wave == 0) {
-    int seen = 0, rows = 0;
-    for (int base = 0; base < p.experts; base += 64) {
-      const uint64_t mine = base + lane < p.experts ? mask_of(s_routing, base + lane) : 0;
-      const uint64_t live = __ballot(mine != 0);
-      const int pairs = __builtin_popcountll(mine);
-      int in = pairs;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(in, d);
-        if (lane >= d) in += o;
-      }
-      if (mine) {
-        const int at = seen + __builtin_popcountll(live & ((uint64_t(1) << lane) - 1));
-        s_list[at][0] = base + lane;
-        s_list[at][1] = rows + in - pairs;
-      }
-      seen += __builtin_popcountll(live);
-      rows += __shfl(in, 63);
-    }
-    if (lane == 0) s_live = seen;
-  }
-  __syncthreads();
-  const int live = s_live, units = static_cast<int>(p.pitch2 / 64);
+  const int units = static_cast<int>(p.pitch2 / 64), pairs = (units + 1) / 2;
   const int64_t n0 = int64_t(16) * blockIdx.x;
-  // the wave's units of all experts' (even numbers: whole lines)
-  const int64_t all = int64_t(live) * units;
-  const int64_t each = 2 * ((all + 2 * kWaves - 1) / (2 * kWaves));
-  int64_t at = min(all, wave * each);
-  const int64_t end = min(all, at + each);
+  auto segment = [&](int j) {
+    const int expert = __builtin_amdgcn_readfirstlane(s_segments.expert[j]), first = __builtin_amdgcn_readfirstlane(s_segments.first[j]);
+    const int tokens = __builtin_amdgcn_readfirstlane(__builtin_popcountll(mask_of(s_routing, expert)));
+    const int64_t place = __builtin_amdgcn_readfirstlane(s_segments.place[j]);
+    return Segment{{channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)},
+                   p.h + place * (kParts * p.h_width), min(tokens - first, kRows)};
+  };
+  // the waves take the pairs of units (whole lines) of all segments in turn
+  const int end = s_segments.count * pairs;
+  int at = wave;
+  uint8_t* lds = s_h + wave * wave_lds<DT, RU>();
   f32x4 total[TT] = {};
-  while (at < end) {
-    const int j = __builtin_amdgcn_readfirstlane(static_cast<int>(at / units));
-    const int first = static_cast<int>(at - int64_t(j) * units);
-    const int last = static_cast<int>(min(int64_t(units), end - int64_t(j) * units));
-    at += last - first;
-    const int expert = __builtin_amdgcn_readfirstlane(s_list[j][0]);
-    const int rows = __builtin_amdgcn_readfirstlane(s_list[j][1]);
-    const uint64_t mask = mask_of(s_routing, expert);
-    const int tokens = __builtin_amdgcn_readfirstlane(__builtin_popcountll(mask));
-    const Channels ch[1] = {channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)};
-    for (int t0 = 0; t0 < tokens; t0 += 16) {
-      const int count = min(tokens - t0, 16);
-      auto row = [&](int r) {
-        return reinterpret_cast<const char*>(p.h + static_cast<int64_t>(rows + t0 + r) * (kParts * p.h_width));
-      };
-      f32x4 acc[1] = {};
-      run_units<kFrom, RU, 1, 4>(ch, first, last, p.h_width, count, s_h[wave], row, acc);
-      // to the tokens' columns; the others keep theirs (not by adding zeros: a channel
-      // whose weights are NaN leaves the tokens of other experts alone)
+  if (at < end) {
+    Loaded w[kAhead][2];
+    u32x4 x[kAhead][2][RU][kParts];
+    int seg = at / pairs, pair = at - seg * pairs;
+    int ahead = at, next_seg = seg, next_pair = pair;
+    Segment next = segment(seg);
+    int count = next.count;
+    auto load = [&](int d) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int unit = 2 * next_pair + i;
+        const bool in = ahead < end && unit < units;
+        w[d][i] = load_unit(next.ch[0], unit, in);
+#pragma unroll
+        for (int j = 0; j < RU; ++j) {
+          if (!in || 4 * j >= next.count) continue;
+          const uint16_t* h =
+              next.h + min(4 * j + (lane >> 4), next.count - 1) * (kParts * p.h_width) + kUnit * unit + 8 * (lane & 15);
+#pragma unroll
+          for (int k = 0; k < kParts; ++k) x[d][i][j][k] = *reinterpret_cast<const u32x4*>(h + k * p.h_width);
+        }
+      }
+      ahead += WAVES;
+      next_pair += WAVES;
+      if (next_pair >= pairs && ahead < end) {
+        next_seg = ahead / pairs;
+        next_pair = ahead - next_seg * pairs;
+        next = segment(next_seg);
+      }
+    };
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) load(d);
+    f32x4 acc = {};
+    auto take = [&](int d) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (2 * pair + i >= units) break;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int j = 0; j < RU; ++j) {
+          if (4 * j >= count) break;
+#pragma unroll
+          for (int k = 0; k < kParts; ++k)
+            *reinterpret_cast<u32x4*>(lds + (k * kRows + 4 * j + (lane >> 4)) * kLdsRow + (lane & 15) * 16) = x[d][i][j][k];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        bf16x8 a[4];
+        operands(w[d][i], a);
+        // four rows' parts are columns of one product (what the others hold nobody asks for)
+        constexpr int kColumns = RU == 1 ? kParts * kRows : kRows;
+        const uint8_t* h = lds + min(lane & 15, kColumns - 1) * kLdsRow + 64 * (lane >> 4);
+#pragma unroll
+        for (int k = 0; k < (RU == 1 ? 1 : kParts); ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                a[e], *reinterpret_cast<const bf16x8*>(h + k * kRows * kLdsRow + 16 * e), acc, 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // After a pair: at the segment's end its sums go to the tokens' columns; the others
+    // keep theirs (not by adding zeros: a channel whose weights are NaN leaves the tokens
+    // of other experts alone).
+    auto advance = [&] {
+      at += WAVES;
+      pair += WAVES;
+      if (pair < pairs && at < end) return;
+      const uint64_t mask = mask_of(s_routing, s_segments.expert[seg]);
+      const int first = s_segments.first[seg];
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
         const int token = 16 * t + (lane & 15);
-        const int column = __builtin_popcountll(mask & ((uint64_t(1) << token) - 1)) - t0;
-        const bool has = (mask >> token & 1) && column >= 0 && column < 16;
+        const int column = __builtin_popcountll(mask & ((uint64_t(1) << token) - 1)) - first;
+        const bool has = (mask >> token & 1) && column >= 0 && column < kRows;
         const int from = (has ? column : 0) + (lane & 48);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float v = acc[0][e];
-          const float o = __shfl(v, from);
+          const float v = acc[e];
+          float o = __shfl(v, from);
+          if constexpr (RU == 1) {
+#pragma unroll
+            for (int k = 1; k < kParts; ++k) o += __shfl(v, from + k * kRows);
+          }
           if (has) total[t][e] += o;
         }
       }
+      acc = f32x4{};
+      if (at >= end) return;
+      seg = at / pairs;
+      pair = at - seg * pairs;
+      count = min(__builtin_popcountll(mask_of(s_routing, s_segments.expert[seg])) - s_segments.first[seg], kRows);
+      count = __builtin_amdgcn_readfirstlane(count);
+    };
+    // (the last ones apart: with a way out in the middle of the loop the compiler has each
+    // turn of it wait for all loads)
+    while (at + (kAhead - 1) * WAVES < end) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        take(d);
+        load(d);
+        advance();
+      }
     }
+#pragma unroll
+    for (int d = 0; d < kAhead - 1; ++d)
+      if (at < end) {
+        take(d);
+        advance();
+      }
   }
+  __syncthreads();  // every wave is through with its rows
+  f32x4* s_sum = reinterpret_cast<f32x4*>(s_h);  // [wave][token tile][lane]
 #pragma unroll
-  for (int t = 0; t < TT; ++t) s_sum[wave][t][lane] = total[t];
+  for (int t = 0; t < TT; ++t) s_sum[(wave * TT + t) * 64 + lane] = total[t];
   __syncthreads();
-  if (wave >= TT) return;
-  f32x4 sum = s_sum[0][wave][lane];
-#pragma unroll
-  for (int v = 1; v < kWaves; ++v) sum += s_sum[v][wave][lane];
   const int token = 16 * wave + (lane & 15);
   const int64_t n = n0 + 4 * (lane >> 4);
   const int left = static_cast<int>(min(p.H - n, int64_t(4)));
-  if (token >= p.T || left <= 0) return;
+  if (wave >= TT || token >= p.T || left <= 0) return;
+  f32x4 sum = s_sum[wave * 64 + lane];
+#pragma unroll
+  for (int v = 1; v < WAVES; ++v) sum += s_sum[(v * TT + wave) * 64 + lane];
   const float f[4] = {sum[0], sum[1], sum[2], sum[3]};
   store_four<DT>(p.y, token * p.H + n, left, f);
 }
 
-// Runs f with the loads of a unit's rows that `rows` rows (16 at most) take.
+// How a workgroup takes its tiles: `split` waves share K, a step is `units` units of each;
+// the rows lie in LDS `width` elements (whole steps) at a time.  Whole rows if they have
+// room, so that every tile finds them there, if need be with one workgroup to a compute
+// unit instead of two.
+struct Held {
+  int split, units, width;
+  int64_t bytes, groups;  // of LDS; of tiles
+  bool two;               // workgroups to a compute unit
+};
+constexpr int64_t kWholeLds = 112 << 10, kHalfLds = 36 << 10;
+
+// tiles: of 16 channels, of all experts that may have tokens.
+Held hold(int64_t units, int64_t rows, int64_t tiles) {
+  Held h = {};
+  auto bytes = [&](int64_t step) { return rows * lds_row(static_cast<int>(kUnit * step)); };
+  // four units of each wave to a step, and as many waves to a tile as that leaves work
+  // (a tile's waves meet at its end); more where there are few tiles
+  h.split = units >= 32 ? 8 : units >= 16 ? 4 : units >= 8 ? 2 : 1;
+  while (h.split < kWaves && units > h.split && tiles * h.split < int64_t(kWaves) * device_cus()) h.split *= 2;
+  auto per_wave = [&] { return (units + h.split - 1) / h.split; };
+  if (bytes(units) > kWholeLds) h.split = kWaves;
+  h.units = h.split < 8 || per_wave() > 2 ? 4 : per_wave() > 1 ? 2 : 1;
+  while (h.units > 1 && bytes(h.split * h.units) > kWholeLds) h.units /= 2;
+  const int64_t step = h.split * h.units, all = units > 0 ? (units + step - 1) / step : 1;
+  const int64_t room = kWholeLds / bytes(step);  // (48 rows' step of 8 units is 97 KiB)
+  h.width = static_cast<int>(kUnit * step * (all < room ? all : room));
+  h.bytes = bytes(h.width / kUnit);
+  h.groups = (tiles + kWaves / h.split - 1) / (kWaves / h.split);
+  h.two = h.bytes <= kHalfLds;
+  return h;
+}
+
 template <class F>
-void with_loads(int64_t rows, F&& f) {
-  if (rows <= 4)
-    f(std::integral_constant<int, 1>{});
-  else if (rows <= 8)
-    f(std::integral_constant<int, 2>{});
+void with_split(const Held& h, F&& f) {
+  auto run = [&](auto split, auto units) { f(split, units); };
+  if (h.split == 8 && h.units == 1)
+    run(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
+  else if (h.split == 8 && h.units == 2)
+    run(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+  else if (h.split == 8)
+    run(std::integral_constant<int, 8>{}, std::integral_constant<int, 4>{});
+  else if (h.split == 4)
+    run(std::integral_constant<int, 4>{}, std::integral_constant<int, 4>{});
+  else if (h.split == 2)
+    run(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
   else
-    f(std::integral_constant<int, 4>{});
+    run(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
 }
 
 int64_t h_width(int64_t F) { return (F + kUnit - 1) / kUnit * kUnit; }
 
-bool known_mlp(int64_t T, int32_t top_k, int64_t F, int32_t dtype) {
-  return T >= 0 && T <= kMaxTokens && top_k >= 1 && top_k <= kMaxTopK && F >= 0 && F <= kMaxK && known_dtype(dtype);
+bool known_mlp(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F, int32_t dtype) {
+  return T >= 0 && T <= kMaxTokens && top_k >= 1 && top_k <= kMaxTopK && experts >= 0 && experts <= kMaxExperts &&
+         H >= 0 && H <= kMaxK && F >= 0 && F <= kMaxK && known_dtype(dtype);
+}
+
+size_t h_bytes(int64_t T, int32_t top_k, int64_t F, int32_t dtype) {
+  return static_cast<size_t>(T * top_k * h_parts(dtype) * h_width(F) * 2 + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -567,24 +778,28 @@ nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const u
   if (!aligned(x, dtype_bytes(x_dtype)) || !aligned(wq, 16) || !aligned(ws, 16) || !aligned(y, dtype_bytes(y_dtype)))
     return NF4_EINVAL;
   if (N > kMaxDim || K > kMaxK) return NF4_EUNSUPPORTED;
-  const Gemv p = {x, wq, ws, y, M, N, K, pitch_of(K), steps_of(K)};
-  const int64_t tiles = (N + 15) / 16, most = 2 * device_cus();
-  const dim3 grid(static_cast<uint32_t>(tiles < most ? tiles : most));
+  const int64_t tiles = (N + 15) / 16, units = pitch_of(K) / 64;
+  Gemv p = {x, wq, ws, y, M, N, K, pitch_of(K), steps_of(K), 0};
+  const Held held = hold(units, M * parts_of(x_dtype), tiles);
+  p.width = held.width;
+  const int64_t most = (held.two ? 2 : 1) * device_cus();
+  const dim3 grid(static_cast<uint32_t>(held.groups < most ? held.groups : most));
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  with_dtype(x_dtype, [&](auto a) {
-    with_dtype(y_dtype, [&](auto d) {
-      with_loads(M, [&](auto r) {
-        hipLaunchKernelGGL((mx_gemv_kernel<decltype(a)::value, decltype(d)::value, decltype(r)::value>), grid,
-                           dim3(kThreads), 0, st, p);
+  with_split(held, [&](auto split, auto u) {
+    with_dtype(x_dtype, [&](auto a) {
+      with_dtype(y_dtype, [&](auto d) {
+        hipLaunchKernelGGL(
+            (mx_gemv_kernel<decltype(a)::value, decltype(d)::value, decltype(split)::value, decltype(u)::value>), grid,
+            dim3(kThreads), static_cast<uint32_t>(held.bytes), st, p);
       });
     });
   });
   return launch_status();
 }
 
-size_t mxfp4_moe_mlp_workspace_size(int64_t T, int32_t top_k, int64_t F, int32_t dtype) {
-  if (!known_mlp(T, top_k, F, dtype)) return 0;
-  return static_cast<size_t>(T * top_k * h_parts(dtype) * h_width(F) * 2 + 255) / 256 * 256;
+size_t mxfp4_moe_mlp_workspace_size(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F, int32_t dtype) {
+  if (!known_mlp(T, top_k, experts, H, F, dtype)) return 0;
+  return h_bytes(T, top_k, F, dtype);
 }
 
 nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const uint8_t* w1s,
@@ -601,10 +816,9 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
     return NF4_EINVAL;
   if (experts > 0 && F > 0 && (!w1q || !w1s || !w2q || !w2s)) return NF4_EINVAL;
   if (!aligned(w1q, 16) || !aligned(w1s, 16) || !aligned(w2q, 16) || !aligned(w2s, 16)) return NF4_EINVAL;
-  if (!known_mlp(T, top_k, F, dtype) || H > kMaxK || experts > kMaxExperts || experts * H > kMaxDim ||
-      experts * F * (gated ? 2 : 1) > kMaxDim)
+  if (!known_mlp(T, top_k, experts, H, F, dtype) || experts * H > kMaxDim || experts * F * (gated ? 2 : 1) > kMaxDim)
     return NF4_EUNSUPPORTED;
-  const size_t need = mxfp4_moe_mlp_workspace_size(T, top_k, F, dtype);
+  const size_t need = h_bytes(T, top_k, F, dtype);
   if (need > 0 && (!workspace || workspace_bytes < need)) return NF4_EINVAL;
   Mlp p = {};
   p.x = x, p.w1q = w1q, p.w1s = w1s, p.w2q = w2q, p.w2s = w2s, p.ids = ids, p.weights = weights, p.y = y;
@@ -614,19 +828,39 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
   p.T = static_cast<int>(T), p.top_k = top_k, p.experts = F > 0 ? experts : 0, p.id_bytes = id_bytes, p.gated = gated;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   const int64_t slots = T * top_k, live = experts < slots ? experts : slots;
+  // rows at a time: twice as many as an expert has on average, eight at least
+  const int64_t often = live > 0 ? 2 * ((slots + live - 1) / live) : 0, some = often < 8 ? 8 : often < 16 ? often : 16;
+  p.rows = static_cast<int>(T < some ? T : some);
+  const int64_t tiles = p.h_width / 16;
+  const Held held = hold(p.pitch1 / 64, p.rows * parts_of(dtype), tiles * live);
+  p.lds = static_cast<int>(held.bytes);
+  // few rows to an expert: four at a time
+  const bool four = T <= 4 || slots <= 2 * live;
+  const dim3 grid(static_cast<uint32_t>((H + 15) / 16));
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
-    with_loads(T, [&](auto r) {
-      constexpr int RU = decltype(r)::value;
-      if (p.experts > 0)
-        hipLaunchKernelGGL((mx_up_kernel<DT, RU>), dim3(static_cast<uint32_t>(p.h_width / 16), static_cast<uint32_t>(live)),
-                           dim3(kThreads), 0, st, p);
-      const dim3 grid(static_cast<uint32_t>((H + 15) / 16));
-      if (T <= 16)
-        hipLaunchKernelGGL((mx_down_kernel<DT, RU, 1>), grid, dim3(kThreads), 0, st, p);
-      else if constexpr (RU == 4)
-        hipLaunchKernelGGL((mx_down_kernel<DT, RU, 4>), grid, dim3(kThreads), 0, st, p);
-    });
+    if (p.experts > 0) {
+      const int64_t share = ((held.two ? 2 : 1) * device_cus() + live - 1) / live;
+      const int64_t groups = (tiles + kWaves / held.split - 1) / (kWaves / held.split);
+      const dim3 up(static_cast<uint32_t>(groups < share ? groups : share), static_cast<uint32_t>(live));
+      with_split(held, [&](auto split, auto u) {
+        constexpr int SPLIT = decltype(split)::value, UNITS = decltype(u)::value;
+        if (gated)
+          hipLaunchKernelGGL((mx_up_kernel<DT, true, SPLIT, UNITS>), up, dim3(kThreads), static_cast<uint32_t>(p.lds), st,
+                             p);
+        else
+          hipLaunchKernelGGL((mx_up_kernel<DT, false, SPLIT, UNITS>), up, dim3(kThreads), static_cast<uint32_t>(p.lds),
+                             st, p);
+      });
+    }
+    if (four && T <= 16)
+      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1>), grid, dim3(1024), 0, st, p);
+    else if (four)
+      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 4>), grid, dim3(1024), 0, st, p);
+    else if (T <= 16)
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1>), grid, dim3(512), 0, st, p);
+    else
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 4>), grid, dim3(512), 0, st, p);
   });
   return launch_status();
 }
