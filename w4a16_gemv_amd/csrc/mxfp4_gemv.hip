@@ -389,10 +389,13 @@ __device__ __forceinline__ int64_t id_of(const Mlp& p, int slot) {
 
 // Fills the masks; past it every wave may read them.
 __device__ __forceinline__ void read_routing(const Mlp& p, Routing& r) {
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) r.masks[e][0] = r.masks[e][1] = 0;
+  // (the ids are asked for first: the kernel can do nothing without them)
+  const int slots = p.T * p.top_k;
+  int64_t e = threadIdx.x < slots ? id_of(p, threadIdx.x) : -1;
+  for (int i = threadIdx.x; i < p.experts; i += blockDim.x) r.masks[i][0] = r.masks[i][1] = 0;
   __syncthreads();
-  for (int s = threadIdx.x; s < p.T * p.top_k; s += blockDim.x) {
-    const int64_t e = id_of(p, s);
+  for (int s = threadIdx.x; s < slots; s += blockDim.x) {
+    if (s != threadIdx.x) e = id_of(p, s);
     const int t = s / p.top_k;
     if (e >= 0 && e < p.experts) atomicOr(&r.masks[e][t >> 5], 1u << (t & 31));
   }
@@ -449,7 +452,8 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
   __shared__ f32x4 s_sum[2][kWaves][CT][64];
   __shared__ Routing s_routing;
-  __shared__ int s_token[kMaxTokens];  // the expert's
+  __shared__ int s_token[kMaxTokens];     // the expert's
+  __shared__ float s_weight[kMaxTokens];  // the router's, of these
   read_routing(p, s_routing);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   // the blockIdx.y'th expert that has tokens, and the pairs before it
@@ -484,12 +488,6 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
   const int units = static_cast<int>(p.pitch1 / 64);
   for (int t0 = 0; t0 < tokens; t0 += p.rows) {
     const int rows = min(tokens - t0, p.rows);
-    const int token = s_token[t0 + min(lane & 15, rows - 1)];  // of the lane's column
-    float weight = 0.0f;
-    for (int j = 0; j < p.top_k; ++j) {
-      const int s = token * p.top_k + j;
-      if (id_of(p, s) == expert) weight += p.weights ? p.weights[s] : 1.0f;
-    }
     // as many steps of the rows as there are and have room
     constexpr int kStep = SPLIT * UNITS;
     const int room = (p.lds / (rows * parts_of(DT)) - 16) / (2 * kUnit) / kStep, steps = (units + kStep - 1) / kStep;
@@ -506,6 +504,15 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
         },
         [&](int unit) {
           __syncthreads();  // every wave is through with the rows before
+          if (unit == 0 && t0 == 0 && threadIdx.x < tokens) {
+            // a few loads one after the other, while the first weights are on their way
+            float weight = 0.0f;
+            for (int j = 0; j < p.top_k; ++j) {
+              const int s = s_token[threadIdx.x] * p.top_k + j;
+              if (id_of(p, s) == expert) weight += p.weights ? p.weights[s] : 1.0f;
+            }
+            s_weight[threadIdx.x] = weight;
+          }
           stage_rows<DT>(s_x, rows, int64_t(kUnit) * unit, width, p.H, [&](int r) {
             return static_cast<const char*>(p.x) + s_token[t0 + r] * p.H * dtype_bytes(DT);
           });
@@ -513,6 +520,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
         },
         [&](int64_t t, const f32x4 (&sum)[CT]) {
           if ((lane & 15) >= rows) return;
+          const float weight = s_weight[t0 + (lane & 15)];
           constexpr int kParts = h_parts(DT);
           uint32_t out[kParts][2];
 #pragma unroll
@@ -575,9 +583,10 @@ __global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Ml
     return Segment{{channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)},
                    p.h + place * (kParts * p.h_width), min(tokens - first, kRows)};
   };
-  // the waves take the pairs of units (whole lines) of all segments in turn
-  const int end = s_segments.count * pairs;
-  int at = wave;
+  // the wave's pairs of units (whole lines) of all segments'
+  const int all = s_segments.count * pairs, each = (all + WAVES - 1) / WAVES;
+  int at = min(all, wave * each);
+  const int end = min(all, at + each);
   uint8_t* lds = s_h + wave * wave_lds<DT, RU>();
   f32x4 total[TT] = {};
   if (at < end) {
@@ -602,12 +611,10 @@ __global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Ml
           for (int k = 0; k < kParts; ++k) x[d][i][j][k] = *reinterpret_cast<const u32x4*>(h + k * p.h_width);
         }
       }
-      ahead += WAVES;
-      next_pair += WAVES;
-      if (next_pair >= pairs && ahead < end) {
-        next_seg = ahead / pairs;
-        next_pair = ahead - next_seg * pairs;
-        next = segment(next_seg);
+      ++ahead;
+      if (++next_pair == pairs && ahead < end) {
+        next_pair = 0;
+        next = segment(++next_seg);
       }
     };
 #pragma unroll
@@ -644,9 +651,8 @@ __global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Ml
     // keep theirs (not by adding zeros: a channel whose weights are NaN leaves the tokens
     // of other experts alone).
     auto advance = [&] {
-      at += WAVES;
-      pair += WAVES;
-      if (pair < pairs && at < end) return;
+      ++at;
+      if (++pair < pairs && at < end) return;
       const uint64_t mask = mask_of(s_routing, s_segments.expert[seg]);
       const int first = s_segments.first[seg];
 #pragma unroll
@@ -668,14 +674,14 @@ __global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Ml
       }
       acc = f32x4{};
       if (at >= end) return;
-      seg = at / pairs;
-      pair = at - seg * pairs;
+      pair = 0;
+      ++seg;
       count = min(__builtin_popcountll(mask_of(s_routing, s_segments.expert[seg])) - s_segments.first[seg], kRows);
       count = __builtin_amdgcn_readfirstlane(count);
     };
     // (the last ones apart: with a way out in the middle of the loop the compiler has each
     // turn of it wait for all loads)
-    while (at + (kAhead - 1) * WAVES < end) {
+    while (at + kAhead - 1 < end) {
 #pragma unroll
       for (int d = 0; d < kAhead; ++d) {
         take(d);
