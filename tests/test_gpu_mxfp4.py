@@ -236,7 +236,8 @@ DENSE = [(1, 1, 1), (1, 8, 18), (3, 17, 33), (16, 100, 129), (15, 33, 255), (1, 
          (1, 9, 12576), (4, 40, 20000), (16, 65, 12000), (17, 40, 128), (100, 20, 300), (42, 2766, 16), (1, 8, 22885),
          (80, 2885, 16), (1271, 8, 15833), (1962, 257, 16), (1, 1019, 28214), (2210, 490, 17), (69, 1856, 41721),
          (1531, 1359, 16), (257, 1619, 34814), (2456, 3478, 1911), (1996, 2597, 2779), (333, 4099, 1501),
-         (4352, 4096, 1500), (5500, 4000, 1650), (4097, 4096, 256), (300, 300, 300), (130, 129, 1000)]
+         (4352, 4096, 1500), (5500, 4000, 1650), (4097, 4096, 256), (300, 300, 300), (130, 129, 1000),
+         (3, 16400, 2000), (2, 32800, 1000), (5, 65600, 500)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -350,7 +351,8 @@ def test_gemm_weights_past_4_gib(M):
 
 @pytest.mark.parametrize("xdtype", TYPES, ids=str)
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 4096, 4096), (2, 33, 31), (3, 100, 127), (4, 17, 1501), (5, 40, 11008),
-                                   (7, 64, 4097), (8, 48, 129), (9, 20, 640), (16, 300, 2000), (16, 9000, 256), (1, 16, 70001)])
+                                   (7, 64, 4097), (8, 48, 129), (9, 20, 640), (16, 300, 2000), (16, 9000, 256), (1, 16, 70001),
+                                   (3, 33000, 500), (5, 33000, 1000), (2, 33000, 2000), (16, 300, 9000)])
 def test_gemv(M, N, K, xdtype):
     """Exact for activations of few bits; within the bound for any."""
     g = torch.Generator(device=dev()).manual_seed(M + K)
@@ -420,7 +422,8 @@ def routing(seed, T, k, E, drop=0.1):
 
 GROUPED = [(1, 2, 1, 8, 20), (5, 2, 3, 33, 300), (16, 4, 64, 40, 512), (1, 1, 1, 11, 4989), (1, 3, 1, 8, 11821),
            (3, 1, 1, 8, 13844), (18, 1, 1, 8, 16), (1687, 3, 1, 33, 17), (208, 3, 50, 163, 19), (1167, 4, 50, 150, 16),
-           (1726, 3, 60, 285, 17), (586, 4, 10, 3044, 1568), (700, 2, 8, 1000, 1100)]
+           (1726, 3, 60, 285, 17), (586, 4, 10, 3044, 1568), (700, 2, 8, 1000, 1100),
+           (20, 2, 64, 400, 1100), (20, 2, 64, 800, 600), (20, 2, 64, 1600, 300)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K", GROUPED)

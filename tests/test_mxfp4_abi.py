@@ -227,7 +227,7 @@ def _variant(plan, detail):
 
 def test_the_gpu_tests_reach_every_variant(lib):
     """A rule that is measured anew may send their sizes elsewhere; then they need others."""
-    units = {(-1, u) for u in (4, 8, 12, 22)}
+    units = {(-1, u) for u in (4, 8, 12, 22, -4, -2, -1)}
     reached = {_variant(*on_gpu.plan(M, N, K)) for M, N, K in on_gpu.DENSE}
     want = units | {(i, s) for i in range(5) for s in ("whole K", "split K")} | {(5, shares) for shares in (1, 2, 3, 5)}
     assert reached >= want, want - reached

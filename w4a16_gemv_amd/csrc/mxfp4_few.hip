@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mxfp4.h"
 #include "mxfp4_format.h"
 #include "mxfp4_product.h"
@@ -31,8 +33,8 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 }
 
 // ---------------------------------------------------------------------------
-// Up to 16 tokens, whose codes and scales a workgroup keeps in LDS.  Its eight waves
-// share K, and it goes through its channels 16 at a time: the weights go from memory
+// Up to 16 tokens, whose codes and scales a workgroup keeps in LDS.  It goes through its
+// channels in tiles of 16, 8 / SPLIT at a time, each with SPLIT waves that share K: the weights go from memory
 // through registers to the matrix cores (v_mfma_scale_f32_16x16x128_f8f6f4: lane i +
 // 16 g holds the codes 32 g .. + 31 of row i of A, B likewise with i the column, and
 // D[4 g .. + 3][i]), each byte read once, the next tile's asked for as soon as the
@@ -42,16 +44,18 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 // Tokens that are not codes yet (XT other than kCodes) are encoded on the way to LDS,
 // after the workgroup's first weights have been asked for.
 // ---------------------------------------------------------------------------
-template <int XT, int DT, bool GROUPED, int UNITS>
+template <int XT, int DT, bool GROUPED, int SPLIT, int UNITS>
 __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void mx_row_kernel(Product p, const void* x, int64_t K) {
   __shared__ f32x4 s_sum[2][kRowWaves][64];
   extern __shared__ __attribute__((aligned(16))) uint8_t s_x[];
-  const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16);
+  constexpr uint32_t kGroup = kRowWaves / SPLIT;  // tiles at a time
+  const uint32_t tiles = static_cast<uint32_t>((p.N + 15) / 16), groups_n = (tiles + kGroup - 1) / kGroup;
   RowTile t = {int64_t(16) * blockIdx.y, min(p.M, int64_t(16) * blockIdx.y + 16), 0};
   if constexpr (GROUPED) t = find_tile<16>(p, blockIdx.y);
   if (t.end <= t.first) return;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int pitch = static_cast<int>(p.pitch), rows = static_cast<int>(t.end - t.first);
+  const int share = wave % SPLIT;  // of K
   // a unit as it is loaded: lane 4 i + g has 16 bytes g of row i, so that four lanes
   // read 64 bytes in a row; turned() hands them to lane i + 16 g
   const int row = lane >> 2, inside = (lane & 3) * 16, g = lane >> 4;
@@ -64,30 +68,31 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void mx_row_kernel(
   };
   // the wave's units of 64 bytes: pairs, so that two loads read whole lines
   const int units = pitch / 64;
-  auto unit = [&](int u) { return 2 * wave + 2 * kRowWaves * (u >> 1) + (u & 1); };
+  auto unit = [&](int u) { return 2 * share + 2 * SPLIT * (u >> 1) + (u & 1); };
   const uint32_t voff = static_cast<uint32_t>(row * pitch + inside);
   const uint8_t* w0 = p.wq + t.expert * p.N * p.pitch;
   i32x4 w[UNITS];
   uint32_t ws[UNITS];
-  struct Rows {
+  struct Tile {
     __amdgpu_buffer_rsrc_t codes, scales;
     uint32_t at;  // of the lane's row's scales
   };
-  auto range = [&](uint32_t tile) {
+  auto range = [&](uint32_t group) {
+    const uint32_t tile = group * kGroup + wave / SPLIT;
     const int64_t n0 = static_cast<int64_t>(min(tile, tiles - 1)) * 16, c0 = t.expert * p.N + n0;
     const int64_t wide = tile < tiles ? min(int64_t(16), p.N - n0) : 0;  // no rows: zeros
-    return Rows{rsrc(w0 + n0 * p.pitch, static_cast<uint32_t>(wide * p.pitch)),
+    return Tile{rsrc(w0 + n0 * p.pitch, static_cast<uint32_t>(wide * p.pitch)),
                 rsrc(p.ws + (c0 >> 5) * p.steps * 256,
                      static_cast<uint32_t>(wide > 0 ? (((c0 + wide + 31) >> 5) - (c0 >> 5)) * p.steps * 256 : 0)),
                 scale_from(c0, c0 + (lane & 15), p.steps, 0)};
   };
-  auto load = [&](const Rows& r, int u) {
+  auto load = [&](const Tile& r, int u) {
     const bool in = unit(u) < units;
     w[u] = __builtin_bit_cast(
         i32x4, __builtin_amdgcn_raw_buffer_load_b128(r.codes, in ? voff + 64 * unit(u) : kNever, 0, 0));
     ws[u] = __builtin_amdgcn_raw_buffer_load_b32(r.scales, in ? r.at + 128 * unit(u) : kNever, 0, 0);
   };
-  const Rows first = range(blockIdx.x);
+  const Tile first = range(blockIdx.x);
 #pragma unroll
   for (int u = 0; u < UNITS; ++u) load(first, u);
 
@@ -95,38 +100,47 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void mx_row_kernel(
   const int wide = lds_pitch(pitch), groups = lds_groups(pitch);
   uint32_t* s_scale = reinterpret_cast<uint32_t*>(s_x + rows * wide);
   if constexpr (XT == kCodes) {
-    for (int r = 0; r < rows; ++r) {
+    // a row of codes after the other to the threads, 16 bytes each, and of scales
+    const int pieces = pitch / 16;
+    for (int i = threadIdx.x; i < rows * pieces; i += kRowThreads) {
+      const int r = i / pieces, at = 16 * (i - r * pieces);
       const int64_t src = source_row<GROUPED>(p, t.first + r);
       const uint8_t* q = src >= 0 ? p.xq + src * p.pitch : w0;  // any row that may be read
-      for (int at = 16 * threadIdx.x; at < pitch; at += 16 * kRowThreads)
-        *reinterpret_cast<i32x4*>(s_x + r * wide + at) = *reinterpret_cast<const i32x4*>(q + at);
-      for (int u = threadIdx.x; u < units; u += kRowThreads)
-        s_scale[r * groups + u] = src >= 0 ? *reinterpret_cast<const uint32_t*>(p.xs + scale_at(src, p.steps, u)) : 0u;
+      *reinterpret_cast<i32x4*>(s_x + r * wide + at) = *reinterpret_cast<const i32x4*>(q + at);
+    }
+    for (int i = threadIdx.x; i < rows * units; i += kRowThreads) {
+      const int r = i / units, u = i - r * units;
+      const int64_t src = source_row<GROUPED>(p, t.first + r);
+      s_scale[r * groups + u] = src >= 0 ? *reinterpret_cast<const uint32_t*>(p.xs + scale_at(src, p.steps, u)) : 0u;
     }
   } else {
-    // four rows' loads at a time
-    for (int r0 = 0; r0 < rows; r0 += 4)
-      for (int at = 8 * threadIdx.x; at < 2 * pitch; at += 8 * kRowThreads) {
-        Piece<XT> v[4];
+    // sixteen lanes take a group of 128 elements of a row, several groups' loads at a time
+    constexpr int kAtOnce = XT == INT8_FP32 ? 4 : 8;
+    const int eights = pitch / 4, all = rows * eights;
+    for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kRowThreads) {
+      Piece<XT> v[kAtOnce];
+      int r[kAtOnce], at[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = Piece<XT>{};
-          if (r0 + i < rows && at < K)
-            v[i] = load_piece<XT>(static_cast<const char*>(x) + (t.first + r0 + i) * K * dtype_bytes(XT), at, K);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (r0 + i >= rows) break;
-          uint32_t m = piece_peak<XT>(v[i]);
-          m = max(m, dpp<0xB1>(m));  // the neighbour
-          m = max(m, dpp<0x4E>(m));  // the other pair of the four, a block
-          const uint32_t e = block_scale(m);
-          *reinterpret_cast<uint32_t*>(s_x + (r0 + i) * wide + at / 2) = encode_piece<XT>(v[i], e);
-          uint32_t s = e | dpp<0x104>(e) << 8;  // four blocks' in the first of sixteen lanes
-          s |= dpp<0x108>(s) << 16;
-          if ((lane & 15) == 0) s_scale[(r0 + i) * groups + at / 128] = s;
-        }
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + k * kRowThreads;
+        r[k] = i / eights, at[k] = 8 * (i - r[k] * eights);
+        v[k] = Piece<XT>{};
+        if (i < all && at[k] < K)
+          v[k] = load_piece<XT>(static_cast<const char*>(x) + (t.first + r[k]) * K * dtype_bytes(XT), at[k], K);
       }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (i0 + k * kRowThreads >= all) break;
+        uint32_t m = piece_peak<XT>(v[k]);
+        m = max(m, dpp<0xB1>(m));  // the neighbour
+        m = max(m, dpp<0x4E>(m));  // the other pair of the four, a block
+        const uint32_t e = block_scale(m);
+        *reinterpret_cast<uint32_t*>(s_x + r[k] * wide + at[k] / 2) = encode_piece<XT>(v[k], e);
+        uint32_t s = e | dpp<0x104>(e) << 8;  // four blocks' in the first of sixteen lanes
+        s |= dpp<0x108>(s) << 16;
+        if ((lane & 15) == 0) s_scale[r[k] * groups + at[k] / 128] = s;
+      }
+    }
   }
   __syncthreads();
 
@@ -136,8 +150,8 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void mx_row_kernel(
   const uint8_t* xc = s_x + mine * wide + 16 * g;
   const uint32_t* xs = s_scale + mine * groups;
   int turn = 0;
-  for (uint32_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++turn) {
-    const Rows next = range(tile + gridDim.x);
+  for (uint32_t group = blockIdx.x; group < groups_n; group += gridDim.x, ++turn) {
+    const Tile next = range(group + gridDim.x);
     f32x4 acc = {};
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
@@ -153,14 +167,19 @@ __global__ __launch_bounds__(kRowThreads, UNITS > 8 ? 2 : 4) void mx_row_kernel(
         load(next, u);
       }
     }
-    s_sum[turn & 1][wave][lane] = acc;
-    __syncthreads();
-    // one wave a turn adds up; its buffer is written again two turns later, after
-    // a barrier that this wave reaches when it is through
-    if (wave != (turn & (kRowWaves - 1))) continue;
-    f32x4 sum = s_sum[turn & 1][0][lane];
+    const uint32_t tile = group * kGroup + wave / SPLIT;
+    settled(acc);
+    f32x4 sum = acc;
+    if constexpr (SPLIT > 1) {
+      s_sum[turn & 1][wave][lane] = acc;
+      __syncthreads();
+      // one of a tile's waves a turn adds up; its buffer is written again two turns later,
+      // after a barrier that this wave reaches when it is through
+      if (share != (turn & (SPLIT - 1))) continue;
+      sum = s_sum[turn & 1][wave - share][lane];
 #pragma unroll
-    for (int v = 1; v < kRowWaves; ++v) sum += s_sum[turn & 1][v][lane];
+      for (int v = 1; v < SPLIT; ++v) sum += s_sum[turn & 1][wave - share + v][lane];
+    }
     const int64_t n = static_cast<int64_t>(tile) * 16 + 4 * g;
     const int left = static_cast<int>(min(p.N - n, int64_t(4)));
     if (m >= t.end || left <= 0) continue;
@@ -180,22 +199,29 @@ int64_t lds_bytes(int64_t pitch, int64_t rows) {
 
 template <int XT, bool GROUPED>
 nf4_status launch_typed(const Product& p, const void* x, int64_t K, int32_t y_dtype, hipStream_t st) {
-  const int64_t tiles = (p.N + 15) / 16, rows = row_tiles<GROUPED>(p, 16);
+  const int64_t rows = row_tiles<GROUPED>(p, 16);
+  const Rows r = row_plan(p, rows);
   // two workgroups fit a compute unit
+  const int64_t groups = ((p.N + 15) / 16 * r.split + kRowWaves - 1) / kRowWaves;
   const int64_t most = 2 * device_cus(), share = (most + rows - 1) / rows;
-  const dim3 grid(static_cast<uint32_t>(tiles < share ? tiles : share), static_cast<uint32_t>(rows));
-  const int64_t units = row_units(p.pitch);
+  const dim3 grid(static_cast<uint32_t>(groups < share ? groups : share), static_cast<uint32_t>(rows));
   const uint32_t lds = static_cast<uint32_t>(lds_bytes(p.pitch, p.M < 16 ? p.M : 16));
   with_dtype(y_dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
-    if (units == 4)
-      hipLaunchKernelGGL((mx_row_kernel<XT, DT, GROUPED, 4>), grid, dim3(kRowThreads), lds, st, p, x, K);
-    else if (units == 8)
-      hipLaunchKernelGGL((mx_row_kernel<XT, DT, GROUPED, 8>), grid, dim3(kRowThreads), lds, st, p, x, K);
-    else if (units == 12)
-      hipLaunchKernelGGL((mx_row_kernel<XT, DT, GROUPED, 12>), grid, dim3(kRowThreads), lds, st, p, x, K);
-    else
-      hipLaunchKernelGGL((mx_row_kernel<XT, DT, GROUPED, 22>), grid, dim3(kRowThreads), lds, st, p, x, K);
+    auto run = [&](auto split, auto units) {
+      hipLaunchKernelGGL((mx_row_kernel<XT, DT, GROUPED, decltype(split)::value, decltype(units)::value>), grid,
+                         dim3(kRowThreads), lds, st, p, x, K);
+    };
+    using std::integral_constant;
+    switch (r.split == kRowWaves ? r.units : -r.split) {
+      case 4: run(integral_constant<int, 8>{}, integral_constant<int, 4>{}); break;
+      case 8: run(integral_constant<int, 8>{}, integral_constant<int, 8>{}); break;
+      case 12: run(integral_constant<int, 8>{}, integral_constant<int, 12>{}); break;
+      case 22: run(integral_constant<int, 8>{}, integral_constant<int, 22>{}); break;
+      case -4: run(integral_constant<int, 4>{}, integral_constant<int, 4>{}); break;
+      case -2: run(integral_constant<int, 2>{}, integral_constant<int, 4>{}); break;
+      default: run(integral_constant<int, 1>{}, integral_constant<int, 4>{}); break;
+    }
   });
   return launch_status();
 }
@@ -204,9 +230,16 @@ nf4_status launch_typed(const Product& p, const void* x, int64_t K, int32_t y_dt
 
 namespace mxdev {
 
-int64_t row_units(int64_t pitch) {
-  const int64_t units = (pitch / 64 + kRowWaves - 1) / kRowWaves;
-  return units <= 4 ? 4 : units <= 8 ? 8 : units <= 12 ? 12 : 22;
+Rows row_plan(const Product& p, int64_t rows) {
+  const int64_t units = p.pitch / 64, tiles = rows * ((p.N + 15) / 16);
+  Rows r = {kRowWaves, 0};
+  // four units to a wave where that leaves each compute unit two workgroups: a tile's waves
+  // meet at its end
+  while (r.split > 1 && 4 * (r.split / 2) >= units && tiles * (r.split / 2) >= int64_t(2 * kRowWaves) * device_cus())
+    r.split /= 2;
+  const int64_t each = (units + r.split - 1) / r.split;
+  r.units = each <= 4 ? 4 : each <= 8 ? 8 : each <= 12 ? 12 : 22;
+  return r;
 }
 
 bool fits_rows(const Product& p, int64_t rows) {

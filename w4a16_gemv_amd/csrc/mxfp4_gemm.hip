@@ -521,6 +521,10 @@ __global__ __launch_bounds__(64 * WM* WN* WK) void mx_stream_kernel(Product p) {
         for (int e = 0; e < 4; ++e) acc[0][0][c + e] += o[e];
       }
   }
+#pragma unroll
+  for (int i = 0; i < TN; ++i)
+#pragma unroll
+    for (int j = 0; j < TM; ++j) settled(acc[i][j]);
   if constexpr (WK == 1) __syncthreads();  // every wave is through with the stages
   if constexpr (!GROUPED) {
     if (p.splits > 1) {
@@ -744,7 +748,8 @@ nf4_status nf4_probe_mxfp4_plan(int64_t M, int64_t N, int64_t K, int32_t experts
   const Plan best = experts > 0 ? choose<true>(p, 0) : choose<false>(p, room);
   *plan = best.tiling;
   if (best.tiling == kToRows) {
-    *detail = static_cast<int32_t>(row_units(p.pitch));
+    const Rows r = row_plan(p, experts > 0 ? row_tiles<true>(p, 16) : row_tiles<false>(p, 16));
+    *detail = r.split == kRowWaves ? r.units : -r.split;
   } else if (best.tiling < kLargest || experts > 0) {
     *detail = best.splits;
   } else {

@@ -278,6 +278,8 @@ __device__ __forceinline__ void stream_tiles(int units, int64_t tiles, int64_t f
       ++step;
       continue;
     }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) settled(acc[c]);
     if constexpr (SPLIT == 1) {
       join_parts<PARTS>(acc, together, rows);
       if (t < tiles) done(t, acc);

@@ -46,6 +46,14 @@ __device__ __forceinline__ i32x8 four(const i32x4& a) {
   return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
+// Keeps sums where they are computed, by all lanes.  Where only some lanes use them the
+// compiler may move a matrix instruction to these lanes alone, though it reads the operands
+// of all.
+template <class V>
+__device__ __forceinline__ void settled(V& v) {
+  asm volatile("" : "+v"(v));
+}
+
 // Offset of the scales of row `row` (of the group of 128 codes g) from those of row
 // `first`'s tile.
 __device__ __forceinline__ uint32_t scale_from(int64_t first, int64_t row, int64_t steps, int g) {
@@ -54,9 +62,13 @@ __device__ __forceinline__ uint32_t scale_from(int64_t first, int64_t row, int64
 
 constexpr int kRowWaves = 8;  // of the few-row kernel
 
-// The variant of the few-row kernel for rows of `pitch` bytes: units of 64 that a wave
+// The few-row kernel's variant: waves that share a tile's K, units of 64 bytes that a wave
 // holds at a time.
-int64_t row_units(int64_t pitch);
+struct Rows {
+  int split, units;
+};
+// rows: tiles of 16 rows.
+Rows row_plan(const Product& p, int64_t rows);
 
 // Whether `rows` rows (16 at most) of the activations' codes have room beside the kernel.
 bool fits_rows(const Product& p, int64_t rows);
