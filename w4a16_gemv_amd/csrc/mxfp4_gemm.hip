@@ -694,8 +694,17 @@ bool few(const Product& p) {
   return p.M <= 16 || tiles <= 2 * cus;
 }
 
-// Whether it encodes the activations too.
-bool encodes_rows(const Product& p) { return few<false>(p); }
+// Whether it encodes the activations too, which each of its workgroups does again: up to
+// 40960 elements (16 rows at a time) where every compute unit has one workgroup, 28672
+// where it has two.  One launch and two: 8 x 4096 x 4096 6.8 us and 8.1, 16 rows 9.7 and
+// 8.9; 4 x 11008 x 4096 8.8 and 10.1, 8 rows 11.0 and 10.6; 2 x 4096 x 11008 10.1 and 11.5,
+// 4 rows 12.3 and 12.1.
+bool encodes_rows(const Product& p) {
+  if (!few<false>(p)) return false;
+  const int64_t elements = (p.M < 16 ? p.M : 16) * 2 * p.pitch;
+  const int64_t tiles = row_tiles<false>(p, 16) * ((p.N + 15) / 16);
+  return elements <= (tiles <= device_cus() ? 40960 : 28672);
+}
 
 // What a product goes to: the few-row kernel, or tiles as planned.
 constexpr int kToRows = -1;
