@@ -109,8 +109,8 @@ size_t mxfp4_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /*
  * mxfp4_linear -- mxfp4_quantize of the activations and mxfp4_gemm in one call
- * (few rows take one launch).  The order of the sums is that of mxfp4_gemm with
- * the room that is left in the workspace.
+ * (few rows take one launch, whose order of the sums need not be mxfp4_gemm's; it
+ * follows from M, N, K and the room in the workspace alone too).
  *  x, x_dtype    : device, M x K activations, contiguous, natural alignment.
  *  workspace     : DEVICE scratch, 256-byte aligned, any contents (may be NULL
  *                  where mxfp4_linear_workspace_size is 0).  Where that is not 0

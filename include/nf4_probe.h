@@ -60,7 +60,7 @@ nf4_status nf4_probe_int8_plan(int64_t M, int64_t N, int64_t K, int32_t experts,
  * nf4_probe_mxfp4_plan -- the same of the products of 4-bit microscaled floats:
  * plan -1 the few-row kernel (detail: units of 64 bytes of codes to a wave where eight
  * share a row, minus the waves that do where fewer do), 0-5 tiles by size (detail as
- * above).
+ * above).  experts -1 is mxfp4_linear's, which encodes few rows on the way.
  */
 nf4_status nf4_probe_mxfp4_plan(int64_t M, int64_t N, int64_t K, int32_t experts, size_t room,
                                 int32_t* plan, int32_t* detail);

@@ -234,10 +234,10 @@ def test_quantize_flattens_and_strides_are_refused():
 
 DENSE = [(1, 1, 1), (1, 8, 18), (3, 17, 33), (16, 100, 129), (15, 33, 255), (1, 4099, 1501), (1, 8, 4175), (2, 100, 9999),
          (1, 9, 12576), (4, 40, 20000), (16, 65, 12000), (17, 40, 128), (100, 20, 300), (42, 2766, 16), (1, 8, 22885),
-         (80, 2885, 16), (1271, 8, 15833), (1962, 257, 16), (1, 1019, 28214), (2210, 490, 17), (69, 1856, 41721),
-         (1531, 1359, 16), (257, 1619, 34814), (2456, 3478, 1911), (1996, 2597, 2779), (333, 4099, 1501),
-         (4352, 4096, 1500), (5500, 4000, 1650), (4097, 4096, 256), (300, 300, 300), (130, 129, 1000),
-         (3, 16400, 2000), (2, 32800, 1000), (5, 65600, 500)]
+         (3, 627, 20100), (1271, 8, 15833), (1172, 197, 8691), (165, 476, 34494), (2210, 490, 17), (65, 2759, 43069),
+         (1962, 257, 16), (4148, 195, 3334), (5441, 520, 538), (69, 3280, 53757), (3415, 4261, 267), (1996, 2597, 2779),
+         (333, 4099, 1501), (5077, 4142, 515), (1750, 2128, 519), (3722, 4596, 524), (300, 300, 300), (130, 129, 1000),
+         (3, 16400, 2000), (5, 65600, 500)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -256,22 +256,35 @@ def test_gemm(M, N, K):
     assert same(amd.mxfp4_gemm(xt, wt, out_dtype=F32, workspace=none), exactly(x, w, 0.25, F32))
 
 
+LINEAR = [(1, 4096, 4096), (2, 33, 7), (13, 1100, 1024), (16, 40, 9999), (1, 70, 20000), (17, 64, 300), (40, 100, 129),
+          (333, 411, 1501), (700, 900, 160), (1, 40, 9999), (2, 70, 6001), (3, 16400, 2000), (2, 32800, 1000), (5, 65600, 500)]
+
+
 @pytest.mark.parametrize("xdtype", TYPES, ids=str)
-@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (2, 33, 7), (13, 1100, 1024), (16, 40, 9999), (5, 64, 12576),
-                                   (17, 64, 300), (40, 100, 129), (333, 411, 1501), (700, 900, 160)])
+@pytest.mark.parametrize("M,N,K", LINEAR)
 def test_linear(M, N, K, xdtype):
-    """The bits of the two calls that it stands for; a vector gives a vector."""
+    """Against the codes' exact products where no sum can round, and for any
+    activations; a vector gives a vector."""
+    x, _ = random_rows(M + K, M, K, 127, 129 if K < 10000 else 128)
+    w, wt = random_rows(N, N, K, 127, 129 if K < 10000 else 128)
+    room = torch.empty(M * K + 1, dtype=xdtype, device=dev())
     g = torch.Generator(device=dev()).manual_seed(M + K)
-    room = torch.randn(M * K + 1, generator=g, device=dev()).to(xdtype)
-    _, wt = random_rows(N, N, K, 120, 130)
+    noise = torch.randn(M, K, generator=g, device=dev())
+    coded = amd.mxfp4_quantize(noise.to(xdtype)).dequant(out_dtype=F32).double()
+    want = coded @ w.t()
     for shift in (0, 1):
-        x = room[shift:shift + M * K].view(M, K)
+        to = room[shift:shift + M * K].view(M, K)
         for dtype in TYPES:
-            got = amd.mxfp4_linear(x, wt, out_dtype=dtype)
-            assert same(got, amd.mxfp4_gemm(amd.mxfp4_quantize(x), wt, out_dtype=dtype))
+            to.copy_(x)  # (every value of a code fits the types, and its block gets the same values again)
+            whole, y = guarded(M, N, dtype)
+            assert amd.mxfp4_linear(to, wt, y=y) is y
+            assert same(y, exactly(x, w, 0.25, dtype)) and untouched(whole, M * N)
+            to.copy_(noise)
+            got = amd.mxfp4_linear(to, wt, out_dtype=dtype).double()
+            assert ((got - want).abs() <= bound(coded, w, want, K / 64 + 17, dtype)).all()
     if M == 1:
         y = torch.empty(N, dtype=F32, device=dev())
-        assert amd.mxfp4_linear(x[0], wt, y=y) is y and same(y, amd.mxfp4_linear(x[0], wt, out_dtype=F32))
+        assert amd.mxfp4_linear(to[0], wt, y=y) is y and same(y, amd.mxfp4_linear(to[0], wt, out_dtype=F32))
 
 
 def bound(x, w, want, terms, dtype):
@@ -421,9 +434,9 @@ def routing(seed, T, k, E, drop=0.1):
 
 
 GROUPED = [(1, 2, 1, 8, 20), (5, 2, 3, 33, 300), (16, 4, 64, 40, 512), (1, 1, 1, 11, 4989), (1, 3, 1, 8, 11821),
-           (3, 1, 1, 8, 13844), (18, 1, 1, 8, 16), (1687, 3, 1, 33, 17), (208, 3, 50, 163, 19), (1167, 4, 50, 150, 16),
-           (1726, 3, 60, 285, 17), (586, 4, 10, 3044, 1568), (700, 2, 8, 1000, 1100),
-           (20, 2, 64, 400, 1100), (20, 2, 64, 800, 600), (20, 2, 64, 1600, 300)]
+           (18, 1, 1, 8, 16), (1687, 3, 1, 33, 17), (208, 3, 50, 163, 19), (1726, 3, 60, 285, 17), (134, 4, 1, 463, 6331),
+           (596, 4, 1, 393, 2310), (586, 2, 3, 2466, 257), (1937, 3, 14, 981, 769), (586, 4, 10, 3044, 1568),
+           (20, 2, 64, 900, 1100), (20, 2, 64, 1600, 600), (105, 3, 81, 645, 33), (20, 2, 64, 1600, 300)]
 
 
 @pytest.mark.parametrize("T,k,E,N,K", GROUPED)

@@ -215,7 +215,7 @@ def test_plan_arguments(lib):
     a, b = C.c_int32(), C.c_int32()
     ask = lambda M=4, N=8, K=64, E=0, a=C.byref(a), b=C.byref(b): lib.nf4_probe_mxfp4_plan(M, N, K, E, 0, a, b)  # noqa: E731
     assert ask() == 0 and (a.value, b.value) == (-1, 4)
-    for bad in (dict(M=0), dict(N=0), dict(K=-1), dict(E=-1), dict(a=None), dict(b=None)):
+    for bad in (dict(M=0), dict(N=0), dict(K=-1), dict(E=-2), dict(a=None), dict(b=None)):
         assert ask(**bad) == EINVAL
     for large in (dict(M=1 << 31), dict(N=1 << 31), dict(K=(1 << 20) + 1), dict(E=1025)):
         assert ask(**large) == 2
@@ -227,10 +227,13 @@ def _variant(plan, detail):
 
 def test_the_gpu_tests_reach_every_variant(lib):
     """A rule that is measured anew may send their sizes elsewhere; then they need others."""
-    units = {(-1, u) for u in (4, 8, 12, 22, -4, -2, -1)}
+    reached = {_variant(*on_gpu.plan(M, N, K, -1)) for M, N, K in on_gpu.LINEAR}
+    want = {(-1, u) for u in (4, 8, 12, 22, -4, -2, -1)}
+    assert reached >= want, want - reached
     reached = {_variant(*on_gpu.plan(M, N, K)) for M, N, K in on_gpu.DENSE}
-    want = units | {(i, s) for i in range(5) for s in ("whole K", "split K")} | {(5, shares) for shares in (1, 2, 3, 5)}
+    want = {(-1, 4)} | {(i, s) for i in range(5) for s in ("whole K", "split K")}
+    want |= {(5, shares) for shares in (1, 2, 3, 4, 5)}
     assert reached >= want, want - reached
     reached = {_variant(*on_gpu.plan(T * k, N, K, E)) for T, k, E, N, K in on_gpu.GROUPED}
-    want = units | {(i, "whole K") for i in range(5)} | {(5, 1)}
+    want = {(-1, u) for u in (-4, -2, -1)} | {(i, "whole K") for i in (0, 2, 4)} | {(5, 1)}
     assert reached >= want, want - reached

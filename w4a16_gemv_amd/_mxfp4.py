@@ -221,7 +221,8 @@ def mxfp4_linear(x: torch.Tensor, w: Mxfp4Tensor, y: torch.Tensor | None = None,
                  out_dtype: torch.dtype = torch.bfloat16,
                  workspace: torch.Tensor | None = None) -> torch.Tensor:
     """mxfp4_gemm(mxfp4_quantize(x), w) in one call: x is [M][K] (or [K], then y
-    is [N]) in bf16, fp16 or fp32.
+    is [N]) in bf16, fp16 or fp32.  The codes are the same; the order of the fp32
+    sums may be another.
 
     workspace: a uint8 tensor from mxfp4_linear_workspace, or None for one from
     torch's allocator."""

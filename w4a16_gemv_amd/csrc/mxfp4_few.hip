@@ -34,10 +34,10 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 
 // ---------------------------------------------------------------------------
 // Up to 16 tokens, whose codes and scales a workgroup keeps in LDS.  It goes through its
-// channels in tiles of 16, 8 / SPLIT at a time, each with SPLIT waves that share K: the weights go from memory
-// through registers to the matrix cores (v_mfma_scale_f32_16x16x128_f8f6f4: lane i +
-// 16 g holds the codes 32 g .. + 31 of row i of A, B likewise with i the column, and
-// D[4 g .. + 3][i]), each byte read once, the next tile's asked for as soon as the
+// channels in tiles of 16, 8 / SPLIT at a time, each with SPLIT waves that share K: the
+// weights go from memory through registers to the matrix cores
+// (v_mfma_scale_f32_16x16x128_f8f6f4: lane i + 16 g holds the codes 32 g .. + 31 of row i
+// of A, B likewise with i the column, and D[4 g .. + 3][i]), each byte read once, the next tile's asked for as soon as the
 // registers are free.  The waves' sums meet in LDS and are added in the waves' order.  More
 // rows than 16 go to more workgroups.
 //
@@ -206,6 +206,7 @@ nf4_status launch_typed(const Product& p, const void* x, int64_t K, int32_t y_dt
   const int64_t most = 2 * device_cus(), share = (most + rows - 1) / rows;
   const dim3 grid(static_cast<uint32_t>(groups < share ? groups : share), static_cast<uint32_t>(rows));
   const uint32_t lds = static_cast<uint32_t>(lds_bytes(p.pitch, p.M < 16 ? p.M : 16));
+  bool known = true;
   with_dtype(y_dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     auto run = [&](auto split, auto units) {
@@ -213,16 +214,23 @@ nf4_status launch_typed(const Product& p, const void* x, int64_t K, int32_t y_dt
                          dim3(kRowThreads), lds, st, p, x, K);
     };
     using std::integral_constant;
-    switch (r.split == kRowWaves ? r.units : -r.split) {
-      case 4: run(integral_constant<int, 8>{}, integral_constant<int, 4>{}); break;
-      case 8: run(integral_constant<int, 8>{}, integral_constant<int, 8>{}); break;
-      case 12: run(integral_constant<int, 8>{}, integral_constant<int, 12>{}); break;
-      case 22: run(integral_constant<int, 8>{}, integral_constant<int, 22>{}); break;
-      case -4: run(integral_constant<int, 4>{}, integral_constant<int, 4>{}); break;
-      case -2: run(integral_constant<int, 2>{}, integral_constant<int, 4>{}); break;
-      default: run(integral_constant<int, 1>{}, integral_constant<int, 4>{}); break;
+    const int variant = r.split == kRowWaves ? r.units : -r.split;
+    if constexpr (!GROUPED) {  // experts' rows take four waves or fewer
+      if (variant == 4) return run(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+      if constexpr (XT != kCodes) {  // codes come in short rows and few tiles
+        if (variant == 8) return run(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+        if (variant == 12) return run(integral_constant<int, 8>{}, integral_constant<int, 12>{});
+        if (variant == 22) return run(integral_constant<int, 8>{}, integral_constant<int, 22>{});
+      }
     }
+    if constexpr (GROUPED || XT != kCodes) {
+      if (variant == -4) return run(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+      if (variant == -2) return run(integral_constant<int, 2>{}, integral_constant<int, 4>{});
+      if (variant == -1) return run(integral_constant<int, 1>{}, integral_constant<int, 4>{});
+    }
+    known = false;
   });
+  if (!known) return NF4_EUNSUPPORTED;
   return launch_status();
 }
 

@@ -614,28 +614,44 @@ nf4_status launch_stream(const Product& p, int32_t y_dtype, hipStream_t st) {
   return launch_status();
 }
 
-// The tiled kernels, and what their steps of 128 bytes of K take (us): where few
-// compute units have a tile, and for each of its tiles where all have one or more (the
-// memory behind them is busier then).
+// The tiled kernels, and what their steps of 128 bytes of K take (us): with a tile on
+// few compute units, and for each of a compute unit's tiles where all have one or more (the
+// memory behind them is busier then).  The figures are fitted to 1 to 2048 rows of
+// 4096 x 4096, 11008 x 4096, 4096 x 11008, 2048 x 2048 and 1024 x 11008 in every tiling:
+// what they pick is within 5% of the best of these.  Largest tiles load the least per
+// product, but leave compute units idle and take the longest for themselves: 512 x
+// 4096 x 4096 takes 23.6 / 20.7 / 10.7 / 10.6 / 13.2 / 13.1 us from the smallest tiles to
+// the largest, 64 x 4096 x 4096 6.1 / 6.8 / 6.9 / 9.1 / 12.3 / 12.1, 1024 x 11008 x 4096
+// - / - / 44 / 49 / 40 / 32.
 struct Tiling {
-  int BM, BN;        // tokens, channels
-  float alone, each; // us a step
-  float fixed;       // us a turn that no step hides
+  int BM, BN;         // tokens, channels
+  double alone, each; // us a step
+  double fixed;       // us a turn that no step hides
 };
-constexpr Tiling kTilings[] = {{32, 32, 0.16f, 0.125f, 0.0f}, {64, 32, 0.215f, 0.25f, 0.0f},
-                               {64, 64, 0.28f, 0.255f, 0.0f}, {128, 64, 0.35f, 0.47f, 0.0f},
-                               {128, 128, 0.55f, 0.69f, 0.0f}, {256, 256, 1.05f, 1.6f, 4.0f}};
+constexpr Tiling kTilings[] = {{32, 32, 0.086, 0.12, 0.8},  {64, 32, 0.09, 0.158, 1.3},
+                               {64, 64, 0.152, 0.21, 0.63}, {128, 64, 0.23, 0.376, 1.2},
+                               {128, 128, 0.376, 0.61, 2.2}, {256, 256, 1.49, 1.49, 11.4}};
 constexpr int kLargest = 5;
-constexpr float kLaunchUs = 3.0f, kJoinUs = 4.5f, kSumUs = 8.0f / 3e6f;  // a sum there and back
+// A last turn of the largest in halves and in quarters.
+constexpr double kHalfStep = 1.03, kHalfFixed = 4.5, kQuarterStep = 0.41, kQuarterFixed = 2.3;
+constexpr double kLaunchUs = 3.2, kJoinUs = 4.5, kSumUs = 8.0 / 3e6;  // a sum there and back
+// Rows sorted by expert: finding a tile, a stream of weights that counts, three launches.
+constexpr double kFindUs = 1.3, kLonger = 1.45, kLaunchesUs = 3.4;
 constexpr int kMaxSplits = 16;
 
 struct Plan {
   int tiling, splits;
 };
 
-// The tiling with the least time by the figures above, with K split over
-// workgroups where that leaves compute units without a tile and the workspace has
-// room for the sums, unless writing and reading the sums costs as much.
+// The tiling with the least time by the figures above, with K split over workgroups
+// where that leaves compute units without a tile and the workspace has room for the sums,
+// unless writing and reading the sums costs as much (17 x 1024 x 11008: 8.3 us in one
+// piece, 8.1 in four; 128 x 4096 x 11008 11.8 and 13.7 in two).  The model orders the
+// tilings; it is no time of long weights from memory, which it does not know.
+//
+// Rows sorted by expert: every expert with rows ends in a tile that is half full.  Tiles
+// of 64 x 32 and 128 x 64 were the best nowhere (8 to 128 experts with 16 to 8192
+// rows), and those of 32 x 32 only where a compute unit has one at most.
 template <bool GROUPED>
 Plan plan(const Product& p, size_t room) {
   const int64_t cus = device_cus();
@@ -650,18 +666,30 @@ Plan plan(const Product& p, size_t room) {
                                                   : static_cast<double>(p.M < p.experts ? p.M : p.experts);
     const double tiles = rows * static_cast<double>((p.N + t.BN - 1) / t.BN);
     if (i < kLargest && tile_groups<GROUPED>(p, t.BM, t.BN, 256) == 0) continue;
-    if (GROUPED && t.BN == 32 && tiles > cus) continue;
+    if (GROUPED && (i == 1 || i == 3 || (i == 0 && tiles > cus))) continue;
     const int most = GROUPED || i == kLargest ? 1 : kMaxSplits;
     for (int splits = 1; splits <= most; ++splits) {
       if (splits > 1 && (tiles * splits > cus || p.M * p.sums_pitch * 4 * splits > static_cast<int64_t>(room) ||
                          steps < 4 * splits))
         break;
       const double full = tiles * splits / cus, part = full - std::floor(full);
-      double turns = std::ceil(full);
-      if (i == kLargest && part > 0 && part <= 0.5) turns -= full > 1 && part <= 0.25 ? 0.6 : 0.3;  // in pieces
-      const double more = t.each > t.alone ? t.each - t.alone : 0.0;
-      const double step = full > 1 || turns < 1 ? turns * t.each : t.alone + more * full;
-      const double us = kLaunchUs + turns * t.fixed + std::ceil(steps / splits) * step + (splits > 1 ? kJoinUs + p.M * p.sums_pitch * splits * kSumUs : 0.0);
+      double us = kLaunchUs;
+      if (i == kLargest) {
+        us += std::floor(full) * (t.fixed + steps * t.each) + (GROUPED ? kLaunchesUs : 0.0);
+        if (part > 0.5) {  // more of the memory's rate for each
+          const double s = 2 * part - 1;
+          us += kHalfFixed + (t.fixed - kHalfFixed) * s + steps * (kHalfStep + (t.each - kHalfStep) * s);
+        } else if (part > 0.25) {
+          us += kHalfFixed + steps * kHalfStep;
+        } else if (part > 0) {
+          us += kQuarterFixed + steps * kQuarterStep;
+        }
+      } else {
+        const double turns = std::ceil(full), step = full > 1 ? turns * t.each : t.alone + (t.each - t.alone) * full;
+        us += turns * (t.fixed + (GROUPED ? kFindUs : 0.0)) +
+              std::ceil(steps / splits) * step * (GROUPED ? kLonger : 1.0);
+      }
+      if (splits > 1) us += kJoinUs + p.M * p.sums_pitch * splits * kSumUs;
       if (us < least * (splits > 1 ? 0.85 : 1.0)) {
         least = us;
         best = {i, splits};
@@ -683,27 +711,37 @@ Product dense(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uin
 }
 
 // Whether the row kernel takes the product: it reads weights once for every 16 rows.
+// Its start is shorter than a tile's, so it does better where every compute unit has one
+// tile of 16 x 16 at most and rows are not long (1 x 1024 x 4096: 4.0 us and 5.3 in tiles,
+// 4 x 4096 x 4096 5.6 and 5.8, 32 x 2048 x 2048 4.5 and 4.7; 4 x 4096 x 11008 9.4 and 8.4,
+// 4 x 11008 x 4096 7.7 and 7.0).  By expert: where the weights' stream counts and a tile
+// of 64 x 64 has few steps (64 experts of 1024 x 2048 with 64 to 512 rows: 12.9-17.2 us and
+// 14.9-17.8; of 2048 x 1024 with 1024 rows 22.5 and 24.6; with 16 rows of 1024 x 2048 8.4
+// and 7.5, 16 experts of 2048 x 4096 with 64 rows 15.5 and 14.8).
+constexpr int64_t kShortPitch = 2048, kShortestPitch = 512;
+
 template <bool GROUPED>
 bool few(const Product& p) {
   if (!fits_rows(p, p.M < 16 ? p.M : 16) || row_tiles<GROUPED>(p, 16) > 65535) return false;
-  const int64_t cus = device_cus(), tiles = row_tiles<GROUPED>(p, 16) * ((p.N + 15) / 16);
+  const int64_t cus = device_cus();
   if (GROUPED) {
-    const int64_t rows = p.M / p.experts;
-    return rows <= 4 || (rows <= 10 && p.experts * ((p.N + 63) / 64) <= cus);
+    const int64_t most = p.M < p.experts ? p.M : p.experts;
+    return p.pitch <= kShortPitch / 2 && most * ((p.N + 15) / 16) > 8 * cus &&
+           p.M <= (p.pitch <= kShortestPitch ? 16 : 8) * int64_t(p.experts);
   }
-  return p.M <= 16 || tiles <= 2 * cus;
+  return p.pitch <= kShortPitch && row_tiles<false>(p, 16) * ((p.N + 15) / 16) <= cus;
 }
 
-// Whether it encodes the activations too, which each of its workgroups does again: up to
-// 40960 elements (16 rows at a time) where every compute unit has one workgroup, 28672
-// where it has two.  One launch and two: 8 x 4096 x 4096 6.8 us and 8.1, 16 rows 9.7 and
-// 8.9; 4 x 11008 x 4096 8.8 and 10.1, 8 rows 11.0 and 10.6; 2 x 4096 x 11008 10.1 and 11.5,
-// 4 rows 12.3 and 12.1.
+// Whether it takes the activations as they are and encodes them too, which each of its
+// workgroups does again: up to 32768 elements (16 rows at a time) where every compute unit
+// has one tile, 16384 where it has more.  One launch and two: 8 x 4096 x 4096 6.8 us and
+// 8.1, 16 rows 9.7 and 8.3; 4 x 11008 x 4096 8.8 and 9.5, 8 rows 11.0 and 9.5; 2 x 4096 x
+// 11008 10.1 and 10.9, 4 rows 12.3 and 10.9; 1 x 44032 x 4096 18.5 and 21.5.
 bool encodes_rows(const Product& p) {
-  if (!few<false>(p)) return false;
+  if (!fits_rows(p, p.M < 16 ? p.M : 16) || row_tiles<false>(p, 16) > 65535) return false;
   const int64_t elements = (p.M < 16 ? p.M : 16) * 2 * p.pitch;
-  const int64_t tiles = row_tiles<false>(p, 16) * ((p.N + 15) / 16);
-  return elements <= (tiles <= device_cus() ? 40960 : 28672);
+  const bool one = row_tiles<false>(p, 16) * ((p.N + 15) / 16) <= device_cus();
+  return elements <= (one ? 32768 : 16384) && (p.M <= 16 || one);
 }
 
 // What a product goes to: the few-row kernel, or tiles as planned.
@@ -723,9 +761,13 @@ nf4_status launch(Product p, int32_t y_dtype, void* workspace, size_t room, hipS
   p.sums = static_cast<float*>(workspace);
   switch (plan_.tiling) {
     case 0: return launch_stream<GROUPED, 1, 1, 4, 1, 1, 8>(p, y_dtype, st);
-    case 1: return launch_stream<GROUPED, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
+    case 1:
+      if constexpr (!GROUPED) return launch_stream<false, 2, 1, 2, 1, 1, 8>(p, y_dtype, st);
+      return NF4_EUNSUPPORTED;
     case 2: return launch_stream<GROUPED, 2, 2, 1, 1, 1, 4>(p, y_dtype, st);
-    case 3: return launch_stream<GROUPED, 2, 2, 1, 2, 1, 4>(p, y_dtype, st);
+    case 3:
+      if constexpr (!GROUPED) return launch_stream<false, 2, 2, 1, 2, 1, 4>(p, y_dtype, st);
+      return NF4_EUNSUPPORTED;
     case 4: return launch_stream<GROUPED, 2, 2, 1, 2, 2, 4>(p, y_dtype, st);
     default: return launch_tiles<GROUPED>(p, y_dtype, st);
   }
@@ -750,11 +792,13 @@ extern "C" {
 
 nf4_status nf4_probe_mxfp4_plan(int64_t M, int64_t N, int64_t K, int32_t experts, size_t room, int32_t* plan,
                                 int32_t* detail) {
-  if (!plan || !detail || M < 1 || N < 1 || K < 0 || experts < 0) return NF4_EINVAL;
+  if (!plan || !detail || M < 1 || N < 1 || K < 0 || experts < -1) return NF4_EINVAL;
   if (M > kMaxDim || N > kMaxDim || K > kMaxK || experts > kMaxExperts) return NF4_EUNSUPPORTED;
   Product p = dense(nullptr, nullptr, nullptr, nullptr, nullptr, M, N, K);
   if (experts > 0) p.experts = experts;
-  const Plan best = experts > 0 ? choose<true>(p, 0) : choose<false>(p, room);
+  const Plan best = experts < 0 && encodes_rows(p) ? Plan{kToRows, 1}
+                    : experts > 0                  ? choose<true>(p, 0)
+                                                   : choose<false>(p, room);
   *plan = best.tiling;
   if (best.tiling == kToRows) {
     const Rows r = row_plan(p, experts > 0 ? row_tiles<true>(p, 16) : row_tiles<false>(p, 16));
