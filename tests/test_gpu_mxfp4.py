@@ -365,7 +365,8 @@ def test_gemm_weights_past_4_gib(M):
 @pytest.mark.parametrize("xdtype", TYPES, ids=str)
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 4096, 4096), (2, 33, 31), (3, 100, 127), (4, 17, 1501), (5, 40, 11008),
                                    (7, 64, 4097), (8, 48, 129), (9, 20, 640), (16, 300, 2000), (16, 9000, 256), (1, 16, 70001),
-                                   (3, 33000, 500), (5, 33000, 1000), (2, 33000, 2000), (16, 300, 9000)])
+                                   (3, 33000, 500), (5, 33000, 1000), (2, 33000, 2000), (16, 300, 9000),
+                                   (4, 60, 15001), (7, 4500, 8300), (16, 9000, 4100), (3, 4200, 20003)])
 def test_gemv(M, N, K, xdtype):
     """Exact for activations of few bits; within the bound for any."""
     g = torch.Generator(device=dev()).manual_seed(M + K)
@@ -380,7 +381,8 @@ def test_gemv(M, N, K, xdtype):
     x = torch.randn(M, K, generator=g, device=dev()).to(xdtype)
     want = x.double() @ w.t()
     got = amd.mxfp4_gemv(x, wt, out_dtype=F32).double()
-    # for every 32 of K an addition to each of three parts at most, eight waves' sums
+    # for every 32 of K an addition to each of three parts at most, eight waves' sums (or 16,
+    # of a sixteenth of K each, with K of thousands)
     assert ((got - want).abs() <= bound(x.double(), w, want, 3 * K / 32 + 9, F32)).all()
 
 

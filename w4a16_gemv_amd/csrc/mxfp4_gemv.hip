@@ -50,35 +50,65 @@ __device__ __forceinline__ uint32_t upper_halves(float even, float odd) {
   return __builtin_bit_cast(uint32_t, even) >> 16 | (__builtin_bit_cast(uint32_t, odd) & 0xFFFF0000u);
 }
 
-// Eight activations to the parts' eight bf16 numbers each.
+// Eight activations to the parts' eight bf16 numbers each.  fp16: without the last three
+// bits, and these, both exact in fp16 and in bf16.  An infinity less itself is a NaN: what
+// is not finite shows in the sum of what is left of the eight, and is seen to apart (tests
+// of every element took as long as the rest: 7 x 4096 x 11008 fp16 16.9 us).
 template <int DT>
 __device__ __forceinline__ void split_piece(const Piece<DT>& p, u32x4 (&out)[parts_of(DT)]) {
   if constexpr (DT == INT8_BF16) {
     out[0] = p.v[0];
   } else if constexpr (DT == INT8_FP16) {
-    // without the last three bits, and these, both exact in fp16 and in bf16; an infinity
-    // is its own first part
+    f16x2 left = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t w = p.v[0][i], high = w & 0xFFF8FFF8u;
       const f16x2 h = __builtin_bit_cast(f16x2, high), low = __builtin_bit_cast(f16x2, w) - h;
-      const float h0 = static_cast<float>(h[0]), h1 = static_cast<float>(h[1]);
-      const float l0 = static_cast<float>(low[0]), l1 = static_cast<float>(low[1]);
-      out[0][i] = upper_halves(h0, h1);
-      out[1][i] = upper_halves(fabsf(h0) < __builtin_inff() ? l0 : 0.0f, fabsf(h1) < __builtin_inff() ? l1 : 0.0f);
-      // (a NaN whose bits are among the last three)
-      if (w != high) {
-        out[0][i] |= ((w & 0x7FFF) > 0x7C00 ? 0x0040u : 0u) | ((w >> 16 & 0x7FFF) > 0x7C00 ? 0x00400000u : 0u);
+      left += low;
+      out[0][i] = upper_halves(static_cast<float>(h[0]), static_cast<float>(h[1]));
+      out[1][i] = upper_halves(static_cast<float>(low[0]), static_cast<float>(low[1]));
+    }
+    const _Float16 sum = left[0] + left[1];
+    if (sum != sum) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = p.v[0][i];
+        if ((w & 0x7C00u) == 0x7C00u) {  // a NaN may have its bits among the last three
+          out[0][i] |= (w & 0x7FFFu) > 0x7C00u ? 0x0040u : 0u;
+          out[1][i] &= 0xFFFF0000u;
+        }
+        if ((w & 0x7C000000u) == 0x7C000000u) {
+          out[0][i] |= (w & 0x7FFF0000u) > 0x7C000000u ? 0x00400000u : 0u;
+          out[1][i] &= 0x0000FFFFu;
+        }
       }
     }
   } else {
+    float left = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
-      float a[3], b[3];
-      split(element<DT>(p, i), a);
-      split(element<DT>(p, i + 1), b);
+      float part[2][3];
 #pragma unroll
-      for (int k = 0; k < parts_of(DT); ++k) out[k][i / 2] = upper_halves(a[k], b[k]);
+      for (int k = 0; k < 2; ++k) {
+        const float f = element<DT>(p, i + k);
+        part[k][0] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, f) & 0xFFFF0000u);
+        const float rest = f - part[k][0];
+        part[k][1] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, rest) & 0xFFFF0000u);
+        part[k][2] = rest - part[k][1];
+        left += part[k][2];
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) out[q][i / 2] = upper_halves(part[0][q], part[1][q]);
+    }
+    if (left != left) {
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float a[3], b[3];
+        split(element<DT>(p, i), a);
+        split(element<DT>(p, i + 1), b);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) out[q][i / 2] = upper_halves(a[q], b[q]);
+      }
     }
   }
 }
@@ -145,10 +175,11 @@ __device__ __forceinline__ void operands(const Loaded& l, bf16x8 (&a)[4]) {
 __device__ __host__ __forceinline__ int lds_row(int width) { return 2 * width + 16; }
 
 // Elements first .. first + width - 1 of rows row(0), row(1), ... of K each (zeros from K
-// on), by all threads of the workgroup, several loads of each in flight.
-template <int XT, class Row>
+// on), by all threads of the workgroup, several loads of each in flight (as many as the
+// registers beside CT tiles' weights leave).
+template <int XT, int CT, class Row>
 __device__ __forceinline__ void stage_rows(uint8_t* lds, int rows, int64_t first, int width, int64_t K, Row&& row) {
-  constexpr int kParts = parts_of(XT), kAtOnce = XT == INT8_FP32 ? 4 : 8;
+  constexpr int kParts = parts_of(XT), kAtOnce = XT == INT8_FP32 ? (CT > 1 ? 2 : 3) : XT == INT8_FP16 ? (CT > 1 ? 4 : 6) : (CT > 1 ? 4 : 8);
   const int pieces = width / 8, all = rows * pieces, pitch = lds_row(width);
   for (int i0 = threadIdx.x; i0 < all; i0 += kAtOnce * kThreads) {
     Piece<XT> v[kAtOnce];
@@ -334,7 +365,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_gemv_kernel(Gemv p) {
       [&](int64_t t) { return Tiles<1>{{channels(p.wq, p.ws, 16 * t, p.N - 16 * t, p.pitch, p.steps)}}; },
       [&](int unit) {
         __syncthreads();  // every wave is through with the rows before
-        stage_rows<XT>(s_x, rows, int64_t(kUnit) * unit, p.width, p.K,
+        stage_rows<XT, 1>(s_x, rows, int64_t(kUnit) * unit, p.width, p.K,
                        [&](int r) { return static_cast<const char*>(p.x) + r * p.K * dtype_bytes(XT); });
         __syncthreads();
       },
@@ -345,6 +376,138 @@ __global__ __launch_bounds__(kThreads, 4) void mx_gemv_kernel(Gemv p) {
         const float f[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
         store_four<DT>(p.y, (lane & 15) * p.N + n, left, f);
       });
+}
+
+// A wave's piece of LDS: rows of a unit at a pitch of 272 bytes (so that a chunk of 16
+// rows lies in different banks), the parts one after the other.
+constexpr int kLdsRow = 2 * kUnit + 16;
+
+// Rows that do not fit LDS as a whole: a workgroup goes through its tiles of 16 channels with
+// K shared by its waves, two units each in turn, and every wave brings the rows of its units
+// itself, through registers and a piece of LDS of its own: no wave waits for another's rows
+// (in LDS a stretch at a time, between barriers, 16 x 11008 x 4096 bf16 took 17.2 us and 7
+// x 4096 x 11008 fp16 16.6; here 14.4 and 13.7, of which half is splitting the rows again in
+// every workgroup).  Rows that do fit are split once for all of a workgroup's tiles: 8
+// x 11008 x 4096 bf16 9.1 us and here 12.2.  RU: loads of a lane for a unit's rows (four
+// rows each).
+template <int XT, int RU>
+constexpr int wide_waves() {
+  return RU * (XT == INT8_FP32 ? 2 : 1) > 2 ? 8 : 16;
+}
+
+template <int XT, int DT, int RU>
+__global__ __launch_bounds__((64 * wide_waves<XT, RU>()), (wide_waves<XT, RU>() / 4)) void mx_gemv_wide_kernel(Gemv p) {
+  constexpr int kParts = parts_of(XT), kRows = 4 * RU, kWide = wide_waves<XT, RU>(), kAhead = 2;
+  constexpr bool kTogether = kParts * kRows <= 16;  // a row's parts as columns of one product
+  __shared__ __attribute__((aligned(16))) uint8_t s_x[kWide][kParts * kRows * kLdsRow];
+  __shared__ f32x4 s_sum[2][kWide][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int rows = static_cast<int>(p.M), units = static_cast<int>(p.pitch / 64), pairs = (units + 1) / 2;
+  const int each = (pairs + kWide - 1) / kWide;  // pairs of a wave in a tile, some past the row
+  const int64_t tiles = (p.N + 15) / 16;
+  const int turns = static_cast<int>((tiles - blockIdx.x + gridDim.x - 1) / gridDim.x), all = turns * each;
+  const char* row[RU];
+#pragma unroll
+  for (int j = 0; j < RU; ++j)
+    row[j] = static_cast<const char*>(p.x) + min(4 * j + (lane >> 4), rows - 1) * p.K * dtype_bytes(XT);
+  auto tile = [&](int64_t t) {
+    const int64_t at = min(t, tiles - 1);
+    return channels(p.wq, p.ws, 16 * at, t < tiles ? p.N - 16 * at : 0, p.pitch, p.steps);
+  };
+  Loaded w[kAhead][2];
+  Piece<XT> x[kAhead][2][RU];
+  int64_t t = blockIdx.x, next_t = t;
+  int step = 0, next_step = 0, turn = 0;
+  Channels next = tile(t);
+  auto load = [&](int d) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int unit = 2 * (wave + kWide * next_step) + i;
+      const bool in = next_t < tiles && unit < units;
+      w[d][i] = load_unit(next, unit, in);
+      const int64_t at = kUnit * unit + 8 * (lane & 15);
+#pragma unroll
+      for (int j = 0; j < RU; ++j) {
+        x[d][i][j] = Piece<XT>{};
+        if (in && 4 * j < rows && at < p.K) x[d][i][j] = load_piece<XT>(row[j], at, p.K);
+      }
+    }
+    if (++next_step == each) {
+      next_step = 0;
+      next_t += gridDim.x;
+      next = tile(next_t);
+    }
+  };
+  f32x4 acc = {};
+  auto take = [&](int d) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (2 * (wave + kWide * step) + i >= units) break;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int j = 0; j < RU; ++j) {
+        if (4 * j >= rows) break;
+        u32x4 part[kParts];
+        split_piece<XT>(x[d][i][j], part);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k)
+          *reinterpret_cast<u32x4*>(s_x[wave] + (k * kRows + 4 * j + (lane >> 4)) * kLdsRow + (lane & 15) * 16) = part[k];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      bf16x8 a[4];
+      operands(w[d][i], a);
+      constexpr int kColumns = kTogether ? kParts * kRows : kRows;
+      const uint8_t* h = s_x[wave] + min(lane & 15, kColumns - 1) * kLdsRow + 64 * (lane >> 4);
+#pragma unroll
+      for (int k = 0; k < (kTogether ? 1 : kParts); ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a[e], *reinterpret_cast<const bf16x8*>(h + k * kRows * kLdsRow + 16 * e), acc, 0, 0, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto advance = [&] {
+    if (++step < each) return;
+    settled(acc);
+    s_sum[turn & 1][wave][lane] = acc;
+    acc = f32x4{};
+    __syncthreads();
+    // one of the waves a turn adds up, in the waves' order; its buffer is written again two
+    // turns later, after a barrier that this wave reaches when it is through
+    if (wave == turn % kWide) {
+      f32x4 sum[1] = {s_sum[turn & 1][0][lane]};
+#pragma unroll 3
+      for (int v = 1; v < kWide; ++v) sum[0] += s_sum[turn & 1][v][lane];
+      join_parts<kParts>(sum, kTogether, kRows);
+      const int64_t n = 16 * t + 4 * (lane >> 4);
+      const int left = static_cast<int>(min(p.N - n, int64_t(4)));
+      const float f[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+      if ((lane & 15) < rows && left > 0) store_four<DT>(p.y, (lane & 15) * p.N + n, left, f);
+    }
+    step = 0;
+    t += gridDim.x;
+    ++turn;
+  };
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) load(d);
+  // (the last ones apart: with a way out in the middle of the loop the compiler has each
+  // turn of it wait for all loads)
+  int i = 0;
+  for (; i + kAhead - 1 < all; i += kAhead) {
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d) {
+      take(d);
+      load(d);
+      advance();
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kAhead - 1; ++d)
+    if (i + d < all) {
+      take(d);
+      advance();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -515,7 +678,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
             }
             s_weight[threadIdx.x] = weight;
           }
-          stage_rows<DT>(s_x, rows, int64_t(kUnit) * unit, width, p.H, [&](int r) {
+          stage_rows<DT, CT>(s_x, rows, int64_t(kUnit) * unit, width, p.H, [&](int r) {
             return static_cast<const char*>(p.x) + s_token[t0 + r] * p.H * dtype_bytes(DT);
           });
           __syncthreads();
@@ -550,9 +713,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
   }
 }
 
-// A wave's piece of LDS in down: rows of a unit at a pitch of 272 bytes (so that a chunk
-// of 16 rows lies in different banks), the parts one after the other.
-constexpr int kLdsRow = 2 * kUnit + 16;
+// A wave's piece of LDS in down.
 template <int DT, int RU>
 constexpr int wave_lds() {
   return h_parts(DT) * 4 * RU * kLdsRow;
@@ -568,8 +729,9 @@ struct Segment {
 // WAVES: of a workgroup; RU: loads of a lane for a unit's rows (four rows each); TT: tiles
 // of 16 tokens.
 template <int DT, int WAVES, int RU, int TT>
-__global__ __launch_bounds__(64 * WAVES, RU == 1 ? 4 : 2) void mx_down_kernel(Mlp p) {
-  constexpr int kParts = h_parts(DT), kRows = 4 * RU, kAhead = 2;  // pairs of units in flight
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
+  constexpr int kParts = h_parts(DT), kRows = 4 * RU;
+  constexpr int kAhead = kParts * RU > 8 ? 1 : 2;  // pairs of units in flight, as registers allow
   constexpr int kSumBytes = WAVES * TT * 64 * 16, kHBytes = WAVES * wave_lds<DT, RU>();
   __shared__ __attribute__((aligned(16))) uint8_t s_h[kHBytes > kSumBytes ? kHBytes : kSumBytes];
   __shared__ Routing s_routing;
@@ -790,6 +952,25 @@ nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const u
   Gemv p = {x, wq, ws, y, M, N, K, pitch_of(K), steps_of(K), 0};
   const Held held = hold(units, M * parts_of(x_dtype), tiles);
   p.width = held.width;
+  if (held.width / kUnit < units) {  // not whole rows
+    const dim3 wide(static_cast<uint32_t>(tiles < device_cus() ? tiles : device_cus()));
+    with_dtype(x_dtype, [&](auto a) {
+      with_dtype(y_dtype, [&](auto d) {
+        auto run = [&](auto ru) {
+          constexpr int XT = decltype(a)::value, RU = decltype(ru)::value;
+          hipLaunchKernelGGL((mx_gemv_wide_kernel<XT, decltype(d)::value, RU>), wide, dim3(64 * wide_waves<XT, RU>()), 0,
+                             reinterpret_cast<hipStream_t>(stream), p);
+        };
+        if (M <= 4)
+          run(std::integral_constant<int, 1>{});
+        else if (M <= 8)
+          run(std::integral_constant<int, 2>{});
+        else
+          run(std::integral_constant<int, 4>{});
+      });
+    });
+    return launch_status();
+  }
   const int64_t most = (held.two ? 2 : 1) * device_cus();
   const dim3 grid(static_cast<uint32_t>(held.groups < most ? held.groups : most));
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -864,7 +1045,7 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
     if (four && T <= 16)
       hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1>), grid, dim3(1024), 0, st, p);
     else if (four)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 4>), grid, dim3(1024), 0, st, p);
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 1, 4>), grid, dim3(512), 0, st, p);
     else if (T <= 16)
       hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1>), grid, dim3(512), 0, st, p);
     else
