@@ -400,9 +400,9 @@ def test_gemv_takes_every_bit_of_an_activation(xdtype):
 
 
 @pytest.mark.parametrize("xdtype", TYPES, ids=str)
-def test_gemv_not_finite(xdtype):
+@pytest.mark.parametrize("M,N,K", [(9, 40, 300), (7, 40, 9000), (16, 40, 9000)])
+def test_gemv_not_finite(M, N, K, xdtype):
     """Infinities and NaN reach the outputs of their row alone."""
-    M, N, K = 9, 40, 300
     w, wt = random_rows(1, N, K, 127, 128)
     x = torch.randint(-8, 9, (M, K), device=dev()).to(xdtype)
     x[2, 7], x[4, 299], x[5, 0], x[5, 1] = float("inf"), float("nan"), float("-inf"), torch.finfo(xdtype).max

@@ -58,6 +58,14 @@ NO_SPILL = (
     "::dot_kernel<0, 0, 1, ",
     "quantize_rows_kernel<0, ",
     "combine_grad_kernel<0, ",
+    "mx_tile_kernel<0, ",
+    "mx_stream_kernel<0, ",
+    "mx_row_kernel<0, 0, ",
+    "mx_row_kernel<3, 0, ",
+    "mx_gemv_kernel<0, 0, ",
+    "mx_gemv_wide_kernel<",
+    "mx_up_kernel<0, ",
+    "mx_down_kernel<",
 )
 RESOURCES = os.path.join(PKG, "kernel_resources.txt")
 REMARKS = "-Rpass-analysis=kernel-resource-usage"

@@ -129,19 +129,21 @@ constexpr int kTileThreads = 256;
 constexpr int kDepth = 128;     // bytes of K per step
 constexpr int kScaleDepth = 8;  // bytes of a row's scales per step
 
+constexpr int kOutBytes = 4 * 32 * 128;  // LDS that the outputs go through
+// A buffer: the codes of the channels and of BM tokens, and the scales behind them.
+__device__ __host__ constexpr int tile_codes(int BM) { return (kTile + BM) * kDepth; }
+constexpr int kBufferBytes = 2 * kTile * (kDepth + kScaleDepth);
+
+// One tile, or half of one; group: of those that do this share.  s_a, s_b: two buffers
+// that the compiler can tell apart: reads of one do not wait for the loads into the other.
 template <int DT, bool GROUPED, Share SHARE>
-__global__ __launch_bounds__(kTileThreads, 1) void mx_tile_kernel(Product p) {
+__device__ __forceinline__ void compute_tile(const Product& p, uint32_t group, int8_t* s_a, int8_t* s_b, int8_t* s_out,
+                                             uint32_t* s_keep) {
   constexpr int TN = kTile / 64, TM = SHARE == kHalves ? TN / 2 : TN;  // 32 x 32 tiles of a wave
   constexpr int BM = 64 * TM;                      // tokens
   constexpr int LN = kTile / 32, LM = BM / 32;     // 16-byte loads of a thread per step
   constexpr int SN = LN / 4, SM = LM / 4;          // its loads of four scales
-  constexpr int kCodes = (kTile + BM) * kDepth;    // of a buffer
-  // two buffers that the compiler can tell apart: reads of one do not wait for
-  // the loads into the other
-  __shared__ __attribute__((aligned(256))) int8_t s_a[kCodes + (kTile + BM) * kScaleDepth];
-  __shared__ __attribute__((aligned(256))) int8_t s_b[kCodes + (kTile + BM) * kScaleDepth];
-  __shared__ __attribute__((aligned(256))) int8_t s_out[4 * 32 * 128];
-  __shared__ uint32_t s_keep[GROUPED ? kTile : 1];  // the tokens' masks
+  constexpr int kCodes = tile_codes(BM);
 
   const uint32_t tiles_n = static_cast<uint32_t>((p.N + kTile - 1) / kTile);
   uint32_t tiles_m = static_cast<uint32_t>((p.M + kTile - 1) / kTile);
@@ -155,11 +157,11 @@ __global__ __launch_bounds__(kTileThreads, 1) void mx_tile_kernel(Product p) {
   uint32_t index, half = 0, tm, tn;
   const uint32_t all = tiles_m * tiles_n, whole = whole_tiles(all, p.cus);
   if constexpr (SHARE == kHalves) {
-    if (in_quarters(all - whole, p.cus) || !tile_of_group(blockIdx.x, 2 * (all - whole), index)) return;
+    if (in_quarters(all - whole, p.cus) || !tile_of_group(group, 2 * (all - whole), index)) return;
     half = index & 1;
     index = whole + index / 2;
   } else {
-    if (!tile_of_group(blockIdx.x, whole, index)) return;
+    if (!tile_of_group(group, whole, index)) return;
   }
   locate_tile(index, tiles_m, tiles_n, tm, tn);
   RowTile t = {static_cast<int64_t>(tm) * kTile, min(p.M, static_cast<int64_t>(tm) * kTile + kTile), 0};
@@ -321,13 +323,37 @@ __global__ __launch_bounds__(kTileThreads, 1) void mx_tile_kernel(Product p) {
       [&](int j) { return GROUPED ? s_keep[GROUPED ? wm + 32 * j + (lane & 31) : 0] : ~0u; });
 }
 
+// The first `halves` workgroups take the halves of a last turn's tiles, the others whole
+// tiles.  Halves first: compute units that start with one are out of step with the others,
+// so that not all write their outputs at the same time (33 MB a turn), and no launch of
+// their own has to wait for the last tile (8192 x 11008 x 4096 bf16: 198 us, with a launch
+// for each 202).
+//
+// Bound by the matrix cores' clock under load and by a turn's start and outputs: a
+// turn of 256 tiles takes 1.5 us for 256 of K (5.6 PF, where the instructions alone reach
+// 6.2 on random codes) and 11.4 us besides, of which 6 are the outputs at a copy's rate.
+// 8192 x 8192 x 8192 takes 244 us (4.5 PF).
+template <int DT, bool GROUPED>
+__global__ __launch_bounds__(kTileThreads, 1) void mx_tile_kernel(Product p, uint32_t halves) {
+  __shared__ __attribute__((aligned(256))) int8_t s_a[kBufferBytes];
+  __shared__ __attribute__((aligned(256))) int8_t s_b[kBufferBytes];
+  __shared__ __attribute__((aligned(256))) int8_t s_out[kOutBytes];
+  __shared__ uint32_t s_keep[GROUPED ? kTile : 1];  // the tokens' masks
+  if (blockIdx.x < halves)
+    compute_tile<DT, GROUPED, kHalves>(p, blockIdx.x, s_a, s_b, s_out, s_keep);
+  else
+    compute_tile<DT, GROUPED, kWhole>(p, blockIdx.x - halves, s_a, s_b, s_out, s_keep);
+}
+
 // ---------------------------------------------------------------------------
 // Small tiles: WM x WN x WK waves, each with TM x TN tiles of 32 x 32; the WK
 // waves of a tile share each step's K, 128 / WK bytes each.  Few steps are long
 // enough to hide anything, so the chain of a step is kept short: STAGES buffers in
 // LDS, each asked for STAGES steps ahead; operands read from LDS a step ahead of
 // the matrix instructions that use them; one barrier, at which a wave waits for
-// the next step's rows only.  LDS is laid out as for the large tiles.
+// the next step's rows only.  LDS is laid out as for the large tiles.  Bound by the loads
+// into a compute unit: a step of 64 x 64 takes 0.15 us for 17 KB (256 x 4096 x 4096: 7.3 us,
+// of which 3.2 are a launch's).
 // ---------------------------------------------------------------------------
 template <int DT, bool GROUPED, int WM, int WN, int WK, int TM, int TN, int STAGES, bool QUARTERS = false>
 __global__ __launch_bounds__(64 * WM* WN* WK) void mx_stream_kernel(Product p) {
@@ -567,32 +593,27 @@ __global__ __launch_bounds__(256) void mx_join_kernel(Product p) {
   }
 }
 
-template <bool GROUPED, Share SHARE>
-void launch_share(const Product& p, int32_t y_dtype, uint32_t groups, hipStream_t st) {
-  with_dtype(y_dtype, [&](auto d) {
-    constexpr int DT = decltype(d)::value;
-    if constexpr (SHARE == kQuarters)
-      hipLaunchKernelGGL((mx_stream_kernel<DT, GROUPED, 2, 2, 1, 2, 2, 4, true>), dim3(groups), dim3(256), 0, st, p);
-    else
-      hipLaunchKernelGGL((mx_tile_kernel<DT, GROUPED, SHARE>), dim3(groups), dim3(kTileThreads), 0, st, p);
-  });
-}
-
 // Tiles of 256 x 256.  A last turn of the compute units that is half full at most is
-// computed in halves of 128 tokens, in a second launch, and one that is a quarter full
+// computed in halves of 128 tokens, by the same launch, and one that is a quarter full
 // at most in quarters, by the kernel for smaller tiles.
 template <bool GROUPED>
 nf4_status launch_tiles(const Product& p, int32_t y_dtype, hipStream_t st) {
   const uint32_t groups = tile_groups<GROUPED>(p, kTile, kTile, kTileThreads);
-  if (groups == 0) return NF4_EUNSUPPORTED;
-  // how many tiles experts' rows make only the GPU knows: the launches find out
+  const uint32_t turn = (p.cus + kDies - 1) / kDies * kDies;
+  if (groups == 0 || (int64_t(groups) + turn) * kTileThreads >= int64_t(1) << 32) return NF4_EUNSUPPORTED;
+  // how many tiles experts' rows make only the GPU knows: the workgroups find out
   const int64_t all = row_tiles<GROUPED>(p, kTile) * ((p.N + kTile - 1) / kTile);
-  const uint32_t whole = whole_tiles(static_cast<uint32_t>(all), p.cus);
-  if (GROUPED || whole > 0) launch_share<GROUPED, kWhole>(p, y_dtype, groups, st);
-  const uint32_t rest = static_cast<uint32_t>(all) - whole, turn = (p.cus + kDies - 1) / kDies * kDies;
-  const bool quarters = in_quarters(rest, p.cus);
-  if (GROUPED || (rest > 0 && !quarters)) launch_share<GROUPED, kHalves>(p, y_dtype, turn, st);
-  if (GROUPED || (rest > 0 && quarters)) launch_share<GROUPED, kQuarters>(p, y_dtype, turn, st);
+  const uint32_t whole = whole_tiles(static_cast<uint32_t>(all), p.cus), rest = static_cast<uint32_t>(all) - whole;
+  const bool quarters = GROUPED || (rest > 0 && in_quarters(rest, p.cus));
+  const uint32_t halves = GROUPED || (rest > 0 && !quarters) ? turn : 0;
+  const uint32_t grid = halves + (GROUPED || whole > 0 ? groups : 0);
+  with_dtype(y_dtype, [&](auto d) {
+    constexpr int DT = decltype(d)::value;
+    if (grid > 0)
+      hipLaunchKernelGGL((mx_tile_kernel<DT, GROUPED>), dim3(grid), dim3(kTileThreads), 0, st, p, halves);
+    if (quarters)
+      hipLaunchKernelGGL((mx_stream_kernel<DT, GROUPED, 2, 2, 1, 2, 2, 4, true>), dim3(turn), dim3(256), 0, st, p);
+  });
   return launch_status();
 }
 
@@ -635,7 +656,7 @@ constexpr int kLargest = 5;
 // A last turn of the largest in halves and in quarters.
 constexpr double kHalfStep = 1.03, kHalfFixed = 4.5, kQuarterStep = 0.41, kQuarterFixed = 2.3;
 constexpr double kLaunchUs = 3.2, kJoinUs = 4.5, kSumUs = 8.0 / 3e6;  // a sum there and back
-// Rows sorted by expert: finding a tile, a stream of weights that counts, three launches.
+// Rows sorted by expert: finding a tile, a stream of weights that counts, two launches.
 constexpr double kFindUs = 1.3, kLonger = 1.45, kLaunchesUs = 3.4;
 constexpr int kMaxSplits = 16;
 
