@@ -93,7 +93,7 @@ def test_mlp(T, k, E, H, F, dtype):
 
 
 @pytest.mark.parametrize("T,k,E,H,F", [(1, 2, 4, 4096, 1500), (7, 2, 3, 1024, 2050), (20, 3, 6, 700, 900), (16, 4, 64, 256, 600),
-                                       (16, 4, 64, 900, 600), (9, 4, 64, 2000, 600)])
+                                       (16, 4, 64, 900, 600), (9, 4, 64, 2000, 600), (4, 2, 8, 2500, 300), (16, 4, 64, 2050, 130)])
 def test_mlp_larger(T, k, E, H, F):
     x, w1, t1, w2, t2, ids, weights = make(2, T, k, E, H, F, True, BF)
     check(amd.mxfp4_moe_mlp(x, t1, t2, ids, weights), x, w1, w2, ids, weights, E, True)

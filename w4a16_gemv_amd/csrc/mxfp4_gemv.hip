@@ -155,10 +155,12 @@ __device__ __forceinline__ Loaded load_unit(const Channels& c, int unit, bool in
           __builtin_amdgcn_raw_buffer_load_b32(c.scales, in ? c.scale_at + 128 * unit : kNever, 0, 0)};
 }
 
-// The lane's block of a unit: 32 codes to lane i + 16 g, as four operands.
+// The lane's block of a unit: 32 codes to lane i + 16 g, as four operands.  EIGHT: of a
+// pair of eight channels, the second unit's as rows 8 to 15.
+template <bool EIGHT = false>
 __device__ __forceinline__ void operands(const Loaded& l, bf16x8 (&a)[4]) {
   const int lane = threadIdx.x & 63, g = lane >> 4;
-  const int from = 4 * (4 * (lane & 15) + g);  // a lane's number times 4
+  const int from = 4 * (EIGHT ? 8 * (lane & 7) + 4 * (lane >> 3 & 1) + g : 4 * (lane & 15) + g);  // a lane's number times 4
   const float s = scale_value(l.scales >> (8 * g) & 255);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -215,6 +217,28 @@ struct Order {
     return from + (u < count ? u : u - count);
   }
 };
+
+// Eight channels for a wave, as Channels: a pair of units at a time, lane 8 i + j 16 bytes j
+// of row i's 128.
+__device__ __forceinline__ Channels eight_channels(const uint8_t* q, const uint8_t* s, int64_t c0, int64_t wide,
+                                                   int64_t pitch, int64_t steps) {
+  const int lane = threadIdx.x & 63;
+  const int64_t n = min(wide, int64_t(8));
+  return Channels{rsrc(q + c0 * pitch, static_cast<uint32_t>(n > 0 ? n * pitch : 0)),
+                  rsrc(s + (c0 >> 5) * steps * 256,
+                       static_cast<uint32_t>(n > 0 ? (((c0 + n + 31) >> 5) - (c0 >> 5)) * steps * 256 : 0)),
+                  static_cast<uint32_t>((lane >> 3) * pitch + (lane & 7) * 16),
+                  scale_from(c0, c0 + (lane & 7), steps, 0)};
+}
+
+// units: of a row; the second of the last pair may lie past it, and is zeros.
+__device__ __forceinline__ Loaded load_pair(const Channels& c, int pair, int units, bool in) {
+  const int lane = threadIdx.x & 63, unit = 2 * pair + (lane >> 3 & 1);
+  const bool codes = in && 2 * pair + (lane >> 2 & 1) < units;
+  return {__builtin_bit_cast(i32x4,
+                             __builtin_amdgcn_raw_buffer_load_b128(c.codes, codes ? c.code_at + 128 * pair : kNever, 0, 0)),
+          __builtin_amdgcn_raw_buffer_load_b32(c.scales, in && unit < units ? c.scale_at + 128 * unit : kNever, 0, 0)};
+}
 
 // Adds to the rows' columns those of their other parts, where these stand beside them.
 template <int PARTS, int CT>
@@ -520,15 +544,15 @@ __global__ __launch_bounds__((64 * wide_waves<XT, RU>()), (wide_waves<XT, RU>() 
 //  up:    a workgroup takes tiles of an expert's 16 channels (of the gate and of the
 //         others) and its tokens, as the kernel above.  act(v) times the router's weight
 //         goes to h as parts.
-//  down:  a workgroup takes 16 channels of y.  Its waves share the experts' F, one expert
+//  down:  a workgroup takes 16 or 8 channels of y.  Its waves share the experts' F, one expert
 //         after the other without a pause in their weights' stream, and add each's sums
 //         to those of the tokens that it has.
 //
 // Bound by the weights' streams: 1 token, 2 of 8 experts of 4096 x 11008, gated: up 24.4 us
 // (95.5 MB, a plain read 15.8), down 16.1 (48 MB, 8.5); 16 tokens, 4 of 64 experts of 2048
-// x 1024: 20.1 and 18.0 (92 and 46 MB).  Down has a workgroup for every 16 channels only,
-// half of the compute units there: sharing K over workgroups and joining in a third launch
-// took 14.5 + 4.6 us (and 64 tokens 95 -> 83), and a join by the last workgroup to arrive 80.
+// x 1024: 20.1 and 15.7 (92 and 46 MB).  With K of the way down shared by workgroups and
+// joined in a third launch that took 14.5 + 4.6 us (64 tokens 83 in all, here 92), with a
+// join by the last workgroup to arrive 80.
 // ---------------------------------------------------------------------------
 constexpr int kMaxTokens = 64, kMaxTopK = 32;
 
@@ -734,45 +758,57 @@ struct Segment {
 };
 
 // WAVES: of a workgroup; RU: loads of a lane for a unit's rows (four rows each); TT: tiles
-// of 16 tokens.
-template <int DT, int WAVES, int RU, int TT>
+// of 16 tokens.  EIGHT: channels of a workgroup, two units of which stand side by side in
+// a product: rows and columns 8 to 15 are the second unit's, and of the sums only those
+// where both sides are of one unit count.
+template <int DT, int WAVES, int RU, int TT, bool EIGHT>
 __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
   constexpr int kParts = h_parts(DT), kRows = 4 * RU;
-  constexpr int kAhead = kParts * RU > 8 ? 1 : 2;  // pairs of units in flight, as registers allow
-  constexpr int kSumBytes = WAVES * TT * 64 * 16, kHBytes = WAVES * wave_lds<DT, RU>();
+  // pairs of units in flight, as registers allow
+  constexpr int kAhead = kParts * RU > 8 ? 1 : EIGHT ? 3 : 2;
+  constexpr int kChannels = EIGHT ? 8 : 16;
+  static_assert(!EIGHT || (RU == 1 && TT == 1 && kParts == 2));
+  constexpr int kSumBytes = WAVES * TT * 64 * 16, kWaveLds = (EIGHT ? 2 : 1) * wave_lds<DT, RU>();
+  constexpr int kHBytes = WAVES * kWaveLds;
   __shared__ __attribute__((aligned(16))) uint8_t s_h[kHBytes > kSumBytes ? kHBytes : kSumBytes];
   __shared__ Routing s_routing;
   __shared__ Segments<kRows> s_segments;
   read_segments(p, s_routing, s_segments);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int units = static_cast<int>(p.pitch2 / 64), pairs = (units + 1) / 2;
-  const int64_t n0 = int64_t(16) * blockIdx.x;
+  const int64_t n0 = int64_t(kChannels) * blockIdx.x;
   auto segment = [&](int j) {
     const int expert = __builtin_amdgcn_readfirstlane(s_segments.expert[j]), first = __builtin_amdgcn_readfirstlane(s_segments.first[j]);
     const int tokens = __builtin_amdgcn_readfirstlane(__builtin_popcountll(mask_of(s_routing, expert)));
     const int64_t place = __builtin_amdgcn_readfirstlane(s_segments.place[j]);
-    return Segment{{channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)},
+    return Segment{{EIGHT ? eight_channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)
+                          : channels(p.w2q, p.w2s, expert * p.H + n0, p.H - n0, p.pitch2, p.steps2)},
                    p.h + place * (kParts * p.h_width), min(tokens - first, kRows)};
   };
   // the wave's pairs of units (whole lines) of all segments'
   const int all = s_segments.count * pairs, each = (all + WAVES - 1) / WAVES;
   int at = min(all, wave * each);
   const int end = min(all, at + each);
-  uint8_t* lds = s_h + wave * wave_lds<DT, RU>();
+  uint8_t* lds = s_h + wave * kWaveLds;
   f32x4 total[TT] = {};
   if (at < end) {
-    Loaded w[kAhead][2];
+    Loaded w[kAhead][EIGHT ? 1 : 2];
     u32x4 x[kAhead][2][RU][kParts];
     int seg = at / pairs, pair = at - seg * pairs;
     int ahead = at, next_seg = seg, next_pair = pair;
     Segment next = segment(seg);
     int count = next.count;
     auto load = [&](int d) {
+      if constexpr (EIGHT) w[d][0] = load_pair(next.ch[0], next_pair, units, ahead < end);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int unit = 2 * next_pair + i;
         const bool in = ahead < end && unit < units;
-        w[d][i] = load_unit(next.ch[0], unit, in);
+        if constexpr (EIGHT) {
+          if (!in) x[d][i][0][0] = x[d][i][0][1] = u32x4{};  // (zeros are multiplied with them)
+        } else {
+          w[d][i] = load_unit(next.ch[0], unit, in);
+        }
 #pragma unroll
         for (int j = 0; j < RU; ++j) {
           if (!in || 4 * j >= next.count) continue;
@@ -792,6 +828,23 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
     for (int d = 0; d < kAhead; ++d) load(d);
     f32x4 acc = {};
     auto take = [&](int d) {
+      if constexpr (EIGHT) {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < kParts; ++k)
+            *reinterpret_cast<u32x4*>(lds + (8 * i + 4 * k + (lane >> 4)) * kLdsRow + (lane & 15) * 16) = x[d][i][0][k];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        bf16x8 a[4];
+        operands<true>(w[d][0], a);
+        const uint8_t* h = lds + (lane & 15) * kLdsRow + 64 * (lane >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[e], *reinterpret_cast<const bf16x8*>(h + 16 * e), acc, 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        return;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (2 * pair + i >= units) break;
@@ -805,7 +858,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         bf16x8 a[4];
-        operands(w[d][i], a);
+        operands(w[d][EIGHT ? 0 : i], a);
         // four rows' parts are columns of one product (what the others hold nobody asks for)
         constexpr int kColumns = RU == 1 ? kParts * kRows : kRows;
         const uint8_t* h = lds + min(lane & 15, kColumns - 1) * kLdsRow + 64 * (lane >> 4);
@@ -831,12 +884,16 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
         const int token = 16 * t + (lane & 15);
         const int column = __builtin_popcountll(mask & ((uint64_t(1) << token) - 1)) - first;
         const bool has = (mask >> token & 1) && column >= 0 && column < kRows;
-        const int from = (has ? column : 0) + (lane & 48);
+        // (of eight channels, those of the lanes from 32 on are the second unit's)
+        const int from = (has ? column : 0) + (lane & (EIGHT ? 16 : 48));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = acc[e];
           float o = __shfl(v, from);
-          if constexpr (RU == 1) {
+          if constexpr (EIGHT) {
+            o += __shfl(v, from + 4);
+            o += __shfl(v, from + 40) + __shfl(v, from + 44);
+          } else if constexpr (RU == 1) {
 #pragma unroll
             for (int k = 1; k < kParts; ++k) o += __shfl(v, from + k * kRows);
           }
@@ -875,7 +932,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES / 4) void mx_down_kernel(Mlp p) {
   const int token = 16 * wave + (lane & 15);
   const int64_t n = n0 + 4 * (lane >> 4);
   const int left = static_cast<int>(min(p.H - n, int64_t(4)));
-  if (wave >= TT || token >= p.T || left <= 0) return;
+  if (wave >= TT || token >= p.T || left <= 0 || (EIGHT && lane >= 32)) return;
   f32x4 sum = s_sum[wave * 64 + lane];
 #pragma unroll
   for (int v = 1; v < WAVES; ++v) sum += s_sum[(v * TT + wave) * 64 + lane];
@@ -1032,7 +1089,11 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
   p.lds = static_cast<int>(held.bytes);
   // few rows to an expert: four at a time
   const bool four = T <= 4 || slots <= 2 * live;
-  const dim3 grid(static_cast<uint32_t>((H + 15) / 16));
+  // eight channels to a workgroup where sixteen would leave half of the compute units without
+  // any, for twice the reads of h: 16 tokens' 4 of 64 experts of 2048 x 1024 15.7 us, with
+  // sixteen 18.0; one token's 2 of 8 of 2048 x 5632 both launches 21.9 and 21.8
+  const bool eight = four && T <= 16 && dtype != INT8_FP32 && (H + 7) / 8 <= device_cus();
+  const dim3 grid(static_cast<uint32_t>(eight ? (H + 7) / 8 : (H + 15) / 16));
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     if (p.experts > 0) {
@@ -1049,14 +1110,20 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
                              st, p);
       });
     }
+    if constexpr (DT != INT8_FP32) {
+      if (eight) {
+        hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, true>), grid, dim3(1024), 0, st, p);
+        return;
+      }
+    }
     if (four && T <= 16)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1>), grid, dim3(1024), 0, st, p);
+      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, false>), grid, dim3(1024), 0, st, p);
     else if (four)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 1, 4>), grid, dim3(512), 0, st, p);
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 1, 4, false>), grid, dim3(512), 0, st, p);
     else if (T <= 16)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1>), grid, dim3(512), 0, st, p);
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1, false>), grid, dim3(512), 0, st, p);
     else
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 4>), grid, dim3(512), 0, st, p);
+      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 4, false>), grid, dim3(512), 0, st, p);
   });
   return launch_status();
 }
