@@ -77,7 +77,7 @@ def make(seed, T, k, E, H, F, gated, dtype, drop=0.0):
 CASES = [(1, 1, 1, 16, 16), (1, 2, 8, 512, 256), (2, 1, 2, 33, 1), (3, 4, 64, 101, 33), (4, 2, 4, 300, 129),
          (5, 2, 3, 1001, 333), (8, 3, 16, 130, 640), (9, 2, 4, 17, 70), (16, 4, 64, 256, 128), (17, 4, 8, 64, 96),
          (33, 2, 5, 100, 60), (64, 8, 128, 48, 40), (64, 2, 1, 40, 300), (40, 6, 200, 20, 20), (1, 32, 1024, 64, 32),
-         (13, 8, 1024, 16, 24)]
+         (13, 8, 1024, 16, 24), (2, 2, 3, 2500, 140)]
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
@@ -93,7 +93,8 @@ def test_mlp(T, k, E, H, F, dtype):
 
 
 @pytest.mark.parametrize("T,k,E,H,F", [(1, 2, 4, 4096, 1500), (7, 2, 3, 1024, 2050), (20, 3, 6, 700, 900), (16, 4, 64, 256, 600),
-                                       (16, 4, 64, 900, 600), (9, 4, 64, 2000, 600), (4, 2, 8, 2500, 300), (16, 4, 64, 2050, 130)])
+                                       (16, 4, 64, 900, 600), (9, 4, 64, 2000, 600),
+                                       (4, 2, 8, 2500, 300), (16, 4, 64, 2050, 130)])
 def test_mlp_larger(T, k, E, H, F):
     x, w1, t1, w2, t2, ids, weights = make(2, T, k, E, H, F, True, BF)
     check(amd.mxfp4_moe_mlp(x, t1, t2, ids, weights), x, w1, w2, ids, weights, E, True)

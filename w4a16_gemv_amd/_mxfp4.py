@@ -179,8 +179,9 @@ def mxfp4_gemm_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | 
 
 def mxfp4_linear_workspace(M: int, N: int, K: int, device=None) -> torch.Tensor | None:
     """A workspace for mxfp4_linear of an M x N x K product on `device` (None
-    when the product would not use one).  Reusable by later calls with no more
-    rows and no larger K on one stream, as mxfp4_gemm_workspace."""
+    when the product would not use one; few rows of few channels do not).  Reusable
+    by later calls with no more rows and no larger K on one stream, as
+    mxfp4_gemm_workspace."""
     return _workspace("mxfp4_linear_workspace_size", M, N, K, device)
 
 
