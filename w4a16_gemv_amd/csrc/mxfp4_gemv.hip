@@ -960,7 +960,9 @@ Held hold(int64_t units, int64_t rows, int64_t tiles) {
   h.split = units >= 32 ? 8 : units >= 16 ? 4 : units >= 8 ? 2 : 1;
   while (h.split < kWaves && units > h.split && tiles * h.split < int64_t(kWaves) * device_cus()) h.split *= 2;
   auto per_wave = [&] { return (units + h.split - 1) / h.split; };
-  if (bytes(units) > kWholeLds) h.split = kWaves;
+  // four or fewer waves take four units each and no others (with_split): where a step of that
+  // has no room, eight waves do
+  if (bytes(units) > kWholeLds || bytes(4 * h.split) > kWholeLds) h.split = kWaves;
   h.units = h.split < 8 || per_wave() > 2 ? 4 : per_wave() > 1 ? 2 : 1;
   while (h.units > 1 && bytes(h.split * h.units) > kWholeLds) h.units /= 2;
   const int64_t step = h.split * h.units, all = units > 0 ? (units + step - 1) / step : 1;
