@@ -1,4 +1,5 @@
-"""What include/mxfp4.h promises beside the values themselves: rows that leave each other alone."""
+"""What include/mxfp4.h promises beside the values themselves: bytes that may hold
+anything, experts that leave each other alone."""
 import pytest
 import torch
 
@@ -8,13 +9,28 @@ from tests.test_gpu_mxfp4_mlp import check, make
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+INF, NAN = float("inf"), float("nan")
 
 
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     amd.load()
+
+
+def padded(t):
+    """t with the scales of the rows past its last, which may hold anything, those of NaN."""
+    scale = t.scale.clone()
+    tiles = scale.view(-(-t.rows // 32), -1, 2, 32, 4)
+    assert t.rows % 32
+    tiles[-1, :, :, t.rows % 32:] = 255
+    return amd.Mxfp4Tensor(t.data, scale, t.K)
+
+
+def bits(a, b):
+    """Equal bit for bit."""
+    as_int = torch.int32 if a.dtype == F32 else torch.int16
+    return torch.equal(a.view(as_int), b.view(as_int))
 
 
 # --- rows whose step of sixteen units has no room in LDS ------------------------
@@ -40,3 +56,56 @@ def test_gemv_nan_stays_in_its_row(M, N, K, dtype):
 def test_mlp_rows_of_257_to_512(T, k, E, H, F, dtype, gated):
     x, w1, t1, w2, t2, ids, weights = make(T + F, T, k, E, H, F, gated, dtype)
     check(amd.mxfp4_moe_mlp(x, t1, t2, ids, weights), x, w1, w2, ids, weights, E, gated)
+
+
+# --- the expert layer's rows between its products -----------------------------
+
+# tokens, slots, experts, H, F: F off the 16 channels of a tile, and no expert's rows a whole tile of scales
+ODD = [(1, 1, 1, 64, 1), (3, 2, 5, 130, 33), (5, 2, 3, 300, 70), (16, 4, 9, 100, 23), (20, 3, 5, 257, 41),
+       (40, 2, 3, 64, 129), (2, 2, 3, 2500, 140), (64, 2, 3, 40, 17)]
+
+
+@pytest.mark.parametrize("gated", (True, False), ids=("gated", "plain"))
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,H,F", ODD)
+def test_mlp_scales_of_rows_past_the_last(T, k, E, H, F, dtype, gated):
+    x, w1, t1, w2, t2, ids, weights = make(T + F, T, k, E, H, F, gated, dtype)
+    clean = amd.mxfp4_moe_mlp(x, t1, t2, ids, weights)
+    assert clean.isfinite().all()
+    for a, b in ((padded(t1), t2), (t1, padded(t2) if t2.rows % 32 else t2)):
+        assert bits(amd.mxfp4_moe_mlp(x, a, b, ids, weights), clean)
+
+
+@pytest.mark.parametrize("gated", (True, False), ids=("gated", "plain"))
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,H,F", [c for c in ODD if c[2] > 1])
+def test_mlp_nan_channel_of_the_next_expert(T, k, E, H, F, dtype, gated):
+    """Its first channel stands behind this one's last in the same tile of scales."""
+    x, w1, t1, w2, t2, ids, weights = make(T + F, T, k, E, H, F, gated, dtype)
+    clean = amd.mxfp4_moe_mlp(x, t1, t2, ids, weights)
+    codes, scales = t1.blocks()
+    sick = E // 2
+    scales[sick * F * (2 if gated else 1)] = 255
+    y = amd.mxfp4_moe_mlp(x, amd.Mxfp4Tensor.from_blocks(codes, scales, H), t2, ids, weights)
+    hit = (ids == sick).any(1)
+    assert bits(y[~hit], clean[~hit]) and y[hit].isnan().all()
+
+
+@pytest.mark.parametrize("gated", (True, False), ids=("gated", "plain"))
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T", (1, 3, 20))
+def test_mlp_infinite_weight_of_the_router(T, dtype, gated):
+    """One channel between the products, positive: y is an infinity with the sign of W2's value.  (The
+    channels past F, zeros, are not multiplied by the router's weight.)"""
+    E, H = 2, 48
+    x = torch.full((T, H), 0.5, dtype=dtype, device=dev())
+    g = torch.Generator(device=dev()).manual_seed(T)
+    one = torch.full((E * (2 if gated else 1), 2, 16), 0x22, dtype=torch.uint8, device=dev())      # ones
+    t1 = amd.Mxfp4Tensor.from_blocks(one, torch.full(one.shape[:2], 127, dtype=torch.uint8, device=dev()), H)
+    code = torch.randint(1, 8, (E * H, 1, 16), generator=g, device=dev(), dtype=torch.uint8)
+    code |= torch.randint(0, 2, code.shape, generator=g, device=dev(), dtype=torch.uint8) << 3
+    t2 = amd.Mxfp4Tensor.from_blocks(code, torch.full((E * H, 1), 127, dtype=torch.uint8, device=dev()), 1)
+    ids = torch.arange(T, device=dev()).view(T, 1) % E
+    y = amd.mxfp4_moe_mlp(x, t1, t2, ids, torch.full((T, 1), INF, device=dev()))
+    want = t2.dequant(out_dtype=F32).view(E, H).sign()[ids[:, 0]] * INF
+    assert same(y, want.to(dtype))
