@@ -93,8 +93,8 @@ nf4_status mxfp4_dequant(const uint8_t* q, const uint8_t* scale, int64_t rows, i
  *                  added by a second kernel).  Nothing is kept between calls;
  *                  calls that may overlap in time need separate workspaces.
  * Each product of two values is exact; they are summed in fp32 in an order that
- * follows from M, N, K and the room in the workspace alone, and the sum is
- * rounded to y_dtype.  Sums below fp32's subnormal numbers are zeros.  K == 0
+ * follows, on a device, from M, N, K and the room in the workspace alone, and the sum
+ * is rounded to y_dtype.  Sums below fp32's subnormal numbers are zeros.  K == 0
  * gives zeros.  Returns NF4_EINVAL for negative sizes, an unknown type, NULL
  * pointers with M * N > 0, codes or scales that are not 16-byte aligned, y not
  * naturally aligned, or a workspace that is not 256-byte aligned;
@@ -134,7 +134,9 @@ size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
  * (bf16), two (fp16) or three (fp32) bf16 numbers that an activation is the sum
  * of: each product is exact (activations below 2^-110 lose what lies under
  * 2^-133; one past fp32's range is an infinity), and they are summed in fp32.  The
- * order of the sums follows from N and K alone.  Also NF4_EINVAL for M outside [0, 16].
+ * order of the sums follows, on a device, from M, N, K and x_dtype alone: a row's result
+ * does not depend on what the other rows hold, but its last bits may on how many they
+ * are.  Also NF4_EINVAL for M outside [0, 16].
  */
 nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const uint8_t* ws,
                       int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* stream);
@@ -193,7 +195,8 @@ nf4_status mxfp4_gemm_grouped(const uint8_t* xq, const uint8_t* xs, int64_t x_ro
  * Activations and weights meet as in mxfp4_gemv.  What lies between the two
  * products is computed in fp32, multiplied by the router's weight and kept as the
  * sum of two bf16 numbers (16 bits; three, so all of fp32, where dtype is fp32).
- * The order of every sum follows from the sizes and the ids alone.  Returns
+ * The order of every sum follows, on a device, from the sizes, the type and the ids
+ * alone.  Returns
  * NF4_EINVAL for negative sizes, another id_bytes, an unknown type, NULL or
  * misaligned pointers or a workspace that is too small; NF4_EUNSUPPORTED outside
  * the ranges above.

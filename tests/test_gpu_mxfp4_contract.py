@@ -58,6 +58,35 @@ def test_mlp_rows_of_257_to_512(T, k, E, H, F, dtype, gated):
     check(amd.mxfp4_moe_mlp(x, t1, t2, ids, weights), x, w1, w2, ids, weights, E, gated)
 
 
+# --- what the order of the sums follows from ------------------------------------
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("N,K", [(100, 400), (300, 4096), (3000, 1000), (40, 20000)])
+def test_gemv_row_does_not_know_the_others(N, K, dtype):
+    """The order follows from the sizes and the type: other rows' values leave a row's bits alone."""
+    _, wt = random_rows(N, N, K, 118, 130)
+    g = torch.Generator(device=dev()).manual_seed(K)
+    for M in (2, 5, 6, 9, 13, 14, 16):
+        x = torch.randn(M, K, generator=g, device=dev()).to(dtype)
+        y = amd.mxfp4_gemv(x, wt, out_dtype=F32)
+        for row in (0, M - 1):
+            other = torch.randn(M, K, generator=g, device=dev()).to(dtype)
+            other[row] = x[row]
+            assert bits(amd.mxfp4_gemv(other, wt, out_dtype=F32)[row], y[row]), (M, row)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,H,F", [(16, 4, 9, 100, 23), (20, 3, 5, 257, 41), (64, 2, 3, 600, 130), (3, 2, 8, 2048, 64)])
+def test_mlp_token_does_not_know_the_others(T, k, E, H, F, dtype):
+    """The same for a layer's tokens, where the ids stay."""
+    x, w1, t1, w2, t2, ids, weights = make(T, T, k, E, H, F, True, dtype)
+    y = amd.mxfp4_moe_mlp(x, t1, t2, ids, weights)
+    for token in (0, T // 2, T - 1):
+        other, scale = x.flip(0).contiguous(), weights.flip(0).contiguous()
+        other[token], scale[token] = x[token], weights[token]
+        assert bits(amd.mxfp4_moe_mlp(other, t1, t2, ids, scale)[token], y[token])
+
+
 # --- the expert layer's rows between its products -----------------------------
 
 # tokens, slots, experts, H, F: F off the 16 channels of a tile, and no expert's rows a whole tile of scales
