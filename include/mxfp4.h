@@ -133,10 +133,12 @@ size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
  * The matrix cores multiply the weights' values, which bf16 holds, with the one
  * (bf16), two (fp16) or three (fp32) bf16 numbers that an activation is the sum
  * of: each product is exact (activations below 2^-110 lose what lies under
- * 2^-133; one past fp32's range is an infinity), and they are summed in fp32.  The
- * order of the sums follows, on a device, from M, N, K and x_dtype alone: a row's result
- * does not depend on what the other rows hold, but its last bits may on how many they
- * are.  Also NF4_EINVAL for M outside [0, 16].
+ * 2^-133; one past fp32's range is an infinity), and they are summed in fp32.  Weights
+ * of 2^128 and more (E of 253 and 254), which bf16 does not hold, are infinities here:
+ * an output that one meets is infinite or NaN.  The order of the sums follows, on a
+ * device, from M, N, K and x_dtype alone: a row's result does not depend on what the
+ * other rows hold, but its last bits may on how many they are.  Also NF4_EINVAL for M
+ * outside [0, 16].
  */
 nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const uint8_t* ws,
                       int64_t M, int64_t N, int64_t K, void* y, int32_t y_dtype, void* stream);
