@@ -1,10 +1,10 @@
 """What include/mxfp4.h promises beside the values themselves: bytes that may hold
-anything, experts that leave each other alone."""
+anything, experts that leave each other alone; and the shares of a launch of large tiles."""
 import pytest
 import torch
 
 import w4a16_gemv_amd as amd
-from tests.test_gpu_mxfp4 import F32, TYPES, dev, exactly, random_rows, same
+from tests.test_gpu_mxfp4 import F32, TYPES, dev, exactly, guarded, plan, random_rows, same, untouched
 from tests.test_gpu_mxfp4_mlp import check, make
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +138,58 @@ def test_mlp_infinite_weight_of_the_router(T, dtype, gated):
     y = amd.mxfp4_moe_mlp(x, t1, t2, ids, torch.full((T, 1), INF, device=dev()))
     want = t2.dequant(out_dtype=F32).view(E, H).sign()[ids[:, 0]] * INF
     assert same(y, want.to(dtype))
+
+
+# --- rows sorted by expert in the largest tiles --------------------------------
+
+# rows of each expert (the rest of the slots, two to a token, are dropped), slots, N, K; whether a turn's
+# tiles are computed whole, and what becomes of the last turn's
+LARGE = [((1400, 1300, 1396), 4096, 5000, 260, (True, "halves")), ((4096,), 4096, 4300, 130, (True, "quarters")),
+         ((2000, 2096), 4096, 6100, 260, (True, "whole")), ((4096,), 4096, 8000, 300, (True, "whole")),
+         ((0, 3000, 0, 1, 1095), 4096, 3800, 200, (True, "quarters")), ((1700, 0, 900), 4000, 6100, 520, (True, "quarters")),
+         ((0, 1300, 500), 4096, 3800, 260, (False, "halves"))]
+
+
+def shares(counts, N, cus):
+    """Whether there are whole tiles of 256 x 256, and how the others are computed."""
+    tiles = sum(-(-c // 256) for c in counts) * -(-N // 256)
+    rest = tiles % cus if 2 * (tiles % cus) <= cus else 0
+    return tiles > rest, "whole" if rest == 0 else "quarters" if 4 * rest <= cus else "halves"
+
+
+@pytest.mark.parametrize("counts,slots,N,K,kind", LARGE)
+def test_grouped_in_the_largest_tiles(counts, slots, N, K, kind):
+    """Every share of a launch, in every type, with rows that have no source and channels that are NaN."""
+    E, T = len(counts), slots // 2
+    assert plan(slots, N, K, E)[0] == 5
+    assert shares(counts, N, torch.cuda.get_device_properties(0).multi_processor_count) == kind
+    ids = torch.full((slots,), -1)
+    ids[:sum(counts)] = torch.repeat_interleave(torch.arange(E), torch.tensor(counts))
+    ids = ids[torch.randperm(slots, generator=torch.Generator().manual_seed(N))].view(T, 2)
+    route = amd.moe_sort(ids.to(dev()), E)
+    x, xt = random_rows(N, T, K, 127, 129)
+    w, wt = random_rows(K, E * N, K, 127, 129)
+    codes, scales = wt.blocks()
+    scales[5::1000], w[5::1000] = 255, NAN
+    wt = amd.Mxfp4Tensor.from_blocks(codes, scales, K)
+    order = route.order.clone()
+    order[3::5], order[4::11] = -1, slots + 9
+    token = (order.long() // 2).clamp(0, T - 1)
+    gone = (order < 0) | (order >= slots)
+    offsets = route.offsets.tolist()
+    for dtype in TYPES:
+        for o, none in ((route.order, None), (order, gone)):
+            whole, y = guarded(slots, N, dtype)
+            amd.mxfp4_gemm_grouped(xt, wt, amd.MoeRoute(route.offsets, o, route.pos), y=y)
+            assert untouched(whole, slots * N) and (y[offsets[E]:] == 7.25).all()
+            for e in range(E):
+                a, b = offsets[e], offsets[e + 1]
+                rows = x[token[a:b]] if none is not None else x[(o[a:b].long() // 2)]
+                we = w[e * N:(e + 1) * N]
+                ok = ~we[:, 0].isnan()
+                want = torch.full((b - a, N), NAN, dtype=dtype, device=dev())
+                if a < b:
+                    want[:, ok] = exactly(rows, we[ok], 0.25, dtype)
+                if none is not None:
+                    want[none[a:b]] = 0.0
+                assert same(y[a:b], want), (dtype, e)
