@@ -65,6 +65,20 @@ nf4_status nf4_probe_int8_plan(int64_t M, int64_t N, int64_t K, int32_t experts,
 nf4_status nf4_probe_mxfp4_plan(int64_t M, int64_t N, int64_t K, int32_t experts, size_t room,
                                 int32_t* plan, int32_t* detail);
 
+/*
+ * nf4_probe_mxfp4_rows -- how mxfp4_moe_mlp takes sizes (T, top_k, experts, H, F and
+ * dtype as there) or, with experts 0, mxfp4_gemv (T rows of H, F channels).
+ *  plan          : host int32[5]; the waves that share a row's K and the units of 128
+ *                  elements that each takes at a time; the elements of a row in LDS at a
+ *                  time (less than H: in turns; 0: mxfp4_gemv's rows that do not fit); the
+ *                  rows at a time; the variant of the way down (-1: mxfp4_gemv; 0 eight
+ *                  channels to a workgroup; four rows of an expert at a time for up to 16
+ *                  tokens (1) and for more (2); sixteen likewise (3, 4)).
+ * Status as for nf4_probe_mxfp4_plan.
+ */
+nf4_status nf4_probe_mxfp4_rows(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F,
+                                int32_t dtype, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,7 @@
 """What include/mxfp4.h promises beside the values themselves: bytes that may hold
-anything, experts that leave each other alone; and the shares of a launch of large tiles."""
+anything, experts that leave each other alone; and the variants of its kernels."""
+import ctypes as C
+
 import pytest
 import torch
 
@@ -56,6 +58,51 @@ def test_gemv_nan_stays_in_its_row(M, N, K, dtype):
 def test_mlp_rows_of_257_to_512(T, k, E, H, F, dtype, gated):
     x, w1, t1, w2, t2, ids, weights = make(T + F, T, k, E, H, F, gated, dtype)
     check(amd.mxfp4_moe_mlp(x, t1, t2, ids, weights), x, w1, w2, ids, weights, E, gated)
+
+
+# --- every way to take rows ------------------------------------------------------
+
+def rows_plan(T, k, E, H, F, dtype):
+    """include/nf4_probe.h's plan of rows (needs no GPU): waves, units, elements in LDS, rows, way down."""
+    a = (C.c_int32 * 5)()
+    assert amd.load().nf4_probe_mxfp4_rows(T, k, E, H, F, TYPES.index(dtype), a) == 0
+    return tuple(a)
+
+
+# rows, channels, K
+GEMV = [(1, 40, 100), (1, 17000, 300), (1, 40, 300), (1, 40, 600), (14, 40, 300), (10, 40, 300), (1, 40, 1200), (1, 40, 2600),
+        (3, 40, 20000), (4, 40, 4200), (3, 40, 4200), (7, 40, 4200), (7, 40, 2600), (5, 40, 2600), (14, 40, 2600),
+        (14, 40, 1200), (10, 40, 1200)]
+# tokens, slots, experts, H, F
+MLP = [(1, 1, 1, 100, 40), (8, 8, 64, 300, 130), (64, 8, 64, 2600, 40), (1, 1, 1, 300, 40), (1, 1, 1, 600, 40),
+       (16, 1, 1, 2600, 40), (1, 1, 1, 1200, 40), (8, 1, 1, 4200, 40), (1, 1, 1, 2600, 40), (3, 1, 1, 4200, 40),
+       (64, 8, 64, 1200, 130), (40, 8, 64, 1200, 130), (16, 1, 1, 1200, 40), (16, 1, 1, 300, 40), (8, 1, 1, 2600, 40),
+       (3, 1, 1, 9000, 40), (8, 8, 64, 2600, 40), (8, 8, 64, 2200, 40), (20, 4, 64, 100, 40), (8, 1, 1, 100, 40),
+       (20, 1, 1, 100, 40), (1, 2, 8, 2048, 50)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("M,N,K", GEMV)
+def test_gemv_variants(M, N, K, dtype):
+    w, wt = random_rows(N, N, K, 127, 129)
+    x = torch.randint(-8, 9, (M, K), device=dev()).to(dtype)
+    for out in TYPES:
+        whole, y = guarded(M, N, out)
+        amd.mxfp4_gemv(x, wt, y=y)
+        assert same(y, exactly(x.double(), w, 0.5, out)) and untouched(whole, M * N)
+
+
+@pytest.mark.parametrize("gated", (True, False), ids=("gated", "plain"))
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("T,k,E,H,F", MLP)
+def test_mlp_variants(T, k, E, H, F, dtype, gated):
+    """All tokens have an expert in common, so that it has as many rows at a time as there may be."""
+    x, w1, t1, w2, t2, ids, weights = make(T + H, T, k, E, H, F, gated, dtype)
+    ids[:, 0] = E // 2
+    whole, y = guarded(T, H, dtype)
+    amd.mxfp4_moe_mlp(x, t1, t2, ids, weights, y=y)
+    check(y, x, w1, w2, ids, weights, E, gated)
+    assert untouched(whole, T * H)
 
 
 # --- what the order of the sums follows from ------------------------------------

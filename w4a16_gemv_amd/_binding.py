@@ -34,7 +34,7 @@ EXPORTED = ("nf4_abi_version", "nf4_status_string", "nf4_dequant", "nf4_gemv", "
             "int8_gemm_grouped",
             "moe_sort", "moe_sort_workspace_size", "moe_gather", "moe_combine",
             "moe_combine_grad",
-            "nf4_probe_mxfp4_plan", "mxfp4_pitch", "mxfp4_scale_size", "mxfp4_quantize",
+            "nf4_probe_mxfp4_plan", "nf4_probe_mxfp4_rows", "mxfp4_pitch", "mxfp4_scale_size", "mxfp4_quantize",
             "mxfp4_dequant", "mxfp4_gemm", "mxfp4_gemm_workspace_size", "mxfp4_linear",
             "mxfp4_linear_workspace_size", "mxfp4_gemv", "mxfp4_gemm_grouped",
             "mxfp4_moe_mlp", "mxfp4_moe_mlp_workspace_size")
@@ -135,6 +135,8 @@ def load() -> C.CDLL:
     lib.moe_combine_grad.argtypes = [p, p, i32, p, p, i64, i32, i64, i64, p, p, p]
     lib.nf4_probe_mxfp4_plan.restype = C.c_int
     lib.nf4_probe_mxfp4_plan.argtypes = [i64, i64, i64, i32, size, p, p]
+    lib.nf4_probe_mxfp4_rows.restype = C.c_int
+    lib.nf4_probe_mxfp4_rows.argtypes = [i64, i32, i32, i64, i64, i32, p]
     lib.mxfp4_pitch.restype = i64
     lib.mxfp4_pitch.argtypes = [i64]
     lib.mxfp4_scale_size.restype = i64

@@ -16,6 +16,7 @@
 #include "mxfp4_format.h"
 #include "mxfp4_product.h"
 #include "nf4_device.h"
+#include "nf4_probe.h"
 #include "product_tiles.h"
 #include "row_io.h"
 
@@ -994,6 +995,9 @@ void with_split(const Held& h, F&& f) {
     run(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
 }
 
+// Whether the rows of mxfp4_gemv lie in LDS whole; else each wave brings its own.
+bool whole_rows(const Held& h, int64_t units) { return h.width / kUnit >= units; }
+
 int64_t h_width(int64_t F) { return (F + kUnit - 1) / kUnit * kUnit; }
 
 bool known_mlp(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F, int32_t dtype) {
@@ -1005,9 +1009,60 @@ size_t h_bytes(int64_t T, int32_t top_k, int64_t F, int32_t dtype) {
   return static_cast<size_t>(T * top_k * h_parts(dtype) * h_width(F) * 2 + 255) / 256 * 256;
 }
 
+// The variants of the way down: eight channels to a workgroup; four rows of an expert at a
+// time, or sixteen, for up to 16 tokens and for more.
+enum Down { kEight, kFourOfFew, kFour, kSixteenOfFew, kSixteen };
+
+struct MlpPlan {
+  Held held;            // of up
+  int64_t live, tiles;  // experts that may have tokens, tiles of 16 channels of each
+  int rows;             // of up, at a time
+  Down down;
+};
+
+MlpPlan plan_mlp(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F, int32_t dtype) {
+  MlpPlan m = {};
+  const int64_t slots = T * top_k;
+  m.live = experts < slots ? experts : slots;
+  m.tiles = h_width(F) / 16;
+  // rows at a time: twice as many as an expert has on average, eight at least
+  const int64_t often = m.live > 0 ? 2 * ((slots + m.live - 1) / m.live) : 0, some = often < 8 ? 8 : often < 16 ? often : 16;
+  m.rows = static_cast<int>(T < some ? T : some);
+  m.held = hold(pitch_of(H) / 64, m.rows * parts_of(dtype), m.tiles * m.live);
+  // few rows to an expert: four at a time
+  const bool four = T <= 4 || slots <= 2 * m.live;
+  // eight channels to a workgroup where sixteen would leave half of the compute units without
+  // any, for twice the reads of h: 16 tokens' 4 of 64 experts of 2048 x 1024 15.7 us, with
+  // sixteen 18.0; one token's 2 of 8 of 2048 x 5632 both launches 21.9 and 21.8
+  const bool eight = four && T <= 16 && dtype != INT8_FP32 && (H + 7) / 8 <= device_cus();
+  m.down = eight ? kEight : four ? (T <= 16 ? kFourOfFew : kFour) : T <= 16 ? kSixteenOfFew : kSixteen;
+  return m;
+}
+
 }  // namespace
 
 extern "C" {
+
+nf4_status nf4_probe_mxfp4_rows(int64_t T, int32_t top_k, int32_t experts, int64_t H, int64_t F, int32_t dtype,
+                                int32_t* plan) {
+  if (!plan || T < 1 || top_k < 1 || experts < 0 || H < 0 || F < 0 || !known_dtype(dtype)) return NF4_EINVAL;
+  Held h = {};
+  if (experts == 0) {
+    if (T > 16) return NF4_EINVAL;
+    if (F > kMaxDim || H > kMaxK) return NF4_EUNSUPPORTED;
+    h = hold(pitch_of(H) / 64, T * parts_of(dtype), (F + 15) / 16);
+    plan[2] = whole_rows(h, pitch_of(H) / 64) ? h.width : 0;
+    plan[3] = static_cast<int32_t>(T);
+    plan[4] = -1;
+  } else {
+    if (!known_mlp(T, top_k, experts, H, F, dtype)) return NF4_EUNSUPPORTED;
+    const MlpPlan m = plan_mlp(T, top_k, experts, H, F, dtype);
+    h = m.held;
+    plan[2] = h.width, plan[3] = m.rows, plan[4] = m.down;
+  }
+  plan[0] = h.split, plan[1] = h.units;
+  return NF4_OK;
+}
 
 nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const uint8_t* ws, int64_t M,
                       int64_t N, int64_t K, void* y, int32_t y_dtype, void* stream) {
@@ -1021,7 +1076,7 @@ nf4_status mxfp4_gemv(const void* x, int32_t x_dtype, const uint8_t* wq, const u
   Gemv p = {x, wq, ws, y, M, N, K, pitch_of(K), steps_of(K), 0};
   const Held held = hold(units, M * parts_of(x_dtype), tiles);
   p.width = held.width;
-  if (held.width / kUnit < units) {  // not whole rows
+  if (!whole_rows(held, units)) {
     const dim3 wide(static_cast<uint32_t>(tiles < device_cus() ? tiles : device_cus()));
     with_dtype(x_dtype, [&](auto a) {
       with_dtype(y_dtype, [&](auto d) {
@@ -1085,26 +1140,16 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
   p.pitch1 = pitch_of(H), p.steps1 = steps_of(H), p.pitch2 = pitch_of(F), p.steps2 = steps_of(F);
   p.T = static_cast<int>(T), p.top_k = top_k, p.experts = F > 0 ? experts : 0, p.id_bytes = id_bytes, p.gated = gated;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  const int64_t slots = T * top_k, live = experts < slots ? experts : slots;
-  // rows at a time: twice as many as an expert has on average, eight at least
-  const int64_t often = live > 0 ? 2 * ((slots + live - 1) / live) : 0, some = often < 8 ? 8 : often < 16 ? often : 16;
-  p.rows = static_cast<int>(T < some ? T : some);
-  const int64_t tiles = p.h_width / 16;
-  const Held held = hold(p.pitch1 / 64, p.rows * parts_of(dtype), tiles * live);
-  p.lds = static_cast<int>(held.bytes);
-  // few rows to an expert: four at a time
-  const bool four = T <= 4 || slots <= 2 * live;
-  // eight channels to a workgroup where sixteen would leave half of the compute units without
-  // any, for twice the reads of h: 16 tokens' 4 of 64 experts of 2048 x 1024 15.7 us, with
-  // sixteen 18.0; one token's 2 of 8 of 2048 x 5632 both launches 21.9 and 21.8
-  const bool eight = four && T <= 16 && dtype != INT8_FP32 && (H + 7) / 8 <= device_cus();
-  const dim3 grid(static_cast<uint32_t>(eight ? (H + 7) / 8 : (H + 15) / 16));
+  const MlpPlan m = plan_mlp(T, top_k, experts, H, F, dtype);
+  const Held& held = m.held;
+  p.rows = m.rows, p.lds = static_cast<int>(held.bytes);
+  const dim3 grid(static_cast<uint32_t>(m.down == kEight ? (H + 7) / 8 : (H + 15) / 16));
   with_dtype(dtype, [&](auto d) {
     constexpr int DT = decltype(d)::value;
     if (p.experts > 0) {
-      const int64_t share = ((held.two ? 2 : 1) * device_cus() + live - 1) / live;
-      const int64_t groups = (tiles + kWaves / held.split - 1) / (kWaves / held.split);
-      const dim3 up(static_cast<uint32_t>(groups < share ? groups : share), static_cast<uint32_t>(live));
+      const int64_t share = ((held.two ? 2 : 1) * device_cus() + m.live - 1) / m.live;
+      const int64_t groups = (m.tiles + kWaves / held.split - 1) / (kWaves / held.split);
+      const dim3 up(static_cast<uint32_t>(groups < share ? groups : share), static_cast<uint32_t>(m.live));
       with_split(held, [&](auto split, auto u) {
         constexpr int SPLIT = decltype(split)::value, UNITS = decltype(u)::value;
         if (gated)
@@ -1115,20 +1160,15 @@ nf4_status mxfp4_moe_mlp(const void* x, int32_t dtype, const uint8_t* w1q, const
                              st, p);
       });
     }
-    if constexpr (DT != INT8_FP32) {
-      if (eight) {
-        hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, true>), grid, dim3(1024), 0, st, p);
-        return;
-      }
+    switch (m.down) {
+      case kEight:
+        if constexpr (DT != INT8_FP32) hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, true>), grid, dim3(1024), 0, st, p);
+        break;
+      case kFourOfFew: hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, false>), grid, dim3(1024), 0, st, p); break;
+      case kFour: hipLaunchKernelGGL((mx_down_kernel<DT, 8, 1, 4, false>), grid, dim3(512), 0, st, p); break;
+      case kSixteenOfFew: hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1, false>), grid, dim3(512), 0, st, p); break;
+      case kSixteen: hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 4, false>), grid, dim3(512), 0, st, p); break;
     }
-    if (four && T <= 16)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 16, 1, 1, false>), grid, dim3(1024), 0, st, p);
-    else if (four)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 1, 4, false>), grid, dim3(512), 0, st, p);
-    else if (T <= 16)
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 1, false>), grid, dim3(512), 0, st, p);
-    else
-      hipLaunchKernelGGL((mx_down_kernel<DT, 8, 4, 4, false>), grid, dim3(512), 0, st, p);
   });
   return launch_status();
 }
