@@ -240,3 +240,29 @@ def test_grouped_in_the_largest_tiles(counts, slots, N, K, kind):
                 if none is not None:
                     want[none[a:b]] = 0.0
                 assert same(y[a:b], want), (dtype, e)
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(8, 2, 4, 50, 300), (16, 4, 64, 900, 512), (208, 3, 5, 163, 190), (586, 4, 2, 3044, 260),
+                                       (2048, 2, 3, 4400, 130)])
+def test_grouped_offsets_are_clamped(T, k, E, N, K):
+    """An end below zero and one past the rows: the first expert has none, the second's begin with row 0,
+    and the last one's go on to the last row: behind the sorted ones, which have no slot and give zeros."""
+    x, xt = random_rows(1, T, K, 127, 129)
+    w, wt = random_rows(2, E * N, K, 127, 129)
+    ids = torch.arange(T * k).view(T, k) % E
+    ids[::7, 0] = -1
+    route = amd.moe_sort(ids.to(dev()), E)
+    wild = route.offsets.clone()
+    wild[1], wild[-1] = -5, 1 << 30
+    offsets = wild.clamp(0, T * k).tolist()
+    for dtype in TYPES:
+        whole, y = guarded(T * k, N, dtype)
+        amd.mxfp4_gemm_grouped(xt, wt, amd.MoeRoute(wild, route.order, route.pos), y=y)
+        assert untouched(whole, T * k * N)
+        for e in range(1, E):
+            a, b = offsets[e], offsets[e + 1]
+            if a < b:
+                order = route.order[a:b].long()
+                want = exactly(x[order.clamp(0) // k], w[e * N:(e + 1) * N], 0.25, dtype)
+                want[order < 0] = 0.0
+                assert same(y[a:b], want), (dtype, e)
