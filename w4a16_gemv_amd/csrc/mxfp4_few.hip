@@ -20,7 +20,6 @@ using namespace tiledev;
 using namespace mxdev;
 
 constexpr int kRowThreads = 64 * kRowWaves;
-constexpr int kRowLds = 128 << 10;  // of the tokens' codes and scales, most
 
 // Bytes in LDS from one token's codes to the next, and dwords from its scales to the
 // next's: such that a chunk of 16 rows lies in different banks.
@@ -255,9 +254,7 @@ Rows row_plan(const Product& p, int64_t rows) {
   return r;
 }
 
-bool fits_rows(const Product& p, int64_t rows) {
-  return p.pitch > 0 && p.pitch <= 22 * 64 * kRowWaves && lds_bytes(p.pitch, rows) <= kRowLds;
-}
+bool fits_rows(const Product& p) { return p.pitch > 0 && p.pitch <= 22 * 64 * kRowWaves; }
 
 nf4_status launch_rows(const Product& p, bool grouped, const void* x, int32_t xt, int64_t K, int32_t y_dtype,
                        hipStream_t st) {

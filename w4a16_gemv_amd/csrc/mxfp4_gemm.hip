@@ -743,7 +743,7 @@ constexpr int64_t kShortPitch = 2048, kShortestPitch = 512;
 
 template <bool GROUPED>
 bool few(const Product& p) {
-  if (!fits_rows(p, p.M < 16 ? p.M : 16) || row_tiles<GROUPED>(p, 16) > 65535) return false;
+  if (!fits_rows(p)) return false;
   const int64_t cus = device_cus();
   if (GROUPED) {
     const int64_t most = p.M < p.experts ? p.M : p.experts;
@@ -759,7 +759,7 @@ bool few(const Product& p) {
 // 8.1, 16 rows 9.7 and 8.3; 4 x 11008 x 4096 8.8 and 9.5, 8 rows 11.0 and 9.5; 2 x 4096 x
 // 11008 10.1 and 10.9, 4 rows 12.3 and 10.9; 1 x 44032 x 4096 18.5 and 21.5.
 bool encodes_rows(const Product& p) {
-  if (!fits_rows(p, p.M < 16 ? p.M : 16) || row_tiles<false>(p, 16) > 65535) return false;
+  if (!fits_rows(p)) return false;
   const int64_t elements = (p.M < 16 ? p.M : 16) * 2 * p.pitch;
   const bool one = row_tiles<false>(p, 16) * ((p.N + 15) / 16) <= device_cus();
   return elements <= (one ? 32768 : 16384) && (p.M <= 16 || one);

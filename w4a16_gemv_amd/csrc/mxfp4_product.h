@@ -70,8 +70,10 @@ struct Rows {
 // rows: tiles of 16 rows.
 Rows row_plan(const Product& p, int64_t rows);
 
-// Whether `rows` rows (16 at most) of the activations' codes have room beside the kernel.
-bool fits_rows(const Product& p, int64_t rows);
+// Whether the few-row kernel takes rows of this length, 22 units to a wave at most.  (LDS for
+// 16 rows of codes and the grid's second dimension set no limit: who chooses the kernel asks
+// for 35 KB and 2048 tiles of rows at most.)
+bool fits_rows(const Product& p);
 
 // The few-row kernel on tokens of type xt at x, or on the product's codes (kCodes).
 nf4_status launch_rows(const Product& p, bool grouped, const void* x, int32_t xt, int64_t K, int32_t y_dtype,
