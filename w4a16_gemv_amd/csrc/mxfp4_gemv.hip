@@ -727,11 +727,7 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
             for (int i = 0; i < 2; ++i) {
               const float gate = sum[0][e + i], other = sum[CT - 1][e + i];
               const float a = gate / (1.0f + expf(-gate));
-              // Past F the codes are zeros, but their scales are those of the rows behind, the
-              // other half's, the next expert's or none's, and may be NaN; and the router's weight
-              // may not be finite.  So these are chosen, not computed.
-              const bool in = 16 * t + 4 * (lane >> 4) + e + i < p.F;
-              split(in ? (GATED ? a * other : a) * weight : 0.0f, part[i]);
+              split((GATED ? a * other : a) * weight, part[i]);
               // the last of the parts that are kept is rounded
               if constexpr (kParts == 2) part[i][1] = part[i][1] + part[i][2];
             }
@@ -739,6 +735,18 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
             for (int k = 0; k < kParts; ++k)
               out[k][e / 2] =
                   k + 1 < kParts ? upper_halves(part[0][k], part[1][k]) : pack_pair<NF4_BF16>(part[0][k], part[1][k]);
+          }
+          // Past F the codes are zeros, but their scales are those of the rows behind, the other
+          // half's, the next expert's or none's, and may be NaN; and the router's weight may not
+          // be finite.  So these zeros are set.  (By choosing every value, in every tile, up
+          // took 0.2-0.8 us longer.)
+          if (p.F - 16 * t < 16) {
+            const int left = static_cast<int>(p.F - 16 * t) - 4 * (lane >> 4);
+#pragma unroll
+            for (int k = 0; k < kParts; ++k) {
+              out[k][0] &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
+              out[k][1] &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
+            }
           }
           uint16_t* to = p.h + (pairs + t0 + (lane & 15)) * (kParts * p.h_width) + 16 * t + 4 * (lane >> 4);
 #pragma unroll
