@@ -413,7 +413,8 @@ constexpr int kLdsRow = 2 * kUnit + 16;
 // itself, through registers and a piece of LDS of its own: no wave waits for another's rows
 // (in LDS a stretch at a time, between barriers, 16 x 11008 x 4096 bf16 took 17.2 us and 7
 // x 4096 x 11008 fp16 16.6; here 14.4 and 13.7, of which half is splitting the rows again in
-// every workgroup).  Rows that do fit are split once for all of a workgroup's tiles: 8
+// every workgroup; to split them once takes a launch of its own and a workspace, which the
+// call has not).  Rows that do fit are split once for all of a workgroup's tiles: 8
 // x 11008 x 4096 bf16 9.1 us and here 12.2.  RU: loads of a lane for a unit's rows (four
 // rows each).
 template <int XT, int RU>
@@ -573,7 +574,11 @@ struct Mlp {
   int rows, lds;  // of up: rows at a time (16 at most), bytes for them
 };
 
-// What h is kept in: 16 bits of each number, or all of fp32.
+// What h is kept in: 16 bits of each number, or all of fp32.  16 bits are off by 2^-17 of a
+// number at most, where the output's own rounding is off by 2^-9 (bf16) or 2^-12 (fp16): one
+// token's 2 of 8 experts of 4096 x 11008 in bf16 differ by 1.6e-4 of their norm from fp32 all the
+// way, flips of last bits, and both are 1.7e-3 from the exact outputs.  Two parts of four rows
+// stand side by side in eight columns; three would not.
 __device__ __host__ constexpr int h_parts(int dt) { return dt == INT8_FP32 ? 3 : 2; }
 
 struct Routing {
@@ -736,22 +741,23 @@ __global__ __launch_bounds__(kThreads, 4) void mx_up_kernel(Mlp p) {
               out[k][e / 2] =
                   k + 1 < kParts ? upper_halves(part[0][k], part[1][k]) : pack_pair<NF4_BF16>(part[0][k], part[1][k]);
           }
-          // Past F the codes are zeros, but their scales are those of the rows behind, the other
-          // half's, the next expert's or none's, and may be NaN; and the router's weight may not
-          // be finite.  So these zeros are set.  (By choosing every value, in every tile, up
-          // took 0.2-0.8 us longer.)
-          if (p.F - 16 * t < 16) {
-            const int left = static_cast<int>(p.F - 16 * t) - 4 * (lane >> 4);
-#pragma unroll
-            for (int k = 0; k < kParts; ++k) {
-              out[k][0] &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
-              out[k][1] &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
-            }
-          }
           uint16_t* to = p.h + (pairs + t0 + (lane & 15)) * (kParts * p.h_width) + 16 * t + 4 * (lane >> 4);
 #pragma unroll
           for (int k = 0; k < kParts; ++k)
             *reinterpret_cast<uint2*>(to + k * p.h_width) = make_uint2(out[k][0], out[k][1]);
+          // Past F the codes are zeros, but their scales are those of the rows behind, the other
+          // half's, the next expert's or none's, and may be NaN; and the router's weight may not
+          // be finite.  So zeros are written over what came of it.  (By choosing every value,
+          // in every tile, up took 0.2-0.8 us longer; to set the zeros before the store takes
+          // registers that fp32 with a gate does not have.)
+          if (p.F - 16 * t < 16) {
+            const int left = static_cast<int>(p.F - 16 * t) - 4 * (lane >> 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e >= left)
+#pragma unroll
+                for (int k = 0; k < kParts; ++k) to[k * p.h_width + e] = 0;
+          }
         });
   }
 }
