@@ -175,7 +175,8 @@ nf4_status mxfp4_gemm_grouped(const uint8_t* xq, const uint8_t* xs, int64_t x_ro
 
 /*
  * mxfp4_moe_mlp -- the expert layer of a few tokens in two launches, from the
- * router's choice:
+ * router's choice (made for up to about 16 tokens; with more, mxfp4_gemm_grouped, which
+ * takes quantized activations, reads an expert's weights less often):
  *
  *     y[t] = sum_j weights[t][j] * W2[e] act(W1[e] x[t]),   e = ids[t][j]
  *

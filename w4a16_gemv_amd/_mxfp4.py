@@ -294,7 +294,8 @@ def mxfp4_moe_mlp(x: torch.Tensor, w1: Mxfp4Tensor, w2: Mxfp4Tensor, ids: torch.
     [T][top_k] with top_k <= 32; ids outside [0, E) are dropped slots.  weights: fp32
     [T][top_k], or None for ones.  Returns y [T][H] in x's type.  workspace: a uint8
     tensor of mxfp4_moe_mlp_workspace_size bytes, or None for one from torch's
-    allocator."""
+    allocator.  Past about 16 tokens mxfp4_gemm_grouped of quantized activations takes
+    less time."""
     if x.dim() != 2:
         raise ValueError(f"x must be [T, H], got shape {tuple(x.shape)}")
     T, H = x.shape

@@ -48,7 +48,8 @@ __device__ __forceinline__ i32x8 four(const i32x4& a) {
 
 // Keeps sums where they are computed, by all lanes.  Where only some lanes use them the
 // compiler may move a matrix instruction to these lanes alone, though it reads the operands
-// of all.
+// of all.  (No instruction is written here, so there is nothing that would have to wait for
+// the sums; the compiler's own next one does.)
 template <class V>
 __device__ __forceinline__ void settled(V& v) {
   asm volatile("" : "+v"(v));
