@@ -2,8 +2,8 @@
 // 16 rows (mxfp4_gemv), and the expert layer of a few tokens (mxfp4_moe_mlp).
 //
 // v_mfma_f32_16x16x32_bf16 with the weights as A: lane i + 16 g holds A[i][8 g .. + 7],
-// B likewise with i the column, and D[4 g .. + 3][i].  Every value of the format is a
-// bf16 number, so the weights are converted on the way (two codes and their scale an
+// B likewise with i the column, and D[4 g .. + 3][i].  Every value of the format below
+// 2^128 is a bf16 number, so the weights are converted on the way (two codes and their scale an
 // instruction) and a lane's block of 32 codes is four matrix instructions' operands; which
 // codes of a row a lane has is free as long as both sides agree.  Activations are split
 // into bf16 numbers whose sum they are (parts): one for bf16, two for fp16 (8 + 3 bits),
